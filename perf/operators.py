@@ -159,6 +159,9 @@ def prepare(case, seed):
                  v=kv[..., NOPE:], k_rope=rows[:, LATENT:], cu_q=cu_q, cu_k=cu_k, spans=list(zip(cu_q.tolist(), cu_k.tolist())),
                  scale=(NOPE + ROPE) ** -0.5, out=torch.empty(Tq, H, VDIM, dtype=torch.bfloat16, device=DEV),
                  lse=torch.empty(Tq, H, device=DEV))
+        if own:
+            import kimi_delta_attention_varlen_gb300 as kda
+            s["workspace"] = torch.empty(kda.kda_latent_prefill_workspace_size(Tq, B, H), dtype=torch.uint8, device=DEV)
     elif case["op"] == "turnover":
         R, F, P, N = case["requests"], case["forks"], case["page"], case["pages"]
         lens = _lengths(R, case["lo"], case["hi"], g)
@@ -341,8 +344,8 @@ def run(s):
                                   scale=s["scale"], lse=s["lse"])
             return {"out": s["out"], "lse": s["lse"]}
         if op == "prefill":
-            kda.kda_latent_prefill(s["q"], s["k_nope"], s["k_rope"], s["v"], s["cu_q"], s["cu_k"], s["out"], scale=s["scale"],
-                                   lse=s["lse"])
+            kda.kda_latent_prefill(s["q"], s["k_nope"], s["k_rope"], s["v"], s["cu_q"], s["cu_k"], s["out"], s["workspace"],
+                                   scale=s["scale"], lse=s["lse"])
             return {"out": s["out"], "lse": s["lse"]}
         s["work"].copy_(s["first"])
         pt = kda.page_table_descriptor(s["table"], s["lens"], s["ref"], s["page"])
