@@ -505,6 +505,199 @@ int kda_decode_step(const void *q, const void *k, const void *v, int32_t io_dtyp
                     float scale, int32_t qk_l2norm, const kda_cache *cache, const void *idx,
                     int32_t idx_type, void *out, void *stream);
 
+/* ========================================================================
+ * Latent attention: the attention layers that a hybrid model alternates with
+ * its recurrent layers.  A token's keys and values all come from one shared
+ * latent vector c (dl values) and one shared rope key r (dr values); the row
+ * [c | r] is what the cache keeps.  With the up-projections W_k and W_v of a
+ * head, its key is [W_k c | r] and its value W_v c.  Two forms:
+ *   absorbed (decode)    W_k^T goes into the query and W_v behind the output,
+ *                        so every head attends to the latents themselves;
+ *   expanded (prefill)   keys and values are formed per head first.
+ *
+ * Latent pages.  A kda_cache [n_pages, 1, page_size, dl + dr] (h = 1,
+ * v = page_size, k = dl + dr): page p holds page_size consecutive tokens of
+ * one request.  A block table row lists a request's pages in order.
+ * ======================================================================== */
+
+/* Who holds which pages (all device memory of the caller's):
+ *   block_table [requests, width], rows table_stride >= width int32 apart:
+ *               entry j < ceil(seq_lens / page_size) is the page of the
+ *               request's tokens j * page_size ...; other entries are -1
+ *   seq_lens    [requests] int32, tokens of each request
+ *   refcount    [n_pages] int32, how many block table rows hold the page;
+ *               0: the page is free
+ * width * page_size < 2^31 and n_pages < 2^31 (KDA_ERR_RANGE). */
+typedef struct {
+    int32_t *block_table;
+    int32_t *seq_lens;
+    int32_t *refcount;
+    int64_t requests;
+    int64_t width;
+    int64_t table_stride; /* in elements */
+    int64_t n_pages;
+    int32_t page_size;
+    int32_t reserved; /* must be 0 */
+} kda_page_table;
+
+/* ------------------------------------------------------------------------
+ * kda_latent_decode
+ *
+ * For request r, query token t (of L), head h, with n = seq_lens[row] the
+ * tokens in the cache (the L query tokens' own rows are the last L of them)
+ * and row = req[r] (r when req == NULL):
+ *   z_j   = scale * q[r,t,h] . x_j         for j < n - (L - 1 - t)
+ *   out   = sum_j softmax(z)_j x_j[0:dl],  lse = log sum_j e^{z_j}
+ * where x_j = [c_j | r_j] is token j's cache row.  L = 1 is the ordinary
+ * single-token step; L > 1 the causal verification of draft tokens.  Where
+ * no token is seen (an empty request, row outside [0, requests), a query
+ * token before the cache's first), out = 0 and lse = -inf.
+ *
+ *   q           [batch, L, h, dl + dr] device bf16 (absorbed queries)
+ *   cache       latent pages, bf16, 16-byte aligned pages
+ *   block_table [requests, width] device int32, rows table_stride apart
+ *   seq_lens    [requests] device int32; a length above width * page_size is
+ *               taken as that, a negative one as 0
+ *   req         [batch] device int32 / int64 (idx_type), or NULL
+ *   out         [batch, L, h, dl] device bf16
+ *   lse         [batch, L, h] device fp32, or NULL
+ *   workspace   kda_latent_decode_workspace_size(...) bytes, 256-byte aligned;
+ *               contents on entry do not matter.  Calls on one workspace must
+ *               not overlap.  Its status word: kda_prefill_workspace_status.
+ * A page number outside [0, n_pages) reads as zero rows, like an invalid
+ * index of kda_state_gather.  Cache rows beyond a request's length are never
+ * used, whatever they hold (NaN and infinities included).  Scores, softmax
+ * statistics and sums are fp32; the probabilities enter the second product
+ * in bf16 (the tensor cores' operand type).
+ * Built: dl in {256, 512}, dr == 64, page_size a multiple of 8, bf16.
+ * Errors: KDA_ERR_NULL, _DTYPE (io or cache not bf16), _LAYOUT, _SHAPE (sizes
+ * below 1 (batch below 0), cache h / k not 1 / dl + dr, table_stride < width),
+ * _UNSUPPORTED (dl, dr, page_size), _RANGE (batch * L * h >= 2^31,
+ * width * page_size >= 2^31, L * h > 2^20), _ALIGN, _WORKSPACE, _CUDA.
+ * batch == 0 launches nothing.
+ * ---------------------------------------------------------------------- */
+size_t kda_latent_decode_workspace_size(int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr);
+int kda_latent_decode(const void *q, int32_t io_dtype, int64_t batch, int32_t L, int32_t h,
+                      int32_t dl, int32_t dr, float scale, const kda_cache *cache,
+                      const int32_t *block_table, int64_t requests, int64_t width,
+                      int64_t table_stride, const int32_t *seq_lens, const void *req,
+                      int32_t idx_type, void *out, float *lse, void *workspace, size_t ws_bytes,
+                      void *stream);
+
+/* ------------------------------------------------------------------------
+ * kda_latent_prefill
+ *
+ * Causal attention over a varlen batch in the expanded form.  Sequence b has
+ * the queries cu_q[b] .. cu_q[b+1]-1 (n_q of them) and the keys cu_k[b] ..
+ * cu_k[b+1]-1 (n_k); its queries are the last n_q of its n_k tokens, so query
+ * i sees the keys j <= i + n_k - n_q.  Per head,
+ *   z_ij = scale * (q_i[0:dn] . k_nope_j + q_i[dn:dn+dr] . k_rope_j)
+ *   out_i = sum_j softmax(z_i)_j v_j,   lse_i = log sum_j e^{z_ij}
+ * with k_rope shared by all heads.  A query that sees no key (n_k < n_q)
+ * gets out = 0 and lse = -inf.
+ *
+ *   q        [total_q, h, dn + dr] device bf16, contiguous
+ *   k_nope   device bf16; head h of token j starts at j * kn_token + h *
+ *            kn_head elements (so a slice of a joint projection can be given)
+ *   k_rope   device bf16; token j starts at j * kr_token elements (so the tail
+ *            of the latent rows can be given)
+ *   v        device bf16, strides v_token, v_head
+ *            All strides multiples of 8 elements, every base 16-byte aligned.
+ *   cu_q, cu_k [num_seqs + 1] device int32, from 0, non-decreasing, ending at
+ *            total_q / total_k (precondition; no key at or beyond total_k and
+ *            no query at or beyond total_q is touched whatever they hold)
+ *   out      [total_q, h, dv] device bf16, lse [total_q, h] fp32 or NULL
+ *   workspace kda_latent_prefill_workspace_size(...) bytes, as above
+ * Built: dn == dv == 128, dr == 64, bf16.  Errors as kda_latent_decode
+ * (_RANGE: total_q or total_k >= 2^31 - 256, num_seqs >= 2^24, h > 1024, a
+ * token stride of 2^38 elements or more).
+ * total_q == 0 launches nothing.
+ * ---------------------------------------------------------------------- */
+size_t kda_latent_prefill_workspace_size(int64_t total_q, int64_t num_seqs, int32_t h);
+int kda_latent_prefill(const void *q, int32_t io_dtype, const void *k_nope, int64_t kn_token,
+                       int64_t kn_head, const void *k_rope, int64_t kr_token, const void *v,
+                       int64_t v_token, int64_t v_head, const int32_t *cu_q, const int32_t *cu_k,
+                       int64_t num_seqs, int64_t total_q, int64_t total_k, int32_t h, int32_t dn,
+                       int32_t dr, int32_t dv, float scale, void *out, float *lse, void *workspace,
+                       size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * kda_latent_append
+ *
+ * Writes new tokens' rows into latent pages.  Tokens cu[i] .. cu[i+1]-1 of x
+ * are the last cu[i+1] - cu[i] tokens of request req[i]: token cu[i] + e goes
+ * to position seq_lens[req[i]] - (cu[i+1] - cu[i]) + e of that request (call
+ * kda_pages_reserve first: it makes room and advances seq_lens).  Tokens of
+ * an invalid request, at a negative position or without a valid page are
+ * skipped.
+ *   x      [total, k] device, the cache's dtype, rows x_stride elements apart
+ *   cu     [count + 1] device int32, non-decreasing, cu[0] >= 0
+ *   req    [count] device int32 / int64, valid entries unique
+ *   cache  h == 1, v == table->page_size, n_rows >= table->n_pages
+ * ---------------------------------------------------------------------- */
+int kda_latent_append(const void *x, int64_t x_stride, int64_t total, const int32_t *cu,
+                      const void *req, int32_t idx_type, int64_t count, const kda_page_table *table,
+                      const kda_cache *cache, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Page upkeep.  The calls below change the tables (block_table, seq_lens,
+ * refcount) of a kda_page_table and name the page copies that go with the
+ * change as pairs (move_src, move_dst); kda_pages_copy then carries them out
+ * on each layer's cache.  Every result is a function of the tables alone:
+ * new pages are the lowest free numbers, in the order of the list.
+ * Index lists are device int32 / int64 (idx_type); entries outside
+ * [0, requests) are skipped; valid entries of one list are unique unless said
+ * otherwise.  count == 0 launches nothing.
+ *
+ * kda_pages_fork     request dst[i] becomes a copy of request src[i]: same
+ *                    pages (one more reference each), same length.  A source
+ *                    may appear several times; a destination holds no pages
+ *                    before and is no source of the same call.  dst[i] ==
+ *                    src[i] is skipped.
+ * kda_pages_release  request req[i] keeps its first keep[i] tokens (device
+ *                    int32; negative: 0, more than it has: all; keep == NULL:
+ *                    0) and gives back the pages behind them.
+ * kda_pages_reserve  request req[i] grows by new_tokens[i] (device int32;
+ *                    <= 0: skipped): new pages enter its row, seq_lens
+ *                    advances.  When its last page is unfinished and shared
+ *                    (refcount > 1 before the call), the request gets a new
+ *                    page in its place (copy on write): (move_src[i],
+ *                    move_dst[i]) = (old, new), else (-1, -1).  All or
+ *                    nothing: with too few free pages, or a row too short,
+ *                    nothing changes and every move is -1.
+ *                    info (device int32[4]): 0 done / 1 too few free pages /
+ *                    2 a row too short; moves; pages asked for; pages free
+ *                    before the call.
+ * kda_pages_compact  moves the live pages to the numbers 0 .. live-1: the
+ *                    k-th live page at or above `live` goes to the k-th free
+ *                    page below it; the tables follow.  move_src, move_dst
+ *                    [capacity], capacity >= n_pages / 2, the moves first,
+ *                    then -1.  info: 0; moves; live pages; free pages.
+ * kda_pages_copy     cache row move_dst[i] = cache row move_src[i] (the
+ *                    payload; gaps are not touched) where both are in
+ *                    [0, n_rows), on any kda_cache: latent pages or recurrent
+ *                    states.  Preconditions: destinations unique, none is a
+ *                    source.
+ * workspace: kda_pages_workspace_size(n_pages, count) bytes (count 0 for
+ * kda_pages_compact), 256-byte aligned, contents on entry do not matter.
+ * Errors: KDA_ERR_NULL, _LAYOUT (a table's sizes below 1, table_stride <
+ * width, reserved != 0), _SHAPE, _DTYPE, _RANGE, _ALIGN, _WORKSPACE, _CUDA.
+ * ---------------------------------------------------------------------- */
+size_t kda_pages_workspace_size(int64_t n_pages, int64_t count);
+int kda_pages_fork(const kda_page_table *table, const void *src, const void *dst, int32_t idx_type,
+                   int64_t count, void *stream);
+int kda_pages_release(const kda_page_table *table, const void *req, int32_t idx_type,
+                      const int32_t *keep, int64_t count, void *stream);
+int kda_pages_reserve(const kda_page_table *table, const void *req, int32_t idx_type,
+                      const int32_t *new_tokens, int64_t count, int32_t *move_src,
+                      int32_t *move_dst, int32_t *info, void *workspace, size_t ws_bytes,
+                      void *stream);
+int kda_pages_compact(const kda_page_table *table, int32_t *move_src, int32_t *move_dst,
+                      int64_t capacity, int32_t *info, void *workspace, size_t ws_bytes,
+                      void *stream);
+int kda_pages_copy(const kda_cache *cache, const void *move_src, const void *move_dst,
+                   int32_t idx_type, int64_t count, void *stream);
+
 /* Human-readable name of a kda_status value (static string, never NULL). */
 const char *kda_status_string(int32_t status);
 

@@ -9,6 +9,10 @@ arguments - every step of the computation runs in the library's CUDA kernels.
     kda_prefill_workspace_size(total_tokens, num_seqs, h, dk, dv)
     kda_prefill_varlen(q, k, v, g, beta, cu_seqlens, out, workspace, ...)
     kda_decode_step(q, k, v, g, beta, cache, idx, out, ...)
+    kda_latent_decode(q, cache, block_table, seq_lens, out, workspace, latent_dim=...)
+    kda_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, out, workspace, ...)
+    kda_latent_append(x, cu, req, table, cache)
+    kda_pages_{fork,release,reserve,compact,copy}(...)
 
 `cache` is a 4-D tensor view [N, H, V, K] whose inner [H, V, K] block is dense
 and whose stride(0) >= H*V*K (page gaps allowed); its data_ptr() already
@@ -21,7 +25,7 @@ import ctypes
 import torch
 
 from ._abi import (EXPORTED, KDA_BF16, KDA_F32, KDA_I32, KDA_I64, LIB_PATH, KdaCache, KdaError,
-                   _check, lib)
+                   KdaPageTable, _check, lib)
 
 __all__ = [
     "kda_state_gather", "kda_state_scatter", "kda_prefill_workspace_size", "kda_prefill_workspace_size_compact",
@@ -29,6 +33,9 @@ __all__ = [
     "kda_prefill_varlen_cached", "kda_prefill_checkpoint_count", "kda_prefill_varlen_noalloc",
     "kda_prefill_noalloc_status", "kda_decode_step",
     "kda_ckpt_store_int8", "kda_ckpt_load_int8", "kda_conv1d_varlen", "kda_conv1d_update", "kda_target_verify",
+    "kda_latent_decode_workspace_size", "kda_latent_decode", "kda_latent_prefill_workspace_size", "kda_latent_prefill",
+    "kda_latent_append", "kda_pages_workspace_size", "kda_pages_fork", "kda_pages_release", "kda_pages_reserve",
+    "kda_pages_compact", "kda_pages_copy", "page_table_descriptor",
     "kda_status_string", "kda_prefill_workspace_status", "kda_selftest_bounded_wait", "cache_descriptor",
     "KdaError", "EXPORTED", "LIB_PATH",
 ]
@@ -365,6 +372,184 @@ def kda_decode_step(q, k, v, g, beta, cache, idx, out, *, scale: float | None = 
                                float(scale), 1 if qk_l2norm else 0, ctypes.byref(d), _ptr(idx),
                                _itype_code(idx), _ptr(out), _stream(stream))
     _check(rc, "kda_decode_step")
+
+
+def page_table_descriptor(block_table: torch.Tensor, seq_lens: torch.Tensor, refcount: torch.Tensor,
+                          page_size: int) -> KdaPageTable:
+    """kda_page_table over [requests, width] block tables (unit inner stride), [requests]
+    lengths and [n_pages] refcounts, all int32 on the device.  The calls write through it, so
+    it keeps the tensors alive."""
+    _need(all(t.dtype == torch.int32 for t in (block_table, seq_lens, refcount)), "page tables must be int32")
+    _need(block_table.dim() == 2 and (block_table.shape[1] == 1 or block_table.stride(1) == 1),
+          "block_table must be [requests, width] with a unit inner stride")
+    R, W = block_table.shape
+    _need(seq_lens.is_contiguous() and tuple(seq_lens.shape) == (R,), "seq_lens must be contiguous [requests]")
+    _need(refcount.is_contiguous() and refcount.dim() == 1, "refcount must be contiguous [n_pages]")
+    stride = block_table.stride(0) if R > 1 else max(W, block_table.stride(0))
+    d = KdaPageTable(block_table.data_ptr(), seq_lens.data_ptr(), refcount.data_ptr(), R, W, stride, refcount.numel(),
+                     int(page_size), 0)
+    d.tensors = (block_table, seq_lens, refcount)
+    return d
+
+
+def kda_latent_decode_workspace_size(batch: int, L: int, h: int, dl: int, dr: int) -> int:
+    return int(lib().kda_latent_decode_workspace_size(batch, L, h, dl, dr))
+
+
+def kda_latent_decode(q, cache, block_table, seq_lens, out, workspace, *, latent_dim: int, scale: float, req=None,
+                      lse=None, stream=None) -> None:
+    """Absorbed latent attention over paged latents: q [R, L, H, dl + dr] (bf16, queries in the
+    latent space) against the tokens of each request; out [R, L, H, dl] bf16, lse [R, L, H]
+    fp32 or None.  cache: a [n_pages, 1, page, dl + dr] bf16 view; block_table [requests,
+    width] and seq_lens [requests] int32; req [R] int32/int64 picks the rows (None: r).  With
+    L > 1 the query tokens are the request's last L (causal).  `scale` is the model's softmax
+    scale (that of its expanded head size, so it has no default here)."""
+    _need(q.dim() == 4, "q must be [R, L, H, dl + dr]")
+    R, L, H, D = q.shape
+    dl = int(latent_dim)
+    _need(q.is_contiguous() and tuple(out.shape) == (R, L, H, dl) and out.is_contiguous(),
+          "q and out must be contiguous [R, L, H, dl + dr] and [R, L, H, dl]")
+    _need(out.dtype == q.dtype, "q and out share a dtype")
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and
+          (block_table.shape[1] == 1 or block_table.stride(1) == 1), "block_table must be int32 [requests, width], unit inner stride")
+    B, W = block_table.shape
+    _need(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and tuple(seq_lens.shape) == (B,),
+          "seq_lens must be contiguous int32 [requests]")
+    if req is not None:
+        _index_vector(req)
+        _need(req.numel() == R, "req must hold one row per batch entry")
+    if lse is not None:
+        _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (R, L, H),
+              "lse must be contiguous float32 [R, L, H]")
+    _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be a uint8 tensor")
+    d = cache_descriptor(cache)
+    rc = lib().kda_latent_decode(_ptr(q), _dtype_code(q), R, L, H, dl, D - dl, float(scale), ctypes.byref(d),
+                                 _ptr(block_table), B, W, block_table.stride(0) if B > 1 else max(W, block_table.stride(0)),
+                                 _ptr(seq_lens), _ptr(req), 0 if req is None else _itype_code(req), _ptr(out), _ptr(lse),
+                                 _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "kda_latent_decode")
+
+
+def kda_latent_prefill_workspace_size(total_q: int, num_seqs: int, h: int) -> int:
+    return int(lib().kda_latent_prefill_workspace_size(total_q, num_seqs, h))
+
+
+def kda_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, out, workspace, *, scale: float | None = None, lse=None,
+                       stream=None) -> None:
+    """Causal latent attention in the expanded form over a varlen batch: q [Tq, H, dn + dr];
+    k_nope [Tk, H, dn] and v [Tk, H, dv] (any token and head strides), k_rope [Tk, dr] shared by
+    the heads (any token stride), all bf16; cu_q, cu_k [B + 1] int32; each sequence's queries
+    are its last tokens.  out [Tq, H, dv] bf16; lse [Tq, H] fp32 or None."""
+    _need(q.dim() == 3 and k_nope.dim() == 3 and v.dim() == 3 and k_rope.dim() == 2,
+          "q, k_nope, v must be 3-D [T, H, D], k_rope 2-D [T, dr]")
+    Tq, H, D = q.shape
+    Tk, _, dn = k_nope.shape
+    dv, dr = v.shape[2], k_rope.shape[1]
+    _need(tuple(k_nope.shape) == (Tk, H, dn) and tuple(v.shape) == (Tk, H, dv) and tuple(k_rope.shape) == (Tk, dr) and
+          D == dn + dr, "shapes must agree: q [Tq, H, dn + dr], k_nope [Tk, H, dn], k_rope [Tk, dr], v [Tk, H, dv]")
+    _need(q.is_contiguous() and out.is_contiguous() and tuple(out.shape) == (Tq, H, dv), "q and out must be contiguous")
+    for name, t in (("k_nope", k_nope), ("k_rope", k_rope), ("v", v)):
+        _need(t.shape[-1] == 1 or t.stride(-1) == 1, f"{name} must have a unit inner stride")
+    _need(len({t.dtype for t in (q, k_nope, k_rope, v, out)}) == 1, "q, k_nope, k_rope, v, out share a dtype")
+    B = cu_q.numel() - 1
+    for name, t in (("cu_q", cu_q), ("cu_k", cu_k)):
+        _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() == B + 1 and B >= 1,
+              f"{name} must be a contiguous int32 tensor of B + 1 >= 2 offsets")
+    if lse is not None:
+        _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (Tq, H),
+              "lse must be contiguous float32 [Tq, H]")
+    _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be a uint8 tensor")
+    if scale is None:
+        scale = D ** -0.5
+    rc = lib().kda_latent_prefill(_ptr(q), _dtype_code(q), _ptr(k_nope), k_nope.stride(0), k_nope.stride(1), _ptr(k_rope),
+                                  k_rope.stride(0), _ptr(v), v.stride(0), v.stride(1), _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, H,
+                                  dn, dr, dv, float(scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                  _stream(stream))
+    _check(rc, "kda_latent_prefill")
+
+
+def kda_latent_append(x, cu, req, table: KdaPageTable, cache, stream=None) -> None:
+    """Rows cu[i] .. cu[i+1]-1 of x [T, D] become the last tokens of request req[i] in its pages
+    (kda_pages_reserve has made room and advanced the lengths)."""
+    _need(x.dim() == 2 and (x.shape[1] == 1 or x.stride(1) == 1), "x must be [T, D] with a unit inner stride")
+    _need(x.dtype == cache.dtype and x.shape[1] == cache.shape[3], "x must have the cache's dtype and row width")
+    _index_vector(req)
+    _need(cu.dtype == torch.int32 and cu.is_contiguous() and cu.numel() == req.numel() + 1,
+          "cu must be a contiguous int32 tensor of count + 1 offsets")
+    d = cache_descriptor(cache)
+    T, D = x.shape
+    rc = lib().kda_latent_append(_ptr(x), x.stride(0) if T > 1 else max(D, x.stride(0)), T, _ptr(cu), _ptr(req),
+                                 _itype_code(req), req.numel(), ctypes.byref(table), ctypes.byref(d), _stream(stream))
+    _check(rc, "kda_latent_append")
+
+
+def kda_pages_workspace_size(n_pages: int, count: int) -> int:
+    return int(lib().kda_pages_workspace_size(n_pages, count))
+
+
+def _same_lists(*lists) -> None:
+    for t in lists:
+        _index_vector(t)
+        _need(t.numel() == lists[0].numel() and t.dtype == lists[0].dtype, "index lists: same length and dtype")
+
+
+def _int32_vector(name: str, t, n: int) -> None:
+    _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n, f"{name} must be a contiguous int32 tensor of {n}")
+
+
+def kda_pages_fork(table: KdaPageTable, src, dst, stream=None) -> None:
+    """Request dst[i] becomes a copy of request src[i] that shares its pages."""
+    _same_lists(src, dst)
+    _check(lib().kda_pages_fork(ctypes.byref(table), _ptr(src), _ptr(dst), _itype_code(src), src.numel(), _stream(stream)),
+           "kda_pages_fork")
+
+
+def kda_pages_release(table: KdaPageTable, req, keep=None, stream=None) -> None:
+    """Request req[i] keeps its first keep[i] tokens (None: none) and gives back the pages behind them."""
+    _index_vector(req)
+    if keep is not None:
+        _int32_vector("keep", keep, req.numel())
+    _check(lib().kda_pages_release(ctypes.byref(table), _ptr(req), _itype_code(req), _ptr(keep), req.numel(),
+                                   _stream(stream)), "kda_pages_release")
+
+
+def kda_pages_reserve(table: KdaPageTable, req, new_tokens, move_src, move_dst, info, workspace, stream=None) -> None:
+    """Request req[i] grows by new_tokens[i]: new pages enter its row, its length advances, and a
+    shared unfinished last page is replaced by a new one, (move_src[i], move_dst[i]) naming
+    the copy to make (-1, -1: none).  info int32 [4]: 0 done / 1 too few free pages / 2 a row
+    too short (then nothing changed); moves; pages asked for; pages free before."""
+    _index_vector(req)
+    n = req.numel()
+    for name, t in (("new_tokens", new_tokens), ("move_src", move_src), ("move_dst", move_dst)):
+        _int32_vector(name, t, n)
+    _int32_vector("info", info, 4)
+    _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be a uint8 tensor")
+    rc = lib().kda_pages_reserve(ctypes.byref(table), _ptr(req), _itype_code(req), _ptr(new_tokens), n, _ptr(move_src),
+                                 _ptr(move_dst), _ptr(info), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "kda_pages_reserve")
+
+
+def kda_pages_compact(table: KdaPageTable, move_src, move_dst, info, workspace, stream=None) -> None:
+    """The live pages take the numbers 0 .. live-1: tables and refcounts follow, (move_src,
+    move_dst) name the copies to make (the moves first, then -1; at least n_pages // 2 entries
+    each).  info int32 [4]: 0; moves; live pages; free pages."""
+    n = move_src.numel()
+    _int32_vector("move_src", move_src, n)
+    _int32_vector("move_dst", move_dst, n)
+    _int32_vector("info", info, 4)
+    _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be a uint8 tensor")
+    rc = lib().kda_pages_compact(ctypes.byref(table), _ptr(move_src), _ptr(move_dst), n, _ptr(info), _ptr(workspace),
+                                 workspace.numel(), _stream(stream))
+    _check(rc, "kda_pages_compact")
+
+
+def kda_pages_copy(cache, move_src, move_dst, stream=None) -> None:
+    """cache[move_dst[i]] = cache[move_src[i]] where both are valid rows (latent pages or states)."""
+    _same_lists(move_src, move_dst)
+    d = cache_descriptor(cache)
+    rc = lib().kda_pages_copy(ctypes.byref(d), _ptr(move_src), _ptr(move_dst), _itype_code(move_src), move_src.numel(),
+                              _stream(stream))
+    _check(rc, "kda_pages_copy")
 
 
 def kda_status_string(status: int) -> str:

@@ -39,6 +39,17 @@ EXPORTED = (
     "kda_ckpt_store_int8",
     "kda_ckpt_load_int8",
     "kda_decode_step",
+    "kda_latent_decode_workspace_size",
+    "kda_latent_decode",
+    "kda_latent_prefill_workspace_size",
+    "kda_latent_prefill",
+    "kda_latent_append",
+    "kda_pages_workspace_size",
+    "kda_pages_fork",
+    "kda_pages_release",
+    "kda_pages_reserve",
+    "kda_pages_compact",
+    "kda_pages_copy",
     "kda_status_string",
     "kda_last_cuda_error_string",
     "kda_prefill_workspace_status",
@@ -57,6 +68,21 @@ class KdaCache(ctypes.Structure):
         ("v", ctypes.c_int64),
         ("k", ctypes.c_int64),
         ("row_stride", ctypes.c_int64),
+    ]
+
+
+class KdaPageTable(ctypes.Structure):
+    """Mirror of the C struct kda_page_table."""
+    _fields_ = [
+        ("block_table", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("refcount", ctypes.c_void_p),
+        ("requests", ctypes.c_int64),
+        ("width", ctypes.c_int64),
+        ("table_stride", ctypes.c_int64),
+        ("n_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -122,6 +148,31 @@ def lib():
         L.kda_decode_step.argtypes = [vp, vp, vp, i32, vp, vp, i64, i32, i32, i32, f32, i32, cache_p, vp, i32,
                                       vp, vp]
         L.kda_decode_step.restype = ctypes.c_int
+        table_p = ctypes.POINTER(KdaPageTable)
+        L.kda_latent_decode_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+        L.kda_latent_decode_workspace_size.restype = sz
+        L.kda_latent_decode.argtypes = [vp, i32, i64, i32, i32, i32, i32, f32, cache_p, vp, i64, i64, i64, vp, vp, i32,
+                                        vp, vp, vp, sz, vp]
+        L.kda_latent_decode.restype = ctypes.c_int
+        L.kda_latent_prefill_workspace_size.argtypes = [i64, i64, i32]
+        L.kda_latent_prefill_workspace_size.restype = sz
+        L.kda_latent_prefill.argtypes = [vp, i32, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i64, i64, i64, i32, i32,
+                                         i32, i32, f32, vp, vp, vp, sz, vp]
+        L.kda_latent_prefill.restype = ctypes.c_int
+        L.kda_latent_append.argtypes = [vp, i64, i64, vp, vp, i32, i64, table_p, cache_p, vp]
+        L.kda_latent_append.restype = ctypes.c_int
+        L.kda_pages_workspace_size.argtypes = [i64, i64]
+        L.kda_pages_workspace_size.restype = sz
+        L.kda_pages_fork.argtypes = [table_p, vp, vp, i32, i64, vp]
+        L.kda_pages_fork.restype = ctypes.c_int
+        L.kda_pages_release.argtypes = [table_p, vp, i32, vp, i64, vp]
+        L.kda_pages_release.restype = ctypes.c_int
+        L.kda_pages_reserve.argtypes = [table_p, vp, i32, vp, i64, vp, vp, vp, vp, sz, vp]
+        L.kda_pages_reserve.restype = ctypes.c_int
+        L.kda_pages_compact.argtypes = [table_p, vp, vp, i64, vp, vp, sz, vp]
+        L.kda_pages_compact.restype = ctypes.c_int
+        L.kda_pages_copy.argtypes = [cache_p, vp, vp, i32, i64, vp]
+        L.kda_pages_copy.restype = ctypes.c_int
         L.kda_status_string.argtypes = [i32]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_last_cuda_error_string.argtypes = []

@@ -402,6 +402,197 @@ int kda_conv1d_update(const void *x, int32_t io_dtype, int64_t batch, int64_t ch
     return cuda_status(kda::launch_conv1d_update(a, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+// [status word | the kernels' own]: every attention workspace is 256-byte aligned and of the full size.
+int check_workspace(const void *ws, size_t have, size_t need)
+{
+    if (ws == nullptr) return KDA_ERR_NULL;
+    return aligned(ws, 256) && have >= need ? KDA_OK : KDA_ERR_WORKSPACE;
+}
+
+int check_page_table(const kda_page_table *t)
+{
+    if (t == nullptr || t->block_table == nullptr || t->seq_lens == nullptr || t->refcount == nullptr) return KDA_ERR_NULL;
+    if (t->reserved != 0 || t->requests < 1 || t->width < 1 || t->n_pages < 1 || t->page_size < 1 ||
+        t->table_stride < t->width)
+        return KDA_ERR_LAYOUT;
+    // page numbers, positions and the requests' page ranks are 32-bit; offsets into the table 64-bit
+    const int64_t lim = INT64_C(1) << 31;
+    if (t->n_pages >= lim || t->requests >= lim || t->width >= lim || t->width * t->page_size >= lim ||
+        t->table_stride > (INT64_C(1) << 40) || static_cast<__int128>(t->requests) * t->table_stride > (INT64_C(1) << 60))
+        return KDA_ERR_RANGE;
+    if (!aligned(t->block_table, 4) || !aligned(t->seq_lens, 4) || !aligned(t->refcount, 4)) return KDA_ERR_ALIGN;
+    return KDA_OK;
+}
+
+// Checks shared by the calls that take a list of requests.  KDA_OK with *count == 0: nothing to launch.
+int check_page_list(const kda_page_table *t, const void *req, int32_t idx_type, int64_t count)
+{
+    const int rc = check_page_table(t);
+    if (rc != KDA_OK) return rc;
+    if (!valid_itype(idx_type)) return KDA_ERR_DTYPE;
+    if (count < 0) return KDA_ERR_SHAPE;
+    if (count >= (INT64_C(1) << 30)) return KDA_ERR_RANGE;
+    return count == 0 ? KDA_OK : check_index_array(req, idx_type);
+}
+}  // namespace
+
+size_t kda_latent_decode_workspace_size(int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr)
+{
+    if (batch < 0 || L < 1 || h < 1 || (dl != 256 && dl != 512) || dr != 64) return 0;
+    if (static_cast<int64_t>(L) * h > (1 << 20) || static_cast<__int128>(batch) * L * h >= (INT64_C(1) << 31)) return 0;
+    return kda::latent_decode_workspace(batch, L, h, dl);
+}
+
+int kda_latent_decode(const void *q, int32_t io_dtype, int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr,
+                      float scale, const kda_cache *cache, const int32_t *block_table, int64_t requests, int64_t width,
+                      int64_t table_stride, const int32_t *seq_lens, const void *req, int32_t idx_type, void *out,
+                      float *lse, void *workspace, size_t ws_bytes, void *stream)
+{
+    kda::CacheDesc c{};
+    int rc = check_cache(cache, &c);
+    if (rc != KDA_OK) return rc;
+    if (io_dtype != KDA_BF16 || c.dtype != KDA_BF16 || (req != nullptr && !valid_itype(idx_type))) return KDA_ERR_DTYPE;
+    if (batch < 0 || L < 1 || h < 1 || dl < 1 || dr < 1 || requests < 1 || width < 1 || table_stride < width ||
+        c.h != 1 || c.k != static_cast<int64_t>(dl) + dr || (req == nullptr && requests < batch))
+        return KDA_ERR_SHAPE;
+    if ((dl != 256 && dl != 512) || dr != 64 || c.v % 8 != 0) return KDA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(L) * h > (1 << 20) || static_cast<__int128>(batch) * L * h >= (INT64_C(1) << 31) ||
+        static_cast<__int128>(width) * c.v >= (INT64_C(1) << 31) || c.n_rows >= (INT64_C(1) << 31) ||
+        static_cast<__int128>(requests) * table_stride > (INT64_C(1) << 60))
+        return KDA_ERR_RANGE;
+    if (batch == 0) return KDA_OK;
+    if (q == nullptr || block_table == nullptr || seq_lens == nullptr || out == nullptr) return KDA_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(c.data, 16) || c.row_stride % 8 != 0 || !aligned(lse, 4) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4) || (req != nullptr && !aligned(req, idx_type == KDA_I32 ? 4 : 8)))
+        return KDA_ERR_ALIGN;
+    if ((rc = check_workspace(workspace, ws_bytes, kda::latent_decode_workspace(batch, L, h, dl))) != KDA_OK) return rc;
+    kda::LatentDecodeArgs a{q, batch, L, h, dl, dr, scale, c, block_table, requests, width, table_stride, c.v, seq_lens, req,
+                            idx_type, out, lse, workspace};
+    return cuda_status(kda::launch_latent_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_latent_prefill_workspace_size(int64_t total_q, int64_t num_seqs, int32_t h)
+{
+    if (total_q < 0 || total_q >= (INT64_C(1) << 31) - 256 || num_seqs < 1 || num_seqs >= (1 << 24) || h < 1 || h > 1024) return 0;
+    return kda::latent_prefill_workspace(total_q, num_seqs, h);
+}
+
+int kda_latent_prefill(const void *q, int32_t io_dtype, const void *k_nope, int64_t kn_token, int64_t kn_head,
+                       const void *k_rope, int64_t kr_token, const void *v, int64_t v_token, int64_t v_head,
+                       const int32_t *cu_q, const int32_t *cu_k, int64_t num_seqs, int64_t total_q, int64_t total_k,
+                       int32_t h, int32_t dn, int32_t dr, int32_t dv, float scale, void *out, float *lse, void *workspace,
+                       size_t ws_bytes, void *stream)
+{
+    if (io_dtype != KDA_BF16) return KDA_ERR_DTYPE;
+    if (num_seqs < 1 || total_q < 0 || total_k < 0 || h < 1 || dn < 1 || dr < 1 || dv < 1 || kn_token < 0 || kn_head < 0 ||
+        kr_token < 0 || v_token < 0 || v_head < 0)
+        return KDA_ERR_SHAPE;
+    if (dn != 128 || dv != 128 || dr != 64) return KDA_ERR_UNSUPPORTED;
+    const int64_t most = (INT64_C(1) << 31) - 256;
+    if (total_q >= most || total_k >= most || num_seqs >= (1 << 24) || h > 1024) return KDA_ERR_RANGE;
+    const int64_t strides[] = {kn_token, kn_head, kr_token, v_token, v_head};
+    for (int64_t s : strides)
+        if (s >= (INT64_C(1) << 38)) return KDA_ERR_RANGE;
+    if (total_q == 0) return KDA_OK;
+    if (q == nullptr || cu_q == nullptr || cu_k == nullptr || out == nullptr) return KDA_ERR_NULL;
+    if (total_k > 0 && (k_nope == nullptr || k_rope == nullptr || v == nullptr)) return KDA_ERR_NULL;
+    const void *vec16[] = {q, k_nope, k_rope, v, out};
+    for (const void *p : vec16)
+        if (!aligned(p, 16)) return KDA_ERR_ALIGN;
+    for (int64_t s : strides)
+        if (s % 8 != 0) return KDA_ERR_ALIGN;
+    if (!aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(lse, 4)) return KDA_ERR_ALIGN;
+    const int rc = check_workspace(workspace, ws_bytes, kda::latent_prefill_workspace(total_q, num_seqs, h));
+    if (rc != KDA_OK) return rc;
+    kda::LatentPrefillArgs a{q, k_nope, k_rope, v, kn_token, kn_head, kr_token, v_token, v_head, cu_q, cu_k, num_seqs,
+                             total_q, total_k, h, scale, out, lse, workspace};
+    return cuda_status(kda::launch_latent_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kda_latent_append(const void *x, int64_t x_stride, int64_t total, const int32_t *cu, const void *req, int32_t idx_type,
+                      int64_t count, const kda_page_table *table, const kda_cache *cache, void *stream)
+{
+    kda::CacheDesc c{};
+    int rc = check_cache(cache, &c);
+    if (rc != KDA_OK) return rc;
+    if ((rc = check_page_list(table, req, idx_type, count)) != KDA_OK) return rc;
+    if (total < 0 || c.h != 1 || c.v != table->page_size || c.n_rows < table->n_pages || x_stride < c.k) return KDA_ERR_SHAPE;
+    if (total >= (INT64_C(1) << 31) || static_cast<__int128>(total) * x_stride > (INT64_C(1) << 60)) return KDA_ERR_RANGE;
+    if (total == 0 || count == 0) return KDA_OK;
+    if (x == nullptr || cu == nullptr) return KDA_ERR_NULL;
+    if (!aligned(x, static_cast<uintptr_t>(esize(c.dtype))) || !aligned(cu, 4)) return KDA_ERR_ALIGN;
+    return cuda_status(kda::launch_latent_append(x, x_stride, total, cu, req, idx_type, count, *table, c,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_pages_workspace_size(int64_t n_pages, int64_t count)
+{
+    if (n_pages < 1 || n_pages >= (INT64_C(1) << 31) || count < 0 || count >= (INT64_C(1) << 30)) return 0;
+    return kda::pages_workspace(n_pages, count);
+}
+
+int kda_pages_fork(const kda_page_table *table, const void *src, const void *dst, int32_t idx_type, int64_t count,
+                   void *stream)
+{
+    int rc = check_page_list(table, src, idx_type, count);
+    if (rc != KDA_OK || count == 0) return rc;
+    if ((rc = check_index_array(dst, idx_type)) != KDA_OK) return rc;
+    return cuda_status(kda::launch_pages_fork(*table, src, dst, idx_type, count, static_cast<cudaStream_t>(stream)));
+}
+
+int kda_pages_release(const kda_page_table *table, const void *req, int32_t idx_type, const int32_t *keep, int64_t count,
+                      void *stream)
+{
+    const int rc = check_page_list(table, req, idx_type, count);
+    if (rc != KDA_OK || count == 0) return rc;
+    if (!aligned(keep, 4)) return KDA_ERR_ALIGN;
+    return cuda_status(kda::launch_pages_release(*table, req, idx_type, keep, count, static_cast<cudaStream_t>(stream)));
+}
+
+int kda_pages_reserve(const kda_page_table *table, const void *req, int32_t idx_type, const int32_t *new_tokens,
+                      int64_t count, int32_t *move_src, int32_t *move_dst, int32_t *info, void *workspace, size_t ws_bytes,
+                      void *stream)
+{
+    int rc = check_page_list(table, req, idx_type, count);
+    if (rc != KDA_OK || count == 0) return rc;
+    if (new_tokens == nullptr || move_src == nullptr || move_dst == nullptr || info == nullptr) return KDA_ERR_NULL;
+    const void *vec4[] = {new_tokens, move_src, move_dst, info};
+    for (const void *p : vec4)
+        if (!aligned(p, 4)) return KDA_ERR_ALIGN;
+    if ((rc = check_workspace(workspace, ws_bytes, kda::pages_workspace(table->n_pages, count))) != KDA_OK) return rc;
+    return cuda_status(kda::launch_pages_reserve(*table, req, idx_type, new_tokens, count, move_src, move_dst, info,
+                                                 workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int kda_pages_compact(const kda_page_table *table, int32_t *move_src, int32_t *move_dst, int64_t capacity, int32_t *info,
+                      void *workspace, size_t ws_bytes, void *stream)
+{
+    int rc = check_page_table(table);
+    if (rc != KDA_OK) return rc;
+    if (capacity < table->n_pages / 2) return KDA_ERR_SHAPE;
+    if (capacity >= (INT64_C(1) << 31)) return KDA_ERR_RANGE;
+    if (info == nullptr || (capacity > 0 && (move_src == nullptr || move_dst == nullptr))) return KDA_ERR_NULL;
+    if (!aligned(move_src, 4) || !aligned(move_dst, 4) || !aligned(info, 4)) return KDA_ERR_ALIGN;
+    if ((rc = check_workspace(workspace, ws_bytes, kda::pages_workspace(table->n_pages, 0))) != KDA_OK) return rc;
+    return cuda_status(kda::launch_pages_compact(*table, move_src, move_dst, capacity, info, workspace,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+int kda_pages_copy(const kda_cache *cache, const void *move_src, const void *move_dst, int32_t idx_type, int64_t count,
+                   void *stream)
+{
+    kda::CacheDesc c{};
+    int rc = check_cache(cache, &c);
+    if (rc != KDA_OK) return rc;
+    if (!valid_itype(idx_type)) return KDA_ERR_DTYPE;
+    if (count < 0) return KDA_ERR_SHAPE;
+    if (count == 0) return KDA_OK;
+    if ((rc = check_index_array(move_src, idx_type)) != KDA_OK) return rc;
+    if ((rc = check_index_array(move_dst, idx_type)) != KDA_OK) return rc;
+    return cuda_status(kda::launch_pages_copy(c, move_src, move_dst, idx_type, count, static_cast<cudaStream_t>(stream)));
+}
+
 const char *kda_status_string(int32_t status)
 {
     switch (status) {

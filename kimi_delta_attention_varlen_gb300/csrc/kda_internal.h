@@ -96,6 +96,56 @@ struct Conv1dUpdateArgs {
 };
 cudaError_t launch_conv1d_update(const Conv1dUpdateArgs &a, cudaStream_t st);
 
+// Absorbed latent attention over paged latents (dl in {256, 512}, dr = 64, bf16).
+struct LatentDecodeArgs {
+    const void *q;  // [batch, L, h, dl + dr]
+    int64_t batch;
+    int32_t L, h, dl, dr;
+    float scale;
+    CacheDesc cache;  // [n_pages, 1, page, dl + dr]
+    const int32_t *block_table;
+    int64_t requests, width, table_stride, page;
+    const int32_t *seq_lens;
+    const void *req;  // nullable
+    int32_t idx_type;
+    void *out;
+    float *lse;  // nullable
+    void *workspace;
+};
+size_t latent_decode_workspace(int64_t batch, int32_t L, int32_t h, int32_t dl);
+cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t st);
+
+// Expanded latent attention over a varlen batch (dn = dv = 128, dr = 64, bf16).
+struct LatentPrefillArgs {
+    const void *q, *k_nope, *k_rope, *v;
+    int64_t kn_token, kn_head, kr_token, v_token, v_head;
+    const int32_t *cu_q, *cu_k;
+    int64_t num_seqs, total_q, total_k;
+    int32_t h;
+    float scale;
+    void *out;
+    float *lse;  // nullable
+    void *workspace;
+};
+size_t latent_prefill_workspace(int64_t total_q, int64_t num_seqs, int32_t h);
+cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st);
+
+// Page upkeep and the append of latent rows (pages.cu).
+size_t pages_workspace(int64_t n_pages, int64_t count);
+cudaError_t launch_pages_fork(const kda_page_table &t, const void *src, const void *dst, int32_t itype, int64_t count,
+                              cudaStream_t st);
+cudaError_t launch_pages_release(const kda_page_table &t, const void *req, int32_t itype, const int32_t *keep,
+                                 int64_t count, cudaStream_t st);
+cudaError_t launch_pages_reserve(const kda_page_table &t, const void *req, int32_t itype, const int32_t *new_tokens,
+                                 int64_t count, int32_t *move_src, int32_t *move_dst, int32_t *info, void *ws,
+                                 cudaStream_t st);
+cudaError_t launch_pages_compact(const kda_page_table &t, int32_t *move_src, int32_t *move_dst, int64_t capacity,
+                                 int32_t *info, void *ws, cudaStream_t st);
+cudaError_t launch_pages_copy(const CacheDesc &c, const void *src, const void *dst, int32_t itype, int64_t count,
+                              cudaStream_t st);
+cudaError_t launch_latent_append(const void *x, int64_t x_stride, int64_t total, const int32_t *cu, const void *req,
+                                 int32_t itype, int64_t count, const kda_page_table &t, const CacheDesc &c, cudaStream_t st);
+
 // INT8 checkpoints; the cache's head size k (== v) is 32, 64 or 128.
 cudaError_t launch_ckpt_store_int8(const CacheDesc &c, const void *src, const void *dst, int32_t idx_type,
                                    int64_t count, int8_t *qdata, float *scale, int64_t n_slots, cudaStream_t st);

@@ -1,0 +1,325 @@
+"""Latent attention on the GPU, the absorbed form over paged latents and the expanded form over
+varlen batches, against plain 64-bit forms (tests/latent_helpers.py: formulas and tolerances).
+Whatever lies outside a request's tokens holds NaN and infinities throughout."""
+import math
+
+import pytest
+import torch
+
+import kimi_delta_attention_varlen_gb300 as kda
+from kimi_delta_attention_varlen_gb300 import workloads as wl
+from tests.latent_helpers import assert_attention, decode_reference, prefill_reference
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+def poisoned(*shape):
+    """NaN, +inf and -inf in turn."""
+    t = torch.empty(*shape, dtype=BF, device=DEV)
+    flat = t.view(-1)
+    flat[0::3], flat[1::3], flat[2::3] = math.nan, math.inf, -math.inf
+    return t
+
+
+def paged_latents(lens, page, dl, seed, gap=0, spare=3, width_extra=0):
+    """Random latents of the given lengths in random pages of a poisoned cache whose rows lie
+    `gap` elements apart; (cache view, block table, seq_lens, per-request rows)."""
+    g = wl.generator(seed, DEV)
+    D = dl + 64
+    need = [-(-n // page) for n in lens]
+    N = sum(need) + spare
+    back = poisoned(N, page * D + gap)
+    cache = back.as_strided((N, 1, page, D), (page * D + gap, page * D, D, 1))
+    perm = torch.randperm(N, generator=g, device=DEV).tolist()
+    W = max(1, max(need)) + width_extra
+    table = torch.full((len(lens), W), -1, dtype=torch.int32)
+    rows, at = [], 0
+    for r, n in enumerate(lens):
+        x = torch.randn(n, D, generator=g, device=DEV).to(BF)
+        rows.append(x)
+        for j in range(need[r]):
+            p = perm[at]
+            at += 1
+            table[r, j] = p
+            part = x[j * page:(j + 1) * page]
+            cache[p, 0, :part.shape[0]] = part
+    return cache, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), rows
+
+
+def run_decode(q, cache, table, lens, dl, scale, req=None, stream=None, lse=True):
+    R, L, H, D = q.shape
+    out = poisoned(R, L, H, dl)
+    ls = torch.full((R, L, H), math.nan, device=DEV) if lse else None
+    ws = torch.empty(kda.kda_latent_decode_workspace_size(R, L, H, dl, D - dl), dtype=torch.uint8, device=DEV)
+    ws.fill_(0xA5)
+    torch.cuda.synchronize()
+    kda.kda_latent_decode(q, cache, table, lens, out, ws, latent_dim=dl, scale=scale, req=req, lse=ls, stream=stream)
+    torch.cuda.synchronize()
+    assert kda.kda_prefill_workspace_status(ws) == 0
+    return out, ls
+
+
+def queries(R, L, H, D, seed):
+    return torch.randn(R, L, H, D, generator=wl.generator(seed + 77, DEV), device=DEV).to(BF)
+
+
+SCALE = 192 ** -0.5
+
+
+@pytest.mark.parametrize("dl", [512, 256])
+@pytest.mark.parametrize("page", [8, 16, 48, 64, 128, 200])
+def test_decode_lengths_and_pages(page, dl):
+    lens = [0, 1, 2, 63, 64, 65, 127, 128, 129, 191, 193, 500, 1000, page, page + 1, 3 * page - 1]
+    cache, table, sl, rows = paged_latents(lens, page, dl, seed=page + dl)
+    q = queries(len(lens), 1, 32, dl + 64, seed=page)
+    out, lse = run_decode(q, cache, table, sl, dl, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, dl), f"page {page} dl {dl}")
+
+
+@pytest.mark.parametrize("heads", [1, 2, 5, 8, 16, 17, 32, 48, 64, 65, 100, 128, 192])
+def test_decode_heads(heads):
+    lens = [1, 70, 333]
+    cache, table, sl, rows = paged_latents(lens, 32, 512, seed=heads, gap=24)
+    q = queries(3, 1, heads, 576, seed=heads)
+    out, lse = run_decode(q, cache, table, sl, 512, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, 512), f"heads {heads}")
+
+
+@pytest.mark.parametrize("L,heads", [(2, 32), (3, 16), (4, 128), (5, 8), (7, 1), (70, 2)])
+def test_decode_draft_tokens_are_causal(L, heads):
+    # lengths below L: the first query tokens see nothing
+    lens = [0, 1, L - 1, L, L + 1, 64 + L, 129, 700]
+    cache, table, sl, rows = paged_latents(lens, 16, 512, seed=L, width_extra=3)
+    q = queries(len(lens), L, heads, 576, seed=L)
+    out, lse = run_decode(q, cache, table, sl, 512, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, 512), f"L {L} heads {heads}")
+
+
+@pytest.mark.parametrize("lens,heads", [([40000], 32), ([9999, 3, 25000], 16), ([6400] * 5, 64), ([20000, 1], 128)])
+def test_decode_long_contexts(lens, heads):
+    # few rows: the cache axis is split and the parts are joined
+    cache, table, sl, rows = paged_latents(lens, 64, 512, seed=heads)
+    q = queries(len(lens), 1, heads, 576, seed=heads)
+    out, lse = run_decode(q, cache, table, sl, 512, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, 512), "long")
+    again, lse2 = run_decode(q, cache, table, sl, 512, SCALE)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)  # no result depends on the order of arrival
+
+
+def test_decode_many_requests():
+    g = wl.generator(5)
+    lens = torch.randint(0, 400, (700,), generator=g).tolist()
+    cache, table, sl, rows = paged_latents(lens, 16, 512, seed=9)
+    q = queries(len(lens), 1, 4, 576, seed=3)
+    out, lse = run_decode(q, cache, table, sl, 512, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, 512), "many")
+
+
+def test_decode_large_scores_and_growing_maxima():
+    # scores rise by hundreds along the cache: every tile brings a new maximum
+    n, dl = 1000, 512
+    cache, table, sl, rows = paged_latents([n], 64, dl, seed=1)
+    x = rows[0]
+    u = torch.randn(576, generator=wl.generator(2, DEV), device=DEV)
+    ramp = torch.linspace(-6, 6, n, device=DEV)[:, None]
+    new = (x.float() * 0.1 + ramp * u / u.norm() * 4).to(BF)
+    for j in range(table.shape[1]):
+        part = new[j * 64:(j + 1) * 64]
+        cache[table[0, j].long(), 0, :part.shape[0]] = part
+    q = (u[None, None, None].expand(1, 1, 16, 576) * torch.tensor([1.0, -1.0] * 8, device=DEV)[None, None, :, None]).to(BF).contiguous()
+    out, lse = run_decode(q, cache, table, sl, dl, 1.0)
+    assert_attention(out, lse, decode_reference(q, lambda r, k: new[:k], [n], 1.0, dl), "ramp")
+
+
+def test_decode_rows_by_request_index_and_invalid_rows():
+    lens = [100, 0, 257, 64]
+    cache, table, sl, rows = paged_latents(lens, 32, 512, seed=4)
+    pick = [2, -1, 0, 4, 3, 2, 1 << 20]
+    q = queries(len(pick), 1, 16, 576, seed=1)
+    ok = [p if 0 <= p < 4 else None for p in pick]
+    ref = decode_reference(q, lambda r, n: rows[ok[r]][:n] if n else rows[0][:0], [0 if p is None else lens[p] for p in ok], SCALE, 512)
+    for dt in (torch.int32, torch.int64):
+        out, lse = run_decode(q, cache, table, sl, 512, SCALE, req=torch.tensor(pick, dtype=dt, device=DEV))
+        assert_attention(out, lse, ref, f"req {dt}")
+    out64, _ = run_decode(q[1:2].contiguous(), cache, table, sl, 512, SCALE, req=torch.tensor([-1 - (1 << 40)], device=DEV), lse=False)
+    assert (out64 == 0).all()
+
+
+def test_decode_invalid_pages_read_as_zeros_and_lengths_are_clamped():
+    lens = [150, 90]
+    cache, table, sl, rows = paged_latents(lens, 16, 512, seed=6)
+    table = table.clone()
+    table[0, 2], table[0, 9], table[1, 0] = -1, cache.shape[0], 2 ** 31 - 1
+    q = queries(2, 1, 32, 576, seed=2)
+    for r, j in ((0, 2), (0, 9), (1, 0)):
+        rows[r][16 * j:16 * j + 16] = 0
+    out, lse = run_decode(q, cache, table, sl, 512, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, 512), "invalid pages")
+    # a length above the row's capacity is that capacity; a negative one is 0
+    full = torch.randn(2 * 16, 576, device=DEV).to(BF)
+    cache2 = full.view(2, 1, 16, 576)
+    t2 = torch.tensor([[1, 0], [0, 1]], dtype=torch.int32, device=DEV)
+    out, lse = run_decode(q, cache2, t2, torch.tensor([2 ** 31 - 1, -5], dtype=torch.int32, device=DEV), 512, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: torch.cat([full[16:], full[:16]])[:n], [32, 0], SCALE, 512), "clamped")
+
+
+def test_decode_shared_pages_strided_table_and_own_stream():
+    lens = [130, 130, 70]
+    cache, table, sl, rows = paged_latents(lens, 64, 512, seed=8, gap=8)
+    table[1] = table[0]  # a fork shares its pages
+    wide = torch.full((3, 11), 2 ** 30, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    q = queries(3, 1, 32, 576, seed=4)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    out, lse = run_decode(q, cache, wide[:, :table.shape[1]], sl, 512, SCALE, stream=st)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[0 if r == 1 else r][:n], lens, SCALE, 512), "shared")
+
+
+def test_decode_pages_beyond_32_bit_offsets():
+    page, D, N = 64, 576, 7
+    stride = (1 << 30) + 8  # elements between pages: the last one starts beyond 2^32 elements
+    back = torch.empty((N - 1) * stride + page * D, dtype=BF, device=DEV)
+    cache = back.as_strided((N, 1, page, D), (stride, page * D, D, 1))
+    x = torch.randn(3 * page, D, generator=wl.generator(1, DEV), device=DEV).to(BF)
+    order = [6, 2, 5]
+    for j, p in enumerate(order):
+        cache[p, 0] = x[j * page:(j + 1) * page]
+    q = queries(1, 1, 32, D, seed=11)
+    n = 3 * page - 5
+    out, lse = run_decode(q, cache, torch.tensor([order], dtype=torch.int32, device=DEV),
+                          torch.tensor([n], dtype=torch.int32, device=DEV), 512, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, k: x[:k], [n], SCALE, 512), "far pages")
+
+
+def test_decode_in_a_graph_follows_new_lengths():
+    lens = [200, 3000]
+    cache, table, sl, rows = paged_latents(lens, 64, 512, seed=3)
+    q = queries(2, 1, 32, 576, seed=5)
+    out, lse = torch.empty(2, 1, 32, 512, dtype=BF, device=DEV), torch.empty(2, 1, 32, device=DEV)
+    ws = torch.empty(kda.kda_latent_decode_workspace_size(2, 1, 32, 512, 64), dtype=torch.uint8, device=DEV)
+    kda.kda_latent_decode(q, cache, table, sl, out, ws, latent_dim=512, scale=SCALE, lse=lse)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kda.kda_latent_decode(q, cache, table, sl, out, ws, latent_dim=512, scale=SCALE, lse=lse)
+    for now in ([200, 3000], [1, 2500], [0, 65]):
+        sl.copy_(torch.tensor(now, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], now, SCALE, 512), f"graph {now}")
+
+
+# ---------------------------------------------------------------- prefill --
+
+def prompt_batch(nq, nk, heads, seed, tail=5):
+    """q, k_nope / v as slices of one projection, k_rope as the tail of latent rows; rows behind the last token are poisoned."""
+    g = wl.generator(seed, DEV)
+    Tq, Tk = sum(nq), sum(nk)
+    kv, rows, q = poisoned(Tk + tail, heads, 256), poisoned(Tk + tail, 576), poisoned(Tq + tail, heads, 192)
+    kv[:Tk] = torch.randn(Tk, heads, 256, generator=g, device=DEV).to(BF)
+    rows[:Tk, 512:] = torch.randn(Tk, 64, generator=g, device=DEV).to(BF)
+    q[:Tq] = torch.randn(Tq, heads, 192, generator=g, device=DEV).to(BF)
+    cu = [[0], [0]]
+    for a, b in zip(nq, nk):
+        cu[0].append(cu[0][-1] + a)
+        cu[1].append(cu[1][-1] + b)
+    return q[:Tq], kv[:Tk, :, :128], rows[:Tk, 512:], kv[:Tk, :, 128:], cu[0], cu[1]
+
+
+def run_prefill(q, kn, kr, v, cu_q, cu_k, scale=SCALE, stream=None):
+    Tq, H, _ = q.shape
+    guard = poisoned(Tq + 2, H, 128)
+    out, lse = guard[1:-1], torch.full((Tq, H), math.nan, device=DEV)
+    ws = torch.empty(kda.kda_latent_prefill_workspace_size(Tq, len(cu_q) - 1, H), dtype=torch.uint8, device=DEV)
+    ws.fill_(0xA5)
+    before = guard.view(torch.int16).clone()
+    cq, ck = (torch.tensor(c, dtype=torch.int32, device=DEV) for c in (cu_q, cu_k))
+    torch.cuda.synchronize()
+    kda.kda_latent_prefill(q, kn, kr, v, cq, ck, out, ws, scale=scale, lse=lse, stream=stream)
+    torch.cuda.synchronize()
+    assert kda.kda_prefill_workspace_status(ws) == 0
+    assert torch.equal(guard.view(torch.int16)[[0, -1]], before[[0, -1]])
+    return out, lse
+
+
+def check_prefill(nq, nk, heads, seed, **kw):
+    q, kn, kr, v, cu_q, cu_k = prompt_batch(nq, nk, heads, seed)
+    out, lse = run_prefill(q, kn, kr, v, cu_q, cu_k, **kw)
+    assert_attention(out, lse, prefill_reference(q, kn, kr, v, cu_q, cu_k, kw.get("scale", SCALE)), f"{nq} {nk} heads {heads}")
+
+
+@pytest.mark.parametrize("n", [1, 2, 31, 63, 64, 65, 127, 128, 129, 191, 255, 256, 257, 383, 385, 640])
+def test_prefill_one_prompt(n):
+    check_prefill([n], [n], 2, seed=n)
+
+
+@pytest.mark.parametrize("heads", [1, 3, 8, 32])
+def test_prefill_batch_with_empty_and_short_prompts(heads):
+    nq = [64, 0, 100, 1, 37, 300, 0, 128, 129, 5]
+    check_prefill(nq, nq, heads, seed=heads)
+
+
+@pytest.mark.parametrize("nq,nk", [([1, 50, 200], [129, 50, 900]), ([256, 3, 17], [300, 1000, 17]), ([5, 1, 128], [2000, 1, 128 * 5]),
+                                   ([130, 0, 2], [131, 40, 258])])
+def test_prefill_on_prefixes(nq, nk):
+    check_prefill(nq, nk, 4, seed=sum(nk))
+
+
+def test_prefill_queries_that_see_nothing():
+    # fewer keys than queries: the first queries of a sequence see no key
+    check_prefill([10, 200, 300, 40], [4, 0, 131, 40], 3, seed=12)
+    q, kn, kr, v, cu_q, cu_k = prompt_batch([7], [0], 2, seed=1)
+    out, lse = run_prefill(q, kn, kr, v, cu_q, cu_k)
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_prefill_large_scores():
+    check_prefill([300], [300], 2, seed=5, scale=3.0)
+
+
+def test_prefill_longer_batch_is_repeatable():
+    q, kn, kr, v, cu_q, cu_k = prompt_batch([1500, 700, 2100], [1500, 1100, 2100], 2, seed=2)
+    out, lse = run_prefill(q, kn, kr, v, cu_q, cu_k)
+    assert_attention(out, lse, prefill_reference(q, kn, kr, v, cu_q, cu_k, SCALE), "long")
+    again, lse2 = run_prefill(q, kn, kr, v, cu_q, cu_k)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_prefill_contiguous_and_head_major_inputs_agree_on_another_stream():
+    q, kn, kr, v, cu_q, cu_k = prompt_batch([150, 61], [150, 200], 5, seed=3)
+    out, lse = run_prefill(q, kn, kr, v, cu_q, cu_k)
+    st = torch.cuda.Stream()
+    head_major = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    out2, lse2 = run_prefill(q, kn.contiguous(), kr.contiguous(), head_major(v), cu_q, cu_k, stream=st)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+def test_prefill_values_shared_by_all_heads():
+    # head stride 0: one key and value head for all query heads
+    q, kn, kr, v, cu_q, cu_k = prompt_batch([140], [140], 4, seed=9)
+    kn1, v1 = kn[:, :1].expand(-1, 4, -1), v[:, :1].expand(-1, 4, -1)
+    out, lse = run_prefill(q, kn1, kr, v1, cu_q, cu_k)
+    assert_attention(out, lse, prefill_reference(q, kn1, kr, v1, cu_q, cu_k, SCALE), "shared heads")
+
+
+def test_prefill_and_decode_are_the_same_attention():
+    # the last token's output, expanded and absorbed: q W_k^T against the latents, W_v behind
+    n, H = 333, 8
+    g = wl.generator(21, DEV)
+    c = torch.randn(n, 576, generator=g, device=DEV).to(BF)
+    wk = (torch.randn(H, 512, 128, generator=g, device=DEV) / 512 ** 0.5).to(BF)
+    wv = (torch.randn(H, 512, 128, generator=g, device=DEV) / 512 ** 0.5).to(BF)
+    q = torch.randn(n, H, 192, generator=g, device=DEV).to(BF)
+    kn, v = (torch.einsum("td,hde->the", c[:, :512].float(), w.float()).to(BF) for w in (wk, wv))
+    out, _ = run_prefill(q, kn, c[:, 512:], v, [0, n], [0, n])
+    qa = torch.cat([torch.einsum("he,hde->hd", q[-1, :, :128].float(), wk.float()), q[-1, :, 128:].float()], -1).to(BF)
+    pad = poisoned(6, 1, 64, 576)
+    pad.view(-1, 576)[:n] = c
+    lat, _ = run_decode(qa[None, None].contiguous(), pad, torch.arange(6, dtype=torch.int32, device=DEV)[None],
+                        torch.tensor([n], dtype=torch.int32, device=DEV), 512, SCALE)
+    want = torch.einsum("hd,hde->he", lat[0, 0].double(), wv.double())
+    # each side rounds its keys or queries, probabilities and outputs to bf16: a few 2^-9 of the values' size
+    assert (out[-1].double() - want).abs().max() <= 6 * 2.0 ** -9 * v.double().abs().max()
