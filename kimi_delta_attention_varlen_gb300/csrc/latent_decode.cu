@@ -1,97 +1,716 @@
 // Absorbed latent attention over paged latents (kda_latent_decode).
 //
-// One warp a query row (one head of one query token), eight rows a CTA; tiles
-// of 32 tokens pass through shared memory once for the eight rows.  Per tile,
-// lane j holds token j's score; the running maximum m, the sum l of
-// e^{z - m} and the output are rescaled by e^{m_old - m_new} when m grows, so
-// the latents are read once.
+// For one request the query rows are its L x H (token, head) pairs, all of them against the same
+// cache rows x_j = [c_j | r_j].  With S = scale Q X^T and P = e^{S - m}, out = P C / l: the cache
+// is read once, as the keys of the first product and (its first dl columns) as the values of the
+// second, while the softmax keeps a running maximum m and sum l a row.
+//
+// One persistent CTA per SM.  The tiles (T tokens of one request, for one group of at most N query
+// rows) of the whole batch lie on one line, request by request; CTA c takes the c-th equal share, so
+// few long requests fill the GPU as well as many short ones.  A (request, group) that falls into
+// several shares leaves unnormalised parts in the workspace, and a second kernel joins them in order
+// of their tiles (so the result does not depend on which CTA was first).
+//
+// Warps of a CTA: one issues the TMA copies, one the MMAs of each product, four do the softmax and
+// the epilogue.
+//   S   = Q X^T        M = 64 (rows; fewer than 64 leave lanes unused), N = T tokens, K = dl + 64
+//   O^T = C^T P^T      M = 128 value dimensions (dl / 128 of them), N rows, K = T tokens
+// The second product is transposed so that the accumulator's width is the number of rows, not dl:
+// 4 x N tensor-memory columns instead of dl.  A tile arrives as panels of T tokens x 64 dimensions
+// (128-byte swizzle), which serve as K-major B of the first product and, two side by side, as
+// MN-major A of the second.  Panels travel in pairs through a ring (the rope panel through a ring of
+// its own) and are handed back pair by pair as the second product is done with them.
+//
+// The probabilities enter the second product in bf16, the only operand type the tensor cores take
+// beside bf16 values; the output is normalised by the sum of those rounded weights (they then sum
+// to one exactly), the log-sum-exp taken from the sum before rounding.  A request of a single tile
+// has few weights to average the rounding over, so there a second pass adds the product of what the
+// rounding left off (its own rounding is 2^-16 of the weight).
+//
+// The accumulator is rescaled only when a row's maximum has grown by more than 2^8 since the last
+// rescale (the exponents are relative to that older maximum, exact in fp32 and in bf16's range).
+// Every wait is bounded; an expired one sets the workspace's status word (6) and ends the CTA.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "tcgen05.cuh"
 
 namespace kda {
+namespace prefill {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // chunk_prep.cu
+}
 namespace {
 
-constexpr int kTile = 32;
-constexpr int kRows = 8;
+constexpr int T = 64;  // tokens a tile
+constexpr int kThreads = 256;
+constexpr int kSoftThreads = 128;
+constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr float kLazy = 8.f;  // log2 of the growth that forces a rescale
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kStatusExpired = 6;
 
-template <int DL, int DR>
-__global__ void __launch_bounds__(kRows * 32) latent_decode_kernel(LatentDecodeArgs a)
+template <int DL_, int N_> struct Cfg {
+    static constexpr int DL = DL_, N = N_;
+    static constexpr int D = DL + 64, PANELS = D / 64, PAIRS = DL / 128;  // of a tile: all panels, pairs of value panels
+    static constexpr int PB = T * 128;                                    // bytes of a panel
+    static constexpr int ROPE = N == 64 ? 2 : 3;                          // rope panels in flight
+    static constexpr int Q_BYTES = PANELS * N * 128, P_BYTES = N * 128;
+    // 230,400 bytes: 227 KB less the alignment slack and the barriers
+    static constexpr int RING_FIT = (230400 - Q_BYTES - P_BYTES - ROPE * PB) / (2 * PB);
+    static constexpr int RING = RING_FIT < 3 * PAIRS ? RING_FIT : 3 * PAIRS;  // pairs in flight
+    static constexpr int OFF_P = Q_BYTES, OFF_ROPE = OFF_P + P_BYTES, OFF_RING = OFF_ROPE + ROPE * PB;
+    static constexpr int SMEM = OFF_RING + RING * 2 * PB + 1024;
+    static_assert(RING >= PAIRS && SMEM <= 231424, "a tile fits the ring, the ring fits shared memory");
+};
+
+struct Params {
+    LatentDecodeArgs a;
+    int32_t rows, groups, box_rows;  // L * h; row groups; rows of a TMA box (divides the page size)
+    float scale_log2;
+    int32_t *status, *item0, *item1;  // [grid]: item whose part is in slot 0 / 1 of the CTA, or -1
+    float4 *ml;                       // [grid][2][N]: m, l, l of the rounded probabilities
+    float *part;                      // [grid][2][N][dl]
+};
+
+struct Maps {
+    CUtensorMap q, cache;
+};
+
+__device__ __forceinline__ int64_t slot_of(const LatentDecodeArgs &a, int64_t r)
 {
-    constexpr int D = DL + DR, PER = DL / 32;
-    __shared__ __nv_bfloat16 kv[kTile][D + 2];
-    __shared__ __nv_bfloat16 qs[kRows][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r = blockIdx.y;
-    const int row = blockIdx.x * kRows + warp, rows = a.L * a.h;
-    int64_t slot = r;
-    if (a.req != nullptr)
-        slot = a.idx_type == KDA_I32 ? static_cast<const int32_t *>(a.req)[r] : static_cast<const int64_t *>(a.req)[r];
-    int64_t n = 0;
-    if (slot >= 0 && slot < a.requests) {
-        const int64_t most = a.width * a.page;
-        n = a.seq_lens[slot];
-        n = n < 0 ? 0 : n > most ? most : n;
+    if (a.req == nullptr) return r;
+    return a.idx_type == KDA_I32 ? static_cast<int64_t>(static_cast<const int32_t *>(a.req)[r])
+                                 : static_cast<const int64_t *>(a.req)[r];
+}
+
+__device__ __forceinline__ int32_t length_of(const LatentDecodeArgs &a, int64_t slot)
+{
+    if (slot < 0 || slot >= a.requests) return 0;
+    const int32_t most = static_cast<int32_t>(a.width * a.page), n = a.seq_lens[slot];
+    return n < 0 ? 0 : n > most ? most : n;
+}
+
+__device__ __forceinline__ int32_t tiles_of(int32_t n) { return n > T ? (n - 1) / T + 1 : 1; }
+
+// Position on the line of tiles.
+struct Walk {
+    int64_t r, slot;
+    int32_t group, tile, n, tiles;
+
+    __device__ void load(const LatentDecodeArgs &a)
+    {
+        slot = slot_of(a, r);
+        n = length_of(a, slot);
+        tiles = tiles_of(n);
     }
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + (r * rows + row) * D;
-    if (row < rows)
-        for (int e = lane; e < D; e += 32) qs[warp][e] = q[e];
-    const int64_t seen = row < rows ? n - (a.L - 1 - row / a.h) : 0;
-    float m = -INFINITY, l = 0.f, o[PER];
+    __device__ bool first() const { return tile == 0; }
+    __device__ bool last() const { return tile + 1 == tiles; }
+    __device__ void next(const Params &p)
+    {
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++group < p.groups) return;
+        group = 0;
+        if (++r < p.a.batch) load(p.a);
+    }
+};
+
+// 32 columns of 16 lanes: registers 4 j + {0, 1} are row lane / 4, columns 8 j + 2 (lane % 4) + {0, 1}, and
+// 4 j + {2, 3} the same columns of row lane / 4 + 8.
+__device__ __forceinline__ void ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+                   "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ bool soft_any(bool v)  // the softmax warps (named barrier 1)
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r)
+                 : "r"(v ? 1u : 0u), "n"(kSoftThreads)
+                 : "memory");
+    return r != 0;
+}
+
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn)  // bf16 operands, fp32 accumulator, B K-major
+{
+    return tc::idesc_bf16(M, N, false) | ((a_mn ? 1u : 0u) << 15);
+}
+
+// One lane of the (converged) warp.  Copies and MMAs are issued under this test and not under a test
+// of the lane number: after elect.sync the compiler knows that one thread runs and keeps addresses and
+// descriptors in uniform registers (measured per MMA: 32 to 48 cycles, the operands' shared memory
+// time, instead of 54 to 112).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r)::"memory");
+    return r != 0;
+}
+
+template <class C> struct Bars {
+    uint64_t full[C::RING], empty[C::RING], rope_full[C::ROPE], rope_empty[C::ROPE];
+    uint64_t q_full, q_free, s[2], s_free[2], p, o, drain[2];
+};
+
+template <int DL, int N>
+__global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, const __grid_constant__ Maps maps)
+{
+    using C = Cfg<DL, N>;
+    extern __shared__ char smem_raw[];
+    char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) Bars<C> bar;
+    __shared__ uint32_t tmem_base;
+    __shared__ float corr[2][N], linv[N];  // corr: by parity of the tile, so that a late reader keeps its own
+    __shared__ int64_t sums[kThreads / 32];
+    __shared__ int64_t start_r;
+    __shared__ int32_t start_rest;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
+    const int cta = blockIdx.x;
+
+    if (warp == 3) {
+        tc::tmem_alloc(&tmem_base, 512);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int j = 0; j < C::RING; ++j) mbar_init(&bar.full[j], 1), mbar_init(&bar.empty[j], 1);
+        for (int j = 0; j < C::ROPE; ++j) mbar_init(&bar.rope_full[j], 1), mbar_init(&bar.rope_empty[j], 1);
+        mbar_init(&bar.q_full, 1), mbar_init(&bar.q_free, 1), mbar_init(&bar.s[0], 1), mbar_init(&bar.s[1], 1);
+        mbar_init(&bar.p, kSoftThreads), mbar_init(&bar.o, 1);
+        for (int j = 0; j < 2; ++j) mbar_init(&bar.s_free[j], kSoftThreads), mbar_init(&bar.drain[j], 1);
+        fence_mbar_init();
+        if (cta == 0) *p.status = 0;
+        p.item0[cta] = p.item1[cta] = -1;
+    }
+    // this CTA's share [w0, w1) of the line: the tiles before each thread's slice of the requests
+    const int64_t per = (p.a.batch + kThreads - 1) / kThreads, r_lo = per * tid;
+    const int64_t r_hi = r_lo + per < p.a.batch ? r_lo + per : p.a.batch;
+    int64_t mine = 0;
+    for (int64_t r = r_lo; r < r_hi; ++r) mine += tiles_of(length_of(p.a, slot_of(p.a, r)));
+    int64_t scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += y;
+    }
+    if (lane == 31) sums[warp] = scan;
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    int64_t before = scan - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        before += w < warp ? sums[w] : 0;
+        all += sums[w];
+    }
+    all *= p.groups;
+    const int64_t shares = all < gridDim.x ? all : gridDim.x;
+    const int64_t w0 = cta < shares ? all * cta / shares : all, w1 = cta < shares ? all * (cta + 1) / shares : all;
+    const int32_t total = static_cast<int32_t>(w1 - w0);
+    before *= p.groups;
+    if (w0 >= before && w0 < before + mine * p.groups) {
+        int64_t left = w0 - before, r = r_lo;
+        for (;; ++r) {
+            const int64_t t = static_cast<int64_t>(tiles_of(length_of(p.a, slot_of(p.a, r)))) * p.groups;
+            if (left < t) break;
+            left -= t;
+        }
+        start_r = r;
+        start_rest = static_cast<int32_t>(left);
+    }
+    __syncthreads();
+    const uint32_t tmem = tmem_base;
+    constexpr uint32_t kColS = 256;
+
+    Walk w{};
+    if (total > 0) {
+        w.r = start_r;
+        w.load(p.a);
+        w.group = start_rest / w.tiles;
+        w.tile = start_rest % w.tiles;
+    }
+    bool gave_up = false;
+    auto wait = [&](uint64_t *b, uint32_t parity) {
+        if (!gave_up && !mbar_wait(b, parity, kWaitLimit)) {
+            gave_up = true;
+            atomicExch(p.status, kStatusExpired);
+        }
+        return !gave_up;
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- copies
+        const int32_t br = p.box_rows, page = static_cast<int32_t>(p.a.page);
+        // page (an out-of-range coordinate, read as zeros, where the number is invalid) and row of chunk `lane`
+        auto lookup = [&](const Walk &x, int32_t *pg, int32_t *row) {
+            const int32_t t = x.tile * T + lane * br;
+            *pg = 0, *row = 0;
+            if (lane * br < T && t < x.n) {
+                const int32_t e = p.a.block_table[x.slot * p.a.table_stride + t / page];
+                *pg = e >= 0 && e < p.a.cache.n_rows ? e : static_cast<int32_t>(p.a.cache.n_rows);
+                *row = t % page;
+            }
+        };
+        auto all_wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+        int32_t pg = 0, row = 0, k = 0, i = 0, segs = 0;
+        if (total > 0) lookup(w, &pg, &row);
+        bool ok = true;  // the same in every lane
+        for (; i < total; ++i) {
+            Walk nx = w;
+            nx.next(p);
+            int32_t pg_next = 0, row_next = 0;
+            if (i + 1 < total) lookup(nx, &pg_next, &row_next);
+            if (i == 0 || w.first()) {
+                if (segs > 0 && !(ok = all_wait(&bar.q_free, (segs - 1) & 1))) break;
+                const int y = static_cast<int>(w.r * p.rows + w.group * N);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&bar.q_full, C::Q_BYTES);
+                    for (int e = 0; e < C::PANELS; ++e) tma_load_3d(smem + e * N * 128, &maps.q, 64 * e, y, 0, &bar.q_full);
+                }
+                __syncwarp();
+                ++segs;
+            }
+            const int32_t valid = w.n - w.tile * T < T ? w.n - w.tile * T : T;
+            const int32_t chunks = (valid + br - 1) / br;
+            for (int u = 0; u < C::PAIRS; ++u, ++k) {
+                const int s = k % C::RING;
+                if (!(ok = all_wait(&bar.empty[s], ((k / C::RING) & 1) ^ 1))) break;
+                if (elect_one()) mbar_arrive_expect_tx(&bar.full[s], 2 * chunks * br * 128);
+                __syncwarp();
+                for (int32_t c = 0; c < chunks; ++c) {
+                    const int32_t z = __shfl_sync(0xffffffffu, pg, c), y = __shfl_sync(0xffffffffu, row, c);
+                    char *dst = smem + C::OFF_RING + 2 * s * C::PB + c * br * 128;
+                    if (elect_one()) {
+                        tma_load_3d(dst, &maps.cache, 128 * u, y, z, &bar.full[s]);
+                        tma_load_3d(dst + C::PB, &maps.cache, 128 * u + 64, y, z, &bar.full[s]);
+                    }
+                    __syncwarp();
+                }
+            }
+            const int s = i % C::ROPE;
+            if (!ok || !(ok = all_wait(&bar.rope_empty[s], ((i / C::ROPE) & 1) ^ 1))) break;
+            if (elect_one()) mbar_arrive_expect_tx(&bar.rope_full[s], chunks * br * 128);
+            __syncwarp();
+            for (int32_t c = 0; c < chunks; ++c) {
+                const int32_t z = __shfl_sync(0xffffffffu, pg, c), y = __shfl_sync(0xffffffffu, row, c);
+                if (elect_one()) tma_load_3d(smem + C::OFF_ROPE + s * C::PB + c * br * 128, &maps.cache, DL, y, z, &bar.rope_full[s]);
+                __syncwarp();
+            }
+            w = nx, pg = pg_next, row = row_next;
+        }
+        if (!ok && lane == 0) {  // gave up: the copies in flight land before the CTA ends
+            for (int32_t e = k > C::RING ? k - C::RING : 0; e < k; ++e) mbar_wait(&bar.full[e % C::RING], (e / C::RING) & 1, kWaitLimit);
+            for (int32_t e = i > C::ROPE ? i - C::ROPE : 0; e < i; ++e) mbar_wait(&bar.rope_full[e % C::ROPE], (e / C::ROPE) & 1, kWaitLimit);
+            if (segs > 0) mbar_wait(&bar.q_full, (segs - 1) & 1, kWaitLimit);
+        }
+    } else if (warp == 1 && total > 0) {
+        // ----------------------------------------------------- first product: S
+        constexpr uint32_t kId = idesc(64, T, false);
+        const uint32_t base = smem_u32(smem);
+        const uint64_t q_desc = tc::sdesc_sw128(base, 16, 1024), key_desc = tc::sdesc_sw128(base + C::OFF_RING, 16, 1024),
+                       rope_desc = tc::sdesc_sw128(base + C::OFF_ROPE, 16, 1024);
+        int slot = 0, rope_slot = 0, segs = 0;
+        uint32_t par = 0, rope_par = 0;
+        auto ready = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+        bool ok = true;
+        for (int32_t i = 0; i < total && ok; ++i) {
+            const uint32_t d = tmem + kColS + T * (i & 1);
+            if (i > 1) ok = ready(&bar.s_free[i & 1], ((i >> 1) & 1) ^ 1);
+            if (ok && __all_sync(0xffffffffu, i == 0 || w.first())) ok = ready(&bar.q_full, segs++ & 1);
+            for (int u = 0; u < C::PAIRS && ok; ++u) {
+                if (!(ok = ready(&bar.full[slot], par))) break;
+                tc::fence_after_sync();
+                if (elect_one()) {
+                    const uint64_t q = q_desc + u * (2 * N * 128 >> 4), x = key_desc + slot * (2 * C::PB >> 4);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        tc::mma_bf16(d, q + (e >> 2) * (N * 128 >> 4) + (e & 3) * 2, x + (e >> 2) * (C::PB >> 4) + (e & 3) * 2, kId,
+                                     e > 0 || u > 0 ? 1u : 0u);
+                }
+                __syncwarp();
+                if (++slot == C::RING) slot = 0, par ^= 1u;
+            }
+            if (!ok || !(ok = ready(&bar.rope_full[rope_slot], rope_par))) break;
+            const bool last = __all_sync(0xffffffffu, w.last()) != 0;
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    tc::mma_bf16(d, q_desc + (2 * C::PAIRS * N * 128 >> 4) + ks * 2, rope_desc + rope_slot * (C::PB >> 4) + ks * 2, kId, 1u);
+                tc::commit(&bar.s[i & 1]);
+                tc::commit(&bar.rope_empty[rope_slot]);
+                if (last) tc::commit(&bar.q_free);
+            }
+            __syncwarp();
+            if (++rope_slot == C::ROPE) rope_slot = 0, rope_par ^= 1u;
+            w.next(p);
+        }
+        if (elect_one()) tc::commit(&bar.drain[0]);  // everything issued has completed before tensor memory is given back
+        mbar_wait(&bar.drain[0], 0, kWaitLimit);
+    } else if (warp == 2 && total > 0) {
+        // --------------------------------------------------- second product: O^T
+        constexpr uint32_t kId = idesc(128, N, true);
+        const uint32_t base = smem_u32(smem);
+        const uint64_t p_desc = tc::sdesc_sw128(base + C::OFF_P, 16, 1024),
+                       val_desc = tc::sdesc_sw128(base + C::OFF_RING, C::PB, 1024);
+        int slot = 0;
+        uint32_t passes = 0;
+        bool ok = true;
+        for (int32_t i = 0; i < total && ok; ++i) {
+            const uint32_t more = __all_sync(0xffffffffu, i == 0 || w.first()) ? 0u : 1u;
+            const bool two = __all_sync(0xffffffffu, w.tiles == 1) != 0;
+            for (int pass = two ? 0 : 1; pass < 2; ++pass, ++passes) {
+                if (!(ok = __all_sync(0xffffffffu, wait(&bar.p, passes & 1)) != 0)) break;
+                tc::fence_after_sync();
+                if (elect_one()) {
+                    int sl = slot;
+#pragma unroll
+                    for (int mt = 0; mt < C::PAIRS; ++mt) {
+                        const uint64_t v = val_desc + sl * (2 * C::PB >> 4);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc::mma_bf16(tmem + mt * N, v + ks * 128, p_desc + ks * 2, kId,
+                                         ks > 0 || (two && pass == 1) ? 1u : more);
+                        if (pass == 1) tc::commit(&bar.empty[sl]);
+                        sl = sl + 1 == C::RING ? 0 : sl + 1;
+                    }
+                    tc::commit(&bar.o);
+                }
+                __syncwarp();
+            }
+            slot = (slot + C::PAIRS) % C::RING;
+            w.next(p);
+        }
+        if (elect_one()) tc::commit(&bar.drain[1]);
+        mbar_wait(&bar.drain[1], 0, kWaitLimit);
+    } else if (warp >= 4 && total > 0) {
+        // --------------------------------------------------- softmax and epilogue
+        const int quad = warp & 3, g = lane >> 2, t = lane & 3;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+        const bool active = 16 * quad < N;  // this warp holds rows 16 quad ... + 15 of S
+        float m[2], l[2], lr[2];  // l: sum of the probabilities, lr: of their bf16 roundings
+        int32_t seen[2];
+        int slot_out = 0;
+        uint32_t passes = 0;  // of the second product, so far
+        // a thread that gave up goes on without waiting: all of them meet at every barrier
+        for (int32_t i = 0; i < total; ++i) {
+            const bool fresh = i == 0 || w.first();
+            if (fresh) {
+                slot_out = w.first() ? 1 : 0;  // where a part that is not the whole goes
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = w.group * N + 16 * quad + 8 * e + g;
+                    m[e] = -INFINITY;
+                    l[e] = lr[e] = 0.f;
+                    seen[e] = row < p.rows ? w.n - (p.a.L - 1 - row / p.a.h) : 0;
+                }
+            }
+            wait(&bar.s[i & 1], (i >> 1) & 1);
+            tc::fence_after_sync();
+            const int32_t t0 = w.tile * T;
+            uint32_t pk[2][T / 8];
+            float z[2][T / 4];  // rows g and g + 8 of this warp; columns 8 j + 2 t, + 1
+            bool grew = false;
+            if (active) {
+#pragma unroll
+                for (int c0 = 0; c0 < T; c0 += 32) {
+                    uint32_t s[16];
+                    ld_16x256b_x4(tl + kColS + T * (i & 1) + c0, s);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            z[e][c0 / 4 + 2 * j] = __uint_as_float(s[4 * j + 2 * e]) * p.scale_log2;
+                            z[e][c0 / 4 + 2 * j + 1] = __uint_as_float(s[4 * j + 2 * e + 1]) * p.scale_log2;
+                        }
+                }
+                tc::fence_before_sync();
+                mbar_arrive(&bar.s_free[i & 1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (t0 + T > seen[e]) {
+#pragma unroll
+                        for (int j = 0; j < T / 4; ++j)
+                            if (t0 + 8 * (j >> 1) + 2 * t + (j & 1) >= seen[e]) z[e][j] = -INFINITY;
+                    }
+                    float mx = z[e][0];
+#pragma unroll
+                    for (int j = 1; j < T / 4; ++j) mx = fmaxf(mx, z[e][j]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    float c = 1.f;
+                    if (m[e] == -INFINITY) {
+                        m[e] = mx;  // nothing summed yet
+                    } else if (mx > m[e] + kLazy) {
+                        c = ex2_approx(m[e] - mx);
+                        l[e] *= c;
+                        lr[e] *= c;
+                        m[e] = mx;
+                        grew = true;
+                    }
+                    if (t == 0) corr[i & 1][16 * quad + 8 * e + g] = c;
+                    const float base = m[e] == -INFINITY ? 0.f : m[e];
+                    float sum = 0.f, sum_r = 0.f;
+#pragma unroll
+                    for (int j = 0; j < T / 8; ++j) {
+                        const float a = ex2_approx(z[e][2 * j] - base), b = ex2_approx(z[e][2 * j + 1] - base);
+                        sum += a + b;
+                        pk[e][j] = pack_bf16x2(a, b);
+                        sum_r += bf16_lo(pk[e][j]) + bf16_hi(pk[e][j]);
+                    }
+                    l[e] += sum;
+                    lr[e] += sum_r;
+                }
+            } else {
+                mbar_arrive(&bar.s_free[i & 1]);
+            }
+            // the second product of the tile before has read P and written O^T
+            if (passes > 0) wait(&bar.o, (passes - 1) & 1);
+            tc::fence_after_sync();
+            auto put = [&]() {  // pk -> the operand P
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = 16 * quad + 8 * e + g;
+                    char *pr = smem + C::OFF_P + row * 128 + 4 * t;
+#pragma unroll
+                    for (int j = 0; j < T / 8; ++j) *reinterpret_cast<uint32_t *>(pr + ((j ^ (row & 7)) << 4)) = pk[e][j];
+                }
+            };
+            if (active) put();
+            if (w.n - t0 < T) {  // rows behind the last token: whatever they hold must not meet P = 0
+                const int from = w.n - t0;
+                for (int e = tid - 128; e < (T - from) * 2 * C::PAIRS * 8; e += kSoftThreads) {
+                    const int c = e & 7, pan = (e >> 3) % (2 * C::PAIRS), r2 = from + (e >> 3) / (2 * C::PAIRS);
+                    const int s = (i * C::PAIRS + (pan >> 1)) % C::RING;
+                    *reinterpret_cast<uint4 *>(smem + C::OFF_RING + (2 * s + (pan & 1)) * C::PB + r2 * 128 + c * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            fence_proxy_async_smem();
+            if (soft_any(grew) && !fresh) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < C::PAIRS * N; c0 += 16) {
+                    uint32_t o[16];
+                    tc::ld16(tl + c0, o);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr[i & 1][(c0 + e) % N]);
+                    tc::st16(tl + c0, o);
+                }
+                tc::wait_st();
+            }
+            tc::fence_before_sync();
+            mbar_arrive(&bar.p);
+            ++passes;
+            if (w.tiles == 1) {  // the second pass: what the rounding left off
+                if (active) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float base = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+                        for (int j = 0; j < T / 8; ++j)
+                            pk[e][j] = pack_bf16x2(ex2_approx(z[e][2 * j] - base) - bf16_lo(pk[e][j]),
+                                                   ex2_approx(z[e][2 * j + 1] - base) - bf16_hi(pk[e][j]));
+                        lr[e] = l[e];
+                    }
+                }
+                wait(&bar.o, (passes - 1) & 1);
+                tc::fence_after_sync();
+                if (active) put();
+                fence_proxy_async_smem();
+                tc::fence_before_sync();
+                mbar_arrive(&bar.p);
+                ++passes;
+            }
+            const bool last = w.last();
+            if (last || i + 1 == total) {  // the segment ends here
+                const bool whole = last && slot_out == 1;
+                const int64_t part = 2 * cta + slot_out;
+                if (active) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float sum = l[e], sum_r = lr[e];
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                        sum_r += __shfl_xor_sync(0xffffffffu, sum_r, 1);
+                        sum_r += __shfl_xor_sync(0xffffffffu, sum_r, 2);
+                        const int row = 16 * quad + 8 * e + g, rr = w.group * N + row;
+                        if (t == 0) {
+                            linv[row] = sum_r > 0.f ? 1.f / sum_r : 0.f;
+                            if (!whole) p.ml[part * N + row] = make_float4(m[e], sum, sum_r, 0.f);
+                            else if (p.a.lse != nullptr && rr < p.rows)
+                                p.a.lse[w.r * p.rows + rr] = sum > 0.f ? (m[e] + log2f(sum)) * kLn2 : -INFINITY;
+                        }
+                    }
+                }
+                if (!whole && tid == 128) (slot_out ? p.item1 : p.item0)[cta] = static_cast<int32_t>(w.r * p.groups + w.group);
+                wait(&bar.o, (passes - 1) & 1);
+                tc::fence_after_sync();
+                soft_any(false);  // linv is complete
+                const int valid = p.rows - w.group * N < N ? p.rows - w.group * N : N;
+                const int dim = 32 * quad + lane;
+#pragma unroll 1
+                for (int c0 = 0; c0 < C::PAIRS * N; c0 += 16) {
+                    uint32_t o[16];
+                    tc::ld16(tl + c0, o);
+                    tc::wait_ld();
+                    const int mt = c0 / N, row0 = c0 % N;
+                    if (whole) {
+                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
+                                             (w.r * p.rows + w.group * N + row0) * DL + mt * 128 + dim;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (row0 + e < valid) out[e * DL] = __float2bfloat16_rn(__uint_as_float(o[e]) * linv[row0 + e]);
+                    } else {
+                        float *out = p.part + (part * N + row0) * DL + mt * 128 + dim;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (row0 + e < valid) out[e * DL] = __uint_as_float(o[e]);
+                    }
+                }
+                tc::fence_before_sync();
+                soft_any(false);  // linv may be written again
+            }
+            w.next(p);
+        }
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 3) tc::tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the items that fell into several shares: CTA (c, row) takes the item whose first
+// part is in slot 1 of share c; the next parts are in slot 0 of the shares behind.
+template <int DL, int N>
+__global__ void __launch_bounds__(512) latent_join_kernel(Params p, int32_t shares)
+{
+    constexpr int PER = DL / 128;
+    __shared__ float acc[3][DL];
+    const int c = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, sub = tid >> 7, d = tid & 127;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int32_t item = p.item1[c];
+    if (item < 0) return;
+    const int64_t r = item / p.groups;
+    const int rr = item % p.groups * N + row;
+    if (rr >= p.rows) return;
+    int32_t parts = 1;
+    while (c + parts < shares && p.item0[c + parts] == item) ++parts;
+    auto at = [&](int32_t j) { return (static_cast<int64_t>(2) * (c + j) + (j == 0 ? 1 : 0)) * N + row; };
+    float m = -INFINITY, l = 0.f, lr = 0.f;
+    for (int32_t j = 0; j < parts; ++j) m = fmaxf(m, p.ml[at(j)].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    float o[PER];
 #pragma unroll
     for (int e = 0; e < PER; ++e) o[e] = 0.f;
-    const __nv_bfloat16 *cache = static_cast<const __nv_bfloat16 *>(a.cache.data);
-    for (int64_t t0 = 0; t0 < n; t0 += kTile) {
-        __syncthreads();
-        for (int j = warp; j < kTile; j += kRows) {
-            const int64_t t = t0 + j;
-            int64_t page = -1;
-            if (t < n) page = a.block_table[slot * a.table_stride + t / a.page];
-            const bool ok = page >= 0 && page < a.cache.n_rows;
-            const __nv_bfloat16 *x = cache + (ok ? page * a.cache.row_stride + (t % a.page) * D : 0);
-            for (int e = lane; e < D; e += 32) kv[j][e] = ok ? x[e] : __float2bfloat16_rn(0.f);
-        }
-        __syncthreads();
-        float z = 0.f;
-        for (int e = 0; e < D; ++e) z += __bfloat162float(qs[warp][e]) * __bfloat162float(kv[lane][e]);
-        z = t0 + lane < seen ? z * a.scale : -INFINITY;
-        float mx = z;
-        for (int s = 16; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-        mx = fmaxf(mx, m);
-        const float base = mx == -INFINITY ? 0.f : mx;
-        const float p = expf(z - base), c = expf(m - base);
-        float sum = p;
-        for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        l = l * c + sum;
-        m = mx;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) o[e] *= c;
-        for (int j = 0; j < kTile; ++j) {
-            const float w = __shfl_sync(0xffffffffu, p, j);
-            if (w != 0.f)  // a token that is not seen adds nothing, whatever its row holds
-#pragma unroll
-                for (int e = 0; e < PER; ++e) o[e] += w * __bfloat162float(kv[j][lane + 32 * e]);
-        }
+    for (int32_t j = 0; j < parts; ++j) {
+        const float4 ml = p.ml[at(j)];
+        const float f = ex2_approx(ml.x - base);
+        l += ml.y * f;
+        lr += ml.z * f;
     }
-    if (row >= rows) return;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (r * rows + row) * DL;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 4
+    for (int32_t j = sub; j < parts; j += 4) {
+        const float f = ex2_approx(p.ml[at(j)].x - base);
+        const float *x = p.part + at(j) * DL + d;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) out[lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
-    if (lane == 0 && a.lse != nullptr) a.lse[r * rows + row] = l > 0.f ? m + logf(l) : -INFINITY;
+        for (int e = 0; e < PER; ++e) o[e] += f * x[128 * e];
+    }
+    if (sub > 0) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[sub - 1][d + 128 * e] = o[e];
+    }
+    __syncthreads();
+    if (sub > 0) return;
+    const float inv = lr > 0.f ? 1.f / lr : 0.f;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (r * p.rows + rr) * DL + d;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        const float x = o[e] + acc[0][d + 128 * e] + acc[1][d + 128 * e] + acc[2][d + 128 * e];
+        out[128 * e] = __float2bfloat16_rn(x * inv);
+    }
+    if (d == 0 && p.a.lse != nullptr) p.a.lse[r * p.rows + rr] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+int rows_per_group(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Box of 64 columns x `rows` rows of a bf16 matrix [n2][n1][n0], strides in elements, 128-byte swizzle.
+bool encode(CUtensorMap *m, const void *base, int64_t n0, int64_t n1, int64_t n2, int64_t s1, int64_t s2, int rows)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = prefill::tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(n0), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1}, elem[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DL, int N> cudaError_t launch(Params p, cudaStream_t st)
+{
+    using C = Cfg<DL, N>;
+    const int grid = static_cast<int>(sm_count());
+    char *ws = static_cast<char *>(p.a.workspace);
+    p.status = reinterpret_cast<int32_t *>(ws);
+    p.item0 = p.status + 64;
+    p.item1 = p.item0 + grid;
+    p.ml = reinterpret_cast<float4 *>(ws + up256(256 + 8 * static_cast<size_t>(grid)));
+    p.part = reinterpret_cast<float *>(p.ml + static_cast<size_t>(2) * grid * N);
+    p.groups = (p.rows + N - 1) / N;
+    Maps maps;
+    const int64_t q_rows = p.a.batch * p.rows, pitch = p.a.cache.row_stride;
+    if (!encode(&maps.q, p.a.q, C::D, q_rows, 1, C::D, q_rows * C::D, N) ||
+        !encode(&maps.cache, p.a.cache.data, C::D, p.a.page, p.a.cache.n_rows, C::D, pitch, p.box_rows))
+        return cudaErrorInvalidValue;
+    auto kern = latent_decode_kernel<DL, N>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kThreads, C::SMEM, st>>>(p, maps);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid, p.rows < N ? p.rows : N);
+    cfg.blockDim = dim3(512);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_join_kernel<DL, N>, p, static_cast<int32_t>(grid));
 }
 
 }  // namespace
 
-size_t latent_decode_workspace(int64_t, int32_t, int32_t, int32_t) { return 256; }
+size_t latent_decode_workspace(int64_t batch, int32_t L, int32_t h, int32_t dl)
+{
+    const size_t n = rows_per_group(static_cast<int64_t>(L) * h), grid = static_cast<size_t>(sm_count());
+    (void)batch;
+    return up256(256 + 8 * grid) + 2 * grid * n * (16 + static_cast<size_t>(dl) * 4);
+}
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t st)
 {
-    cudaError_t e = cudaMemsetAsync(a.workspace, 0, 4, st);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>((a.L * a.h + kRows - 1) / kRows), static_cast<unsigned>(a.batch));
-    if (a.dl == 512) latent_decode_kernel<512, 64><<<grid, kRows * 32, 0, st>>>(a);
-    else latent_decode_kernel<256, 64><<<grid, kRows * 32, 0, st>>>(a);
-    return cudaGetLastError();
+    Params p{};
+    p.a = a;
+    p.rows = a.L * a.h;
+    p.scale_log2 = a.scale * kLog2e;
+    const int n = rows_per_group(p.rows);
+    p.box_rows = T;  // the largest power of two that divides the page, at most a tile
+    while (a.page % p.box_rows != 0) p.box_rows >>= 1;
+    if (a.dl == 512)
+        return n == 16 ? launch<512, 16>(p, st) : n == 32 ? launch<512, 32>(p, st) : launch<512, 64>(p, st);
+    return n == 16 ? launch<256, 16>(p, st) : n == 32 ? launch<256, 32>(p, st) : launch<256, 64>(p, st);
 }
 
 }  // namespace kda
