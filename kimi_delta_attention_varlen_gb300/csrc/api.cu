@@ -410,6 +410,9 @@ int check_workspace(const void *ws, size_t have, size_t need)
     return aligned(ws, 256) && have >= need ? KDA_OK : KDA_ERR_WORKSPACE;
 }
 
+// A softmax scale: positive and finite (its running maximum is taken before the scale is applied).
+bool valid_scale(float s) { return s > 0.f && s <= 3.0e38f; }
+
 int check_page_table(const kda_page_table *t)
 {
     if (t == nullptr || t->block_table == nullptr || t->seq_lens == nullptr || t->refcount == nullptr) return KDA_ERR_NULL;
@@ -457,7 +460,7 @@ int kda_latent_decode(const void *q, int32_t io_dtype, int64_t batch, int32_t L,
         c.h != 1 || c.k != static_cast<int64_t>(dl) + dr || (req == nullptr && requests < batch))
         return KDA_ERR_SHAPE;
     if ((dl != 256 && dl != 512) || dr != 64 || c.v % 8 != 0) return KDA_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(L) * h > (1 << 20) || static_cast<__int128>(batch) * L * h >= (INT64_C(1) << 31) ||
+    if (!valid_scale(scale) || static_cast<int64_t>(L) * h > (1 << 20) || static_cast<__int128>(batch) * L * h >= (INT64_C(1) << 31) ||
         static_cast<__int128>(width) * c.v >= (INT64_C(1) << 31) || c.n_rows >= (INT64_C(1) << 31) ||
         static_cast<__int128>(requests) * table_stride > (INT64_C(1) << 60))
         return KDA_ERR_RANGE;
@@ -490,10 +493,11 @@ int kda_latent_prefill(const void *q, int32_t io_dtype, const void *k_nope, int6
         return KDA_ERR_SHAPE;
     if (dn != 128 || dv != 128 || dr != 64) return KDA_ERR_UNSUPPORTED;
     const int64_t most = (INT64_C(1) << 31) - 256;
-    if (total_q >= most || total_k >= most || num_seqs >= (1 << 24) || h > 1024) return KDA_ERR_RANGE;
+    if (!valid_scale(scale) || total_q >= most || total_k >= most || num_seqs >= (1 << 24) || h > 1024) return KDA_ERR_RANGE;
     const int64_t strides[] = {kn_token, kn_head, kr_token, v_token, v_head};
     for (int64_t s : strides)
         if (s >= (INT64_C(1) << 38)) return KDA_ERR_RANGE;
+    if (total_k > 1 && (kn_token == 0 || kr_token == 0 || v_token == 0)) return KDA_ERR_SHAPE;  // tokens that share a row
     if (total_q == 0) return KDA_OK;
     if (q == nullptr || cu_q == nullptr || cu_k == nullptr || out == nullptr) return KDA_ERR_NULL;
     if (total_k > 0 && (k_nope == nullptr || k_rope == nullptr || v == nullptr)) return KDA_ERR_NULL;

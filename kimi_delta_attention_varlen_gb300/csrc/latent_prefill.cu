@@ -1,95 +1,551 @@
 // Expanded latent attention over a varlen batch (kda_latent_prefill).
 //
-// One warp a query, eight queries of one head a CTA; tiles of 32 keys and
-// values pass through shared memory once for the eight queries, with the
-// running maximum and sum of the softmax in registers.
+//   S = scale (Q_nope K_nope^T + Q_rope K_rope^T),  P = e^{S - m},  out = P V / l
+// per sequence and head, causal with the queries at the end of the keys, the keys visited in tiles
+// of 128 with a running maximum m and sum l a row.
+//
+// plan_kernel (one CTA) lists the query blocks (256 queries of one sequence), longest first by the
+// key tiles they see.  One persistent CTA per SM then takes every grid-th (block, head) pair of the
+// list.  A block is two query tiles s = 0, 1 of 128 rows that share the key and value tiles:
+//   S_s   = Q_s K^T     M = 128, N = 128, K = 192 (two nope panels and the shared rope panel)
+//   O_s  += P_s V       M = 128, N = 64 twice, K = 128, P_s in tensor memory
+// Tensor memory holds S_0, S_1, O_0, O_1 (128 columns each); P_s (bf16) overlays S_s.  While the
+// softmax of one tile runs, the tensor cores do the other tile's two products.  Warps: one issues the
+// TMA copies, one the MMAs, two warpgroups do the softmax (one row a thread) and the epilogues.
+// Key and value panels (128 tokens x 64, 16 KB, 128-byte swizzle) pass through one ring: per key tile
+// three key panels (K-major B), two value panels (MN-major B).
+//
+// O is rescaled only when a row's maximum has grown by more than 2^8 since the last rescale.  The
+// probabilities are rounded to bf16, the tensor cores' operand type; the output is normalised by the
+// sum of the rounded weights, the log-sum-exp taken from the sum before rounding.  A query tile that
+// sees a single key tile has few weights to average the rounding over, so there what the rounding
+// left off goes through a second product (the other half of S_s holds it).
+// Every wait is bounded; an expired one sets the workspace's status word (7).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "tcgen05.cuh"
 
 namespace kda {
+namespace prefill {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // chunk_prep.cu
+}
 namespace {
 
-constexpr int kTile = 32;
-constexpr int kRows = 8;
-constexpr int DN = 128, DR = 64, DV = 128, D = DN + DR;
+constexpr int DN = 128, DR = 64, DV = 128, DQ = DN + DR;
+constexpr int T = 128;                     // queries and keys of a tile
+constexpr int kBlock = 2 * T;              // queries of a block
+constexpr int PB = T * 128;                // bytes of a panel
+constexpr int kRing = 8;                   // panels in flight
+constexpr int kQBytes = DQ / 64 * PB;      // of one query tile
+constexpr int OFF_RING = 2 * kQBytes, kSmem = OFF_RING + kRing * PB + 1024;
+constexpr int kThreads = 384;              // four service warps, two softmax warpgroups
+constexpr int kServiceRegs = 72, kSoftRegs = 216;  // 128 x 72 + 256 x 216 = 64,512 = 384 x 168 registers
+constexpr uint32_t kColO = 256;            // S_s at 128 s, O_s at 256 + 128 s
+constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr float kLazy = 8.f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kStatusExpired = 7;
+constexpr int kBuckets = 1024;
 
-__global__ void __launch_bounds__(kRows * 32) latent_prefill_kernel(LatentPrefillArgs a)
+enum Order { kHeadsFirst = 0, kTokensFirst = 1, kOneHead = 2 };  // (x, head, token), (x, token, head), (x, 0, token)
+
+struct Params {
+    LatentPrefillArgs a;
+    float scale_log2;
+    int32_t kn_order, v_order;  // of the map's coordinates: Order
+    int32_t *status, *n_blocks;
+    int2 *table;         // [max_blocks] (sequence, block of the sequence)
+    int32_t *seq_off;    // [num_seqs + 1] blocks before each sequence
+    int64_t max_blocks;
+};
+
+struct Maps {
+    CUtensorMap q, kn, kr, v;
+};
+
+__device__ __forceinline__ int64_t clamp64(int64_t x, int64_t most) { return x < 0 ? 0 : x > most ? most : x; }
+
+// One block's sizes, from offsets held to the tensors' extents.
+struct Item {
+    int64_t q0, k0;        // first query row of the block, first key of the sequence
+    int32_t nk, n;         // keys of the sequence; key tiles of the block
+    int32_t rows0, rows1;  // valid queries of each query tile
+    int32_t see0;          // keys that the block's first query sees (may be negative)
+    int32_t tiles0, tiles1;
+
+    __device__ void load(const LatentPrefillArgs &a, int64_t b, int64_t blk)
+    {
+        const int64_t qb = clamp64(a.cu_q[b], a.total_q), qe = clamp64(a.cu_q[b + 1], a.total_q);
+        const int64_t kb = clamp64(a.cu_k[b], a.total_k), ke = clamp64(a.cu_k[b + 1], a.total_k);
+        const int32_t nq = static_cast<int32_t>(qe > qb ? qe - qb : 0), r0 = static_cast<int32_t>(blk * kBlock);
+        nk = static_cast<int32_t>(ke > kb ? ke - kb : 0);
+        k0 = kb;
+        q0 = qb + r0;
+        see0 = r0 + nk - nq + 1;
+        rows0 = static_cast<int32_t>(clamp64(nq - r0, T));
+        rows1 = static_cast<int32_t>(clamp64(nq - r0 - T, T));
+        tiles0 = tiles_of(see0, rows0);
+        tiles1 = tiles_of(see0 + T, rows1);
+        n = tiles0 > tiles1 ? tiles0 : tiles1;
+    }
+    // the tile's last query sees the most
+    static __device__ int32_t tiles_of(int32_t see, int32_t rows) { return rows > 0 && see + rows > 1 ? (see + rows - 2) / T + 1 : 0; }
+    __device__ int32_t rows(int s) const { return s ? rows1 : rows0; }
+    __device__ int32_t tiles(int s) const { return s ? tiles1 : tiles0; }
+    __device__ int32_t see(int s) const { return see0 + s * T; }
+};
+
+__device__ __forceinline__ bool elect_one()
 {
-    __shared__ __nv_bfloat16 ks[kTile][D + 2], vs[kTile][DV], qs[kRows][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = blockIdx.y;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows, i = first + warp;
-    auto seq_of = [&](int64_t t) {  // the sequence b with cu_q[b] <= t < cu_q[b + 1]
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r)::"memory");
+    return r != 0;
+}
+
+__host__ __device__ constexpr int64_t blocks_bound(int64_t total_q, int64_t num_seqs) { return total_q / kBlock + num_seqs; }
+
+// ------------------------------------------------------------------ the plan --
+__global__ void __launch_bounds__(1024) plan_kernel(Params p)
+{
+    __shared__ int32_t hist[kBuckets], sums[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const LatentPrefillArgs &a = p.a;
+    auto scan = [&](int32_t x, int32_t *total) {  // exclusive prefix over the CTA
+        int32_t s = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = s;
+        __syncthreads();
+        int32_t before = 0, all = 0;
+        for (int w = 0; w < 32; ++w) {
+            before += w < warp ? sums[w] : 0;
+            all += sums[w];
+        }
+        *total = all;
+        return before + s - x;
+    };
+    if (tid == 0) *p.status = 0;
+    hist[tid] = 0;
+    int32_t base = 0;
+    for (int64_t b0 = 0; b0 < a.num_seqs; b0 += 1024) {
+        const int64_t b = b0 + tid;
+        int32_t nb = 0;
+        if (b < a.num_seqs) {
+            const int64_t n = clamp64(a.cu_q[b + 1], a.total_q) - clamp64(a.cu_q[b], a.total_q);
+            nb = n > 0 ? static_cast<int32_t>((n + kBlock - 1) / kBlock) : 0;
+        }
+        int32_t total;
+        const int32_t at = base + scan(nb, &total);
+        if (b < a.num_seqs) p.seq_off[b] = at;
+        base += total;
+    }
+    // more blocks than the bound only if the offsets are not what the contract says
+    const int32_t blocks = base < p.max_blocks ? base : static_cast<int32_t>(p.max_blocks);
+    if (tid == 0) *p.n_blocks = blocks;
+    __syncthreads();
+    auto locate = [&](int32_t i, int2 *e) {
         int64_t lo = 0, hi = a.num_seqs;
         while (lo + 1 < hi) {
             const int64_t mid = (lo + hi) >> 1;
-            if (a.cu_q[mid] <= t) lo = mid;
+            if (p.seq_off[mid] <= i) lo = mid;
             else hi = mid;
         }
-        return lo;
+        *e = make_int2(static_cast<int>(lo), i - p.seq_off[lo]);
+        Item it;
+        it.load(a, e->x, e->y);
+        return it.n < kBuckets ? kBuckets - 1 - it.n : 0;  // longest first
     };
-    const int64_t last = first + kRows < a.total_q ? first + kRows : a.total_q;
-    const int64_t mine = i < a.total_q ? seq_of(i) : -1;
-    if (i < a.total_q) {
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + (i * a.h + head) * D;
-        for (int e = lane; e < D; e += 32) qs[warp][e] = q[e];
+    int2 e;
+    for (int32_t i = tid; i < blocks; i += 1024) atomicAdd(&hist[locate(i, &e)], 1);
+    __syncthreads();
+    int32_t total;
+    const int32_t first = scan(hist[tid], &total);
+    __syncthreads();
+    hist[tid] = first;
+    __syncthreads();
+    // the order within a bucket is open: it decides which CTA takes a block, not what it computes
+    for (int32_t i = tid; i < blocks; i += 1024) {
+        const int bucket = locate(i, &e);
+        p.table[atomicAdd(&hist[bucket], 1)] = e;
     }
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t b = seq_of(first); b <= seq_of(last - 1); ++b) {  // the CTA's queries may belong to several sequences
-        const int64_t k0 = a.cu_k[b], nk = a.cu_k[b + 1] - k0, nq = a.cu_q[b + 1] - a.cu_q[b];
-        const int64_t seen = mine == b ? i - a.cu_q[b] + nk - nq + 1 : 0;
-        for (int64_t t0 = 0; t0 < nk; t0 += kTile) {
-            __syncthreads();
-            for (int j = warp; j < kTile; j += kRows) {
-                const int64_t t = k0 + t0 + j;
-                const bool ok = t0 + j < nk && t < a.total_k;
-                const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(a.k_nope) + t * a.kn_token + head * a.kn_head;
-                const __nv_bfloat16 *kr = static_cast<const __nv_bfloat16 *>(a.k_rope) + t * a.kr_token;
-                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + t * a.v_token + head * a.v_head;
-                const __nv_bfloat16 zero = __float2bfloat16_rn(0.f);
-                for (int e = lane; e < D; e += 32) ks[j][e] = !ok ? zero : e < DN ? kn[e] : kr[e - DN];
-                for (int e = lane; e < DV; e += 32) vs[j][e] = ok ? v[e] : zero;
-            }
-            __syncthreads();
-            float z = 0.f;
-            for (int e = 0; e < D; ++e) z += __bfloat162float(qs[warp][e]) * __bfloat162float(ks[lane][e]);
-            z = t0 + lane < seen ? z * a.scale : -INFINITY;
-            float mx = z;
-            for (int s = 16; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-            mx = fmaxf(mx, m);
-            const float base = mx == -INFINITY ? 0.f : mx;
-            const float p = expf(z - base), c = expf(m - base);
-            float sum = p;
-            for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-            l = l * c + sum;
-            m = mx;
+}
+
+// ------------------------------------------------------------------ the kernel --
+struct Bars {
+    uint64_t full[kRing], empty[kRing], q_full[2], q_free[2], s[2], p[2], o[2], drain;
+};
+
+__global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, const __grid_constant__ Maps maps)
+{
+    extern __shared__ char smem_raw[];
+    char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) Bars bar;
+    __shared__ uint32_t tmem_base;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
+
+    if (warp == 2) {
+        tc::tmem_alloc(&tmem_base, 512);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int j = 0; j < kRing; ++j) mbar_init(&bar.full[j], 1), mbar_init(&bar.empty[j], 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar.q_full[s], 1), mbar_init(&bar.q_free[s], 1), mbar_init(&bar.s[s], 1);
+            mbar_init(&bar.p[s], T), mbar_init(&bar.o[s], 1);
+        }
+        mbar_init(&bar.drain, 1);
+        fence_mbar_init();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_base;
+    const int32_t H = p.a.h;
+    const int64_t items = static_cast<int64_t>(*p.n_blocks) * H;
+
+    bool gave_up = false;
+    auto wait = [&](uint64_t *b, uint32_t parity) {
+        if (!gave_up && !mbar_wait(b, parity, kWaitLimit)) {
+            gave_up = true;
+            atomicExch(p.status, kStatusExpired);
+        }
+        return !gave_up;
+    };
+    auto all_wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kServiceRegs) : "memory");
+        if (warp == 0) {
+            // ------------------------------------------------------------ copies
+            uint32_t k = 0, loads0 = 0, loads1 = 0;  // panels, query tiles so far
+            auto query = [&](int s, uint32_t &loads, const Item &it, int head) {
+                if (it.tiles(s) == 0) return true;
+                if (loads > 0 && !all_wait(&bar.q_free[s], (loads - 1) & 1)) return false;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&bar.q_full[s], kQBytes);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] *= c;
-            for (int j = 0; j < kTile; ++j) {
-                const float w = __shfl_sync(0xffffffffu, p, j);
-                if (w != 0.f)  // a key that is not seen adds nothing, whatever its value holds
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] += w * __bfloat162float(vs[j][lane + 32 * e]);
+                    for (int u = 0; u < DQ / 64; ++u)
+                        tma_load_3d(smem + s * kQBytes + u * PB, &maps.q, 64 * u, head, static_cast<int>(it.q0) + s * T, &bar.q_full[s]);
+                }
+                __syncwarp();
+                ++loads;
+                return true;
+            };
+            bool ok = true;
+            for (int64_t idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
+                const int2 e = p.table[idx / H];
+                const int head = static_cast<int>(idx % H);
+                Item it;
+                it.load(p.a, e.x, e.y);
+                if (!(ok = query(0, loads0, it, head))) break;
+                for (int32_t j = 0; j < it.n && ok; ++j) {
+                    const int tok = static_cast<int>(it.k0) + j * T;
+                    for (int u = 0; u < 5; ++u, ++k) {
+                        if (j == 0 && u == 3 && !(ok = query(1, loads1, it, head))) break;
+                        const int slot = k % kRing;
+                        if (!(ok = all_wait(&bar.empty[slot], ((k / kRing) & 1) ^ 1))) break;
+                        if (elect_one()) {
+                            char *dst = smem + OFF_RING + slot * PB;
+                            mbar_arrive_expect_tx(&bar.full[slot], PB);
+                            if (u == 2) {
+                                tma_load_3d(dst, &maps.kr, 0, 0, tok, &bar.full[slot]);
+                            } else {
+                                const int order = u > 2 ? p.v_order : p.kn_order, x = 64 * (u > 2 ? u - 3 : u);
+                                const int y = order == kTokensFirst ? tok : order == kOneHead ? 0 : head;
+                                tma_load_3d(dst, u > 2 ? &maps.v : &maps.kn, x, y, order == kTokensFirst ? head : tok, &bar.full[slot]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
             }
+            if (!ok) {  // gave up: the copies in flight land before the CTA ends
+                for (uint32_t e = k > kRing ? k - kRing : 0; e < k; ++e) mbar_wait(&bar.full[e % kRing], (e / kRing) & 1, kWaitLimit);
+                if (loads0 > 0) mbar_wait(&bar.q_full[0], (loads0 - 1) & 1, kWaitLimit);
+                if (loads1 > 0) mbar_wait(&bar.q_full[1], (loads1 - 1) & 1, kWaitLimit);
+            }
+        } else if (warp == 1) {
+            // -------------------------------------------------------------- MMAs
+            constexpr uint32_t kIdS = tc::idesc_bf16(T, T, false), kIdO = tc::idesc_bf16(T, 64, true);
+            const uint32_t base = smem_u32(smem);
+            const uint64_t q_desc = tc::sdesc_sw128(base, 16, 1024), ring_desc = tc::sdesc_sw128(base + OFF_RING, 16, 1024);
+            uint32_t k0 = 0, loads0 = 0, loads1 = 0, pvs0 = 0, pvs1 = 0;  // panels of the items before; query tiles, second products
+            bool ok = true;
+            for (int64_t idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
+                const int2 e = p.table[idx / H];
+                Item it;
+                it.load(p.a, e.x, e.y);
+                const int t0 = it.tiles0, t1 = it.tiles1;
+                // S_s of key tile j; the last query tile that uses the panels hands them back
+                auto first = [&](int s, int j, uint32_t &loads) {
+                    const uint32_t k = k0 + 5 * j;
+                    if (j == 0 && !all_wait(&bar.q_full[s], loads++ & 1)) return false;
+                    for (int u = 0; u < 3; ++u)
+                        if (!all_wait(&bar.full[(k + u) % kRing], ((k + u) / kRing) & 1)) return false;
+                    tc::fence_after_sync();
+                    const bool free_k = s == 1 || j >= t1, free_q = j + 1 == (s ? t1 : t0);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int u = 0; u < 3; ++u) {
+                            const uint64_t a = q_desc + ((s * kQBytes + u * PB) >> 4), b = ring_desc + ((k + u) % kRing) * (PB >> 4);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                tc::mma_bf16(tmem + 128 * s, a + 2 * ks, b + 2 * ks, kIdS, u > 0 || ks > 0 ? 1u : 0u);
+                        }
+                        tc::commit(&bar.s[s]);
+                        if (free_k)
+                            for (int u = 0; u < 3; ++u) tc::commit(&bar.empty[(k + u) % kRing]);
+                        if (free_q) tc::commit(&bar.q_free[s]);
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                // O_s += P_s V of key tile j
+                auto second = [&](int s, int j, uint32_t &pvs) {
+                    const uint32_t k = k0 + 5 * j + 3;
+                    if (!all_wait(&bar.p[s], pvs++ & 1)) return false;
+                    for (int u = 0; u < 2; ++u)
+                        if (!all_wait(&bar.full[(k + u) % kRing], ((k + u) / kRing) & 1)) return false;
+                    tc::fence_after_sync();
+                    const bool free_v = s == 1 || j >= t1;
+                    const int halves = (s ? t1 : t0) == 1 ? 2 : 1;  // what the rounding left off, too
+                    if (elect_one()) {
+                        for (int half = 0; half < halves; ++half)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const uint64_t b = ring_desc + ((k + u) % kRing) * (PB >> 4);
+#pragma unroll
+                                for (int ks = 0; ks < 8; ++ks)
+                                    tc::mma_bf16_ts(tmem + kColO + 128 * s + 64 * u, tmem + 128 * s + 64 * half + 8 * ks, b + 128 * ks,
+                                                    kIdO, j > 0 || half > 0 || ks > 0 ? 1u : 0u);
+                            }
+                        tc::commit(&bar.o[s]);
+                        if (free_v)
+                            for (int u = 0; u < 2; ++u) tc::commit(&bar.empty[(k + u) % kRing]);
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                if (t0 > 0) ok = first(0, 0, loads0);
+                if (t1 > 0 && ok) ok = first(1, 0, loads1);
+                for (int j = 0; j < it.n && ok; ++j) {
+                    if (j < t0) ok = second(0, j, pvs0) && (j + 1 >= t0 || first(0, j + 1, loads0));
+                    if (j < t1 && ok) ok = second(1, j, pvs1) && (j + 1 >= t1 || first(1, j + 1, loads1));
+                }
+                k0 += 5 * it.n;
+            }
+            if (elect_one()) tc::commit(&bar.drain);  // everything issued has completed before tensor memory is given back
+            mbar_wait(&bar.drain, 0, kWaitLimit);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs) : "memory");
+        // ------------------------------------------------------- softmax, epilogue
+        const int s = (warp - 4) >> 2, row = tid & 127;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        const uint32_t ts = tl + 128 * s, to = tl + kColO + 128 * s;
+        uint32_t k0 = 0, steps = 0;  // panels of the items before; key tiles so far (of this query tile)
+        for (int64_t idx = blockIdx.x; idx < items; idx += gridDim.x) {
+            const int2 e = p.table[idx / H];
+            const int head = static_cast<int>(idx % H);
+            Item it;
+            it.load(p.a, e.x, e.y);
+            const int32_t nt = it.tiles(s), limit = row < it.rows(s) ? it.see(s) + row : 0;  // keys that this row sees
+            float m = -INFINITY, l = 0.f, lr = 0.f;
+            // a thread that gave up goes on without waiting
+            for (int32_t j = 0; j < nt; ++j, ++steps) {
+                wait(&bar.s[s], steps & 1);
+                tc::fence_after_sync();
+                float z[T];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, *reinterpret_cast<uint32_t (*)[32]>(&z[32 * c]));
+                tc::wait_ld();
+                const int32_t left = limit - j * T;  // of this tile's keys, those before `left`
+                if (__any_sync(0xffffffffu, left < T)) {
+#pragma unroll
+                    for (int c = 0; c < T; ++c) z[c] = c < left ? z[c] : -INFINITY;
+                }
+                float mx = z[0];
+#pragma unroll
+                for (int c = 1; c + 1 < T; c += 2) mx = fmaxf(mx, fmaxf(z[c], z[c + 1]));
+                mx = fmaxf(mx, z[T - 1]) * p.scale_log2;
+                const bool grew = mx > m + kLazy && m > -INFINITY;
+                if (__any_sync(0xffffffffu, grew)) {
+                    const float f = grew ? ex2_approx(m - mx) : 1.f;
+                    l *= f;
+                    lr *= f;
+                    wait(&bar.o[s], (steps - 1) & 1);  // grew only behind the first tile of the item
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < DV; c += 32) {
+                        uint32_t o[32];
+                        tc::ld32(to + c, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+                        tc::st32(to + c, o);
+                    }
+                }
+                if (grew || m == -INFINITY) m = mx;
+                const float base = m == -INFINITY ? 0.f : m;
+                const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
+                float2 sum = make_float2(0.f, 0.f), sum_r = make_float2(0.f, 0.f);
+                // scores -> probabilities, rounded, into S_s; LOW: what the rounding left off stays in z
+                auto probabilities = [&](auto low) {
+#pragma unroll
+                    for (int c = 0; c < T; c += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            float2 x = fma2(make_float2(z[c + 2 * q], z[c + 2 * q + 1]), sc, nb);
+                            x.x = ex2_approx(x.x);
+                            x.y = ex2_approx(x.y);
+                            sum = add2(sum, x);
+                            pk[q] = pack_bf16x2(x.x, x.y);
+                            const float2 r = make_float2(bf16_lo(pk[q]), bf16_hi(pk[q]));
+                            if constexpr (decltype(low)::value) {
+                                z[c + 2 * q] = x.x - r.x;
+                                z[c + 2 * q + 1] = x.y - r.y;
+                            } else {
+                                sum_r = add2(sum_r, r);
+                            }
+                        }
+                        tc::st16(ts + c / 2, pk);
+                    }
+                };
+                if (nt == 1) {
+                    probabilities(std::true_type{});
+#pragma unroll
+                    for (int c = 0; c < T; c += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) pk[q] = pack_bf16x2(z[c + 2 * q], z[c + 2 * q + 1]);
+                        tc::st16(ts + 64 + c / 2, pk);
+                    }
+                    sum_r = sum;
+                } else {
+                    probabilities(std::false_type{});
+                }
+                l += sum.x + sum.y;
+                lr += sum_r.x + sum_r.y;
+                // value rows behind the sequence's last key: whatever they hold must not meet P = 0
+                const int32_t keys = it.nk - j * T;
+                if (keys < T && (s == 0 || j >= it.tiles0)) {
+                    const uint32_t k = k0 + 5 * j + 3;
+                    for (int u = 0; u < 2; ++u) wait(&bar.full[(k + u) % kRing], ((k + u) / kRing) & 1);
+                    for (int q = row; q < (T - keys) * 16; q += T) {
+                        const int u = q >> 3 & 1, r = keys + (q >> 4);
+                        *reinterpret_cast<uint4 *>(smem + OFF_RING + (k + u) % kRing * PB + r * 128 + (q & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc::wait_st();
+                tc::fence_before_sync();
+                mbar_arrive(&bar.p[s]);
+            }
+            const int64_t out_row = (it.q0 + s * T + row) * H + head;
+            if (nt > 0) {
+                wait(&bar.o[s], (steps - 1) & 1);
+                tc::fence_after_sync();
+            }
+            const float inv = lr > 0.f ? 1.f / lr : 0.f;
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.a.out) + out_row * DV);
+#pragma unroll
+            for (int c = 0; c < DV; c += 32) {
+                uint32_t o[32];
+                if (nt > 0) {
+                    tc::ld32(to + c, o);
+                    tc::wait_ld();
+                }
+                if (row < it.rows(s)) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            w[r] = inv > 0.f ? pack_bf16x2(__uint_as_float(o[8 * q + 2 * r]) * inv, __uint_as_float(o[8 * q + 2 * r + 1]) * inv) : 0u;
+                        out[c / 8 + q] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            tc::fence_before_sync();
+            if (row < it.rows(s) && p.a.lse != nullptr) p.a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            k0 += 5 * it.n;
         }
     }
-    if (i >= a.total_q) return;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (i * a.h + head) * DV;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) out[lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
-    if (lane == 0 && a.lse != nullptr) a.lse[i * a.h + head] = l > 0.f ? m + logf(l) : -INFINITY;
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 2) tc::tmem_dealloc(tmem, 512);
+}
+
+// Boxes of 64 columns x 128 tokens of a bf16 [tokens][heads][cols] tensor (strides in elements), 128-byte
+// swizzle, zeros outside.  Of heads and tokens the one with the smaller stride comes first; heads that
+// share their rows (stride 0) are one head.
+bool encode(CUtensorMap *m, const void *base, int64_t cols, int64_t heads, int64_t tokens, int64_t s_head, int64_t s_token,
+            int32_t *order)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = prefill::tensor_map_encoder();
+    if (fn == nullptr) return false;
+    if (heads == 1 || s_head == 0) heads = 1, s_head = cols;  // a stride of a size-one dimension means nothing
+    if (tokens == 1) s_token = heads * s_head;
+    const bool tf = s_head > s_token;
+    *order = heads == 1 ? kOneHead : tf ? kTokensFirst : kHeadsFirst;
+    const bool swap = *order == kTokensFirst;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(swap ? tokens : heads),
+                                static_cast<cuuint64_t>(swap ? heads : tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(swap ? s_token : s_head) * 2, static_cast<cuuint64_t>(swap ? s_head : s_token) * 2};
+    const cuuint32_t box[3] = {64, swap ? static_cast<cuuint32_t>(T) : 1u, swap ? 1u : static_cast<cuuint32_t>(T)}, elem[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
-size_t latent_prefill_workspace(int64_t, int64_t, int32_t) { return 256; }
+size_t latent_prefill_workspace(int64_t total_q, int64_t num_seqs, int32_t)
+{
+    const size_t n = static_cast<size_t>(blocks_bound(total_q, num_seqs));
+    return 256 + n * sizeof(int2) + static_cast<size_t>(num_seqs + 1) * 4;
+}
 
 cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st)
 {
-    cudaError_t e = cudaMemsetAsync(a.workspace, 0, 4, st);
+    Params p{};
+    p.a = a;
+    p.scale_log2 = a.scale * kLog2e;
+    p.max_blocks = blocks_bound(a.total_q, a.num_seqs);
+    p.status = static_cast<int32_t *>(a.workspace);
+    p.n_blocks = p.status + 1;
+    p.table = reinterpret_cast<int2 *>(static_cast<char *>(a.workspace) + 256);
+    p.seq_off = reinterpret_cast<int32_t *>(p.table + p.max_blocks);
+    Maps maps{};
+    int32_t plain;  // q's heads lie within a token (or there is one), k_rope has one
+    if (!encode(&maps.q, a.q, DQ, a.h, a.total_q, DQ, static_cast<int64_t>(a.h) * DQ, &plain)) return cudaErrorInvalidValue;
+    if (a.total_k > 0 && (!encode(&maps.kn, a.k_nope, DN, a.h, a.total_k, a.kn_head, a.kn_token, &p.kn_order) ||
+                          !encode(&maps.v, a.v, DV, a.h, a.total_k, a.v_head, a.v_token, &p.v_order) ||
+                          !encode(&maps.kr, a.k_rope, DR, 1, a.total_k, DR, a.kr_token, &plain)))
+        return cudaErrorInvalidValue;
+    plan_kernel<<<1, 1024, 0, st>>>(p);
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>((a.total_q + kRows - 1) / kRows), static_cast<unsigned>(a.h));
-    latent_prefill_kernel<<<grid, kRows * 32, 0, st>>>(a);
+    e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    // the register split (setmaxnreg) needs a launch with exactly 168 registers a thread
+    cudaFuncAttributes at;
+    if ((e = cudaFuncGetAttributes(&at, latent_prefill_kernel)) != cudaSuccess) return e;
+    if (at.numRegs != 168) return cudaErrorInvalidConfiguration;
+    const int64_t items = p.max_blocks * a.h, sms = sm_count();
+    latent_prefill_kernel<<<static_cast<unsigned>(items < sms ? items : sms), kThreads, kSmem, st>>>(p, maps);
     return cudaGetLastError();
 }
 
