@@ -612,7 +612,8 @@ int kda_latent_decode(const void *q, int32_t io_dtype, int64_t batch, int32_t L,
  * Built: dn == dv == 128, dr == 64, bf16.  Errors as kda_latent_decode
  * (_SHAPE: negative strides, a token stride of 0 with several tokens; _RANGE:
  * scale not positive and finite, total_q or total_k >= 2^31 - 256, num_seqs >=
- * 2^24, h > 1024, a stride of 2^38 elements or more).
+ * 2^24, h > 1024, (total_q / 256 + num_seqs) * h >= 2^31, a stride of 2^38
+ * elements or more).
  * total_q == 0 launches nothing.
  * ---------------------------------------------------------------------- */
 size_t kda_latent_prefill_workspace_size(int64_t total_q, int64_t num_seqs, int32_t h);

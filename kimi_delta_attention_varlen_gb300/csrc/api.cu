@@ -493,7 +493,9 @@ int kda_latent_prefill(const void *q, int32_t io_dtype, const void *k_nope, int6
         return KDA_ERR_SHAPE;
     if (dn != 128 || dv != 128 || dr != 64) return KDA_ERR_UNSUPPORTED;
     const int64_t most = (INT64_C(1) << 31) - 256;
-    if (!valid_scale(scale) || total_q >= most || total_k >= most || num_seqs >= (1 << 24) || h > 1024) return KDA_ERR_RANGE;
+    if (!valid_scale(scale) || total_q >= most || total_k >= most || num_seqs >= (1 << 24) || h > 1024 ||
+        (total_q / 256 + num_seqs) * h >= (INT64_C(1) << 31))  // (block of 256 queries, head) pairs
+        return KDA_ERR_RANGE;
     const int64_t strides[] = {kn_token, kn_head, kr_token, v_token, v_head};
     for (int64_t s : strides)
         if (s >= (INT64_C(1) << 38)) return KDA_ERR_RANGE;

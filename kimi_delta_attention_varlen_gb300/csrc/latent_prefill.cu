@@ -11,9 +11,11 @@
 //   O_s  += P_s V       M = 128, N = 64 twice, K = 128, P_s in tensor memory
 // Tensor memory holds S_0, S_1, O_0, O_1 (128 columns each); P_s (bf16) overlays S_s.  While the
 // softmax of one tile runs, the tensor cores do the other tile's two products.  Warps: one issues the
-// TMA copies, one the MMAs, two warpgroups do the softmax (one row a thread) and the epilogues.
-// Key and value panels (128 tokens x 64, 16 KB, 128-byte swizzle) pass through one ring: per key tile
-// three key panels (K-major B), two value panels (MN-major B).
+// TMA copies, one the MMAs of each query tile, two warpgroups do the softmax (one row a thread) and the epilogues.
+// Key and value panels (128 tokens x 64, 16 KB, 128-byte swizzle) pass through one ring of eight: per
+// key tile three key panels (K-major B), then two value panels (MN-major B).  The probabilities are
+// handed over in two halves, and the sums are formed behind them, so that they are off the path from
+// S_s to O_s.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the last rescale.  The
 // probabilities are rounded to bf16, the tensor cores' operand type; the output is normalised by the
@@ -44,7 +46,7 @@ constexpr int kRing = 8;                   // panels in flight
 constexpr int kQBytes = DQ / 64 * PB;      // of one query tile
 constexpr int OFF_RING = 2 * kQBytes, kSmem = OFF_RING + kRing * PB + 1024;
 constexpr int kThreads = 384;              // four service warps, two softmax warpgroups
-constexpr int kServiceRegs = 72, kSoftRegs = 216;  // 128 x 72 + 256 x 216 = 64,512 = 384 x 168 registers
+constexpr int kServiceRegs = 88, kSoftRegs = 208;  // 128 x 88 + 256 x 208 = 64,512 = 384 x 168 registers
 constexpr uint32_t kColO = 256;            // S_s at 128 s, O_s at 256 + 128 s
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kLazy = 8.f;
@@ -72,23 +74,24 @@ __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t most) { return x <
 
 // One block's sizes, from offsets held to the tensors' extents.
 struct Item {
-    int64_t q0, k0;        // first query row of the block, first key of the sequence
+    int32_t q0, k0;        // first query row of the block, first key of the sequence
     int32_t nk, n;         // keys of the sequence; key tiles of the block
     int32_t rows0, rows1;  // valid queries of each query tile
     int32_t see0;          // keys that the block's first query sees (may be negative)
     int32_t tiles0, tiles1;
 
-    __device__ void load(const LatentPrefillArgs &a, int64_t b, int64_t blk)
+    __device__ static int32_t hold(int32_t x, int32_t most) { return x < 0 ? 0 : x > most ? most : x; }
+    __device__ void load(const LatentPrefillArgs &a, int32_t b, int32_t blk)
     {
-        const int64_t qb = clamp64(a.cu_q[b], a.total_q), qe = clamp64(a.cu_q[b + 1], a.total_q);
-        const int64_t kb = clamp64(a.cu_k[b], a.total_k), ke = clamp64(a.cu_k[b + 1], a.total_k);
-        const int32_t nq = static_cast<int32_t>(qe > qb ? qe - qb : 0), r0 = static_cast<int32_t>(blk * kBlock);
-        nk = static_cast<int32_t>(ke > kb ? ke - kb : 0);
+        const int32_t tq = static_cast<int32_t>(a.total_q), tk = static_cast<int32_t>(a.total_k);
+        const int32_t qb = hold(a.cu_q[b], tq), qe = hold(a.cu_q[b + 1], tq), kb = hold(a.cu_k[b], tk), ke = hold(a.cu_k[b + 1], tk);
+        const int32_t nq = qe > qb ? qe - qb : 0, r0 = blk * kBlock;
+        nk = ke > kb ? ke - kb : 0;
         k0 = kb;
         q0 = qb + r0;
         see0 = r0 + nk - nq + 1;
-        rows0 = static_cast<int32_t>(clamp64(nq - r0, T));
-        rows1 = static_cast<int32_t>(clamp64(nq - r0 - T, T));
+        rows0 = hold(nq - r0, T);
+        rows1 = hold(nq - r0 - T, T);
         tiles0 = tiles_of(see0, rows0);
         tiles1 = tiles_of(see0 + T, rows1);
         n = tiles0 > tiles1 ? tiles0 : tiles1;
@@ -106,6 +109,11 @@ __device__ __forceinline__ bool elect_one()
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r)::"memory");
     return r != 0;
 }
+
+// A value that is the same in all lanes, in a form in which the compiler knows it: branches and
+// addresses that depend on it then stay uniform, and the MMA takes its descriptors from uniform registers
+// (with descriptors from vector registers an MMA took about 100 cycles to issue).
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __host__ __device__ constexpr int64_t blocks_bound(int64_t total_q, int64_t num_seqs) { return total_q / kBlock + num_seqs; }
 
@@ -181,7 +189,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(Params p)
 
 // ------------------------------------------------------------------ the kernel --
 struct Bars {
-    uint64_t full[kRing], empty[kRing], q_full[2], q_free[2], s[2], p[2], o[2], drain;
+    // by parity of the key tile: its key panels and value panels, loaded and handed back
+    uint64_t k_full[2][3], k_free[2], v_full[2], v_free[2];  // k_full: by panel
+    uint64_t q_full[2], q_free[2], s[2], p[2][2], o[2], drain[2];  // by query tile; p: by half of the keys
 };
 
 __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, const __grid_constant__ Maps maps)
@@ -193,25 +203,24 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
 
-    if (warp == 2) {
+    if (warp == 3) {
         tc::tmem_alloc(&tmem_base, 512);
         tc::tmem_relinquish();
     }
     if (tid == 0) {
-        for (int j = 0; j < kRing; ++j) mbar_init(&bar.full[j], 1), mbar_init(&bar.empty[j], 1);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&bar.q_full[s], 1), mbar_init(&bar.q_free[s], 1), mbar_init(&bar.s[s], 1);
-            mbar_init(&bar.p[s], T), mbar_init(&bar.o[s], 1);
+            mbar_init(&bar.k_full[s][0], 1), mbar_init(&bar.k_full[s][1], 1), mbar_init(&bar.k_full[s][2], 1), mbar_init(&bar.k_free[s], 2), mbar_init(&bar.v_full[s], 1), mbar_init(&bar.v_free[s], 2);  // handed back by both query tiles
+            mbar_init(&bar.drain[s], 1);
+            mbar_init(&bar.q_full[s], 1), mbar_init(&bar.q_free[s], 1), mbar_init(&bar.s[s], 1), mbar_init(&bar.o[s], 1);
+            mbar_init(&bar.p[s][0], T), mbar_init(&bar.p[s][1], T);
         }
-        mbar_init(&bar.drain, 1);
         fence_mbar_init();
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = tmem_base;
-    const int32_t H = p.a.h;
-    const int64_t items = static_cast<int64_t>(*p.n_blocks) * H;
+    const uint32_t tmem = uniform(tmem_base);
+    const int32_t H = p.a.h, items = uniform(*p.n_blocks) * H;  // below 2^31: checked on the host
 
     bool gave_up = false;
     auto wait = [&](uint64_t *b, uint32_t parity) {
@@ -221,13 +230,17 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
         }
         return !gave_up;
     };
-    auto all_wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+    // by a whole warp: the test that usually passes first, the bounded wait behind it
+    auto all_wait = [&](uint64_t *b, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_test(b, parity))) return true;
+        return __all_sync(0xffffffffu, wait(b, parity)) != 0;
+    };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kServiceRegs) : "memory");
         if (warp == 0) {
             // ------------------------------------------------------------ copies
-            uint32_t k = 0, loads0 = 0, loads1 = 0;  // panels, query tiles so far
+            uint32_t g = 0, loads0 = 0, loads1 = 0;  // key tiles, query tiles so far
             auto query = [&](int s, uint32_t &loads, const Item &it, int head) {
                 if (it.tiles(s) == 0) return true;
                 if (loads > 0 && !all_wait(&bar.q_free[s], (loads - 1) & 1)) return false;
@@ -235,117 +248,149 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                     mbar_arrive_expect_tx(&bar.q_full[s], kQBytes);
 #pragma unroll
                     for (int u = 0; u < DQ / 64; ++u)
-                        tma_load_3d(smem + s * kQBytes + u * PB, &maps.q, 64 * u, head, static_cast<int>(it.q0) + s * T, &bar.q_full[s]);
+                        tma_load_3d(smem + s * kQBytes + u * PB, &maps.q, 64 * u, head, it.q0 + s * T, &bar.q_full[s]);
                 }
                 __syncwarp();
                 ++loads;
                 return true;
             };
             bool ok = true;
-            for (int64_t idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
+            for (int32_t idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
                 const int2 e = p.table[idx / H];
-                const int head = static_cast<int>(idx % H);
+                const int head = idx % H;
                 Item it;
                 it.load(p.a, e.x, e.y);
                 if (!(ok = query(0, loads0, it, head))) break;
-                for (int32_t j = 0; j < it.n && ok; ++j) {
-                    const int tok = static_cast<int>(it.k0) + j * T;
-                    for (int u = 0; u < 5; ++u, ++k) {
-                        if (j == 0 && u == 3 && !(ok = query(1, loads1, it, head))) break;
-                        const int slot = k % kRing;
-                        if (!(ok = all_wait(&bar.empty[slot], ((k / kRing) & 1) ^ 1))) break;
-                        if (elect_one()) {
-                            char *dst = smem + OFF_RING + slot * PB;
-                            mbar_arrive_expect_tx(&bar.full[slot], PB);
-                            if (u == 2) {
-                                tma_load_3d(dst, &maps.kr, 0, 0, tok, &bar.full[slot]);
-                            } else {
-                                const int order = u > 2 ? p.v_order : p.kn_order, x = 64 * (u > 2 ? u - 3 : u);
-                                const int y = order == kTokensFirst ? tok : order == kOneHead ? 0 : head;
-                                tma_load_3d(dst, u > 2 ? &maps.v : &maps.kn, x, y, order == kTokensFirst ? head : tok, &bar.full[slot]);
-                            }
+                for (int32_t j = 0; j < it.n; ++j, ++g) {
+                    // panel i of tile g lies in slot (5 g + i) % 8: its first key panel where tile g - 2's last one was (waited
+                    // for with tile g - 1's values), the others where tile g - 2's values were, its values where tile g - 1's
+                    // first keys were
+                    const int tok = it.k0 + j * T;
+                    char *const ring = smem + OFF_RING;
+                    const int kn_y = p.kn_order == kTokensFirst ? tok : p.kn_order == kOneHead ? 0 : head;
+                    const int kn_z = p.kn_order == kTokensFirst ? head : tok;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&bar.k_full[g & 1][0], PB);
+                        tma_load_3d(ring + 5 * g % kRing * PB, &maps.kn, 0, kn_y, kn_z, &bar.k_full[g & 1][0]);
+                    }
+                    __syncwarp();
+                    if (g > 1 && !(ok = all_wait(&bar.v_free[g & 1], ((g >> 1) & 1) ^ 1))) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&bar.k_full[g & 1][1], PB);
+                        tma_load_3d(ring + (5 * g + 1) % kRing * PB, &maps.kn, 64, kn_y, kn_z, &bar.k_full[g & 1][1]);
+                        mbar_arrive_expect_tx(&bar.k_full[g & 1][2], PB);
+                        tma_load_3d(ring + (5 * g + 2) % kRing * PB, &maps.kr, 0, 0, tok, &bar.k_full[g & 1][2]);
+                    }
+                    __syncwarp();
+                    if (j == 0 && !(ok = query(1, loads1, it, head))) break;
+                    if (g > 0 && !(ok = all_wait(&bar.k_free[(g - 1) & 1], (g - 1) >> 1 & 1))) break;
+                    if (elect_one()) {
+                        const int order = p.v_order, y = order == kTokensFirst ? tok : order == kOneHead ? 0 : head;
+                        const int z = order == kTokensFirst ? head : tok;
+                        mbar_arrive_expect_tx(&bar.v_full[g & 1], 2 * PB);
+                        tma_load_3d(ring + (5 * g + 3) % kRing * PB, &maps.v, 0, y, z, &bar.v_full[g & 1]);
+                        tma_load_3d(ring + (5 * g + 4) % kRing * PB, &maps.v, 64, y, z, &bar.v_full[g & 1]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) {  // gave up: the copies in flight land before the CTA ends
+                // what tile g has under way is not told apart: a wait for what was not begun runs out, bounded like the others
+                for (uint32_t e = g > 0 ? g - 1 : 0; e <= g; ++e) {
+                    for (int u = 0; u < 3; ++u) mbar_wait(&bar.k_full[e & 1][u], e >> 1 & 1, kWaitLimit);
+                    mbar_wait(&bar.v_full[e & 1], e >> 1 & 1, kWaitLimit);
+                }
+                if (loads0 > 0) mbar_wait(&bar.q_full[0], (loads0 - 1) & 1, kWaitLimit);
+                if (loads1 > 0) mbar_wait(&bar.q_full[1], (loads1 - 1) & 1, kWaitLimit);
+            }
+        } else if (warp < 3) {
+            // -------------------------------------------- MMAs of query tile s
+            // One warp a query tile: while one waits, looks at barriers or forms descriptors, the other's products run (with
+            // one warp for both the tensor pipe idled a third of the time behind its serial code).
+            const int s = warp - 1;
+            constexpr uint32_t kIdS = tc::idesc_bf16(T, T, false), kIdO = tc::idesc_bf16(T, 64, true);
+            const uint32_t base = smem_u32(smem), ts = tmem + 128 * s, to = tmem + kColO + 128 * s;
+            const uint64_t q_desc = tc::sdesc_sw128(base + s * kQBytes, 16, 1024), ring_desc = tc::sdesc_sw128(base + OFF_RING, 16, 1024);
+            uint32_t g = 0, loads = 0, pvs = 0;  // key tiles, query tiles, second products so far
+            // S of key tile g, panel by panel as they arrive
+            auto first = [&](uint32_t g, bool free_q) {
+#pragma unroll
+                for (int u = 0; u < 3; ++u) {
+                    if (!all_wait(&bar.k_full[g & 1][u], g >> 1 & 1)) return false;
+                    if (elect_one()) {
+                        const uint64_t a = q_desc + (u * PB >> 4), b = ring_desc + (5 * g + u) % kRing * (PB >> 4);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) tc::mma_bf16(ts, a + 2 * ks, b + 2 * ks, kIdS, u > 0 || ks > 0 ? 1u : 0u);
+                        if (u == 2) {
+                            tc::commit(&bar.s[s]);
+                            tc::commit(&bar.k_free[g & 1]);
+                            if (free_q) tc::commit(&bar.q_free[s]);
                         }
+                    }
+                    __syncwarp();
+                }
+                return true;
+            };
+            // O += P V of key tile g
+            auto second = [&](uint32_t g, bool fresh, bool single) {
+                const uint64_t b0 = ring_desc + (5 * g + 3) % kRing * (PB >> 4), b1 = ring_desc + (5 * g + 4) % kRing * (PB >> 4);
+                if (!all_wait(&bar.v_full[g & 1], g >> 1 & 1) || !all_wait(&bar.p[s][0], pvs & 1)) return false;
+                tc::fence_after_sync();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        tc::mma_bf16_ts(to, ts + 8 * ks, b0 + 128 * ks, kIdO, ks > 0 || !fresh ? 1u : 0u);
+                        tc::mma_bf16_ts(to + 64, ts + 8 * ks, b1 + 128 * ks, kIdO, ks > 0 || !fresh ? 1u : 0u);
+                    }
+                }
+                __syncwarp();
+                if (!all_wait(&bar.p[s][1], pvs++ & 1)) return false;
+                tc::fence_after_sync();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 4; ks < 8; ++ks) {
+                        tc::mma_bf16_ts(to, ts + 8 * ks, b0 + 128 * ks, kIdO, 1u);
+                        tc::mma_bf16_ts(to + 64, ts + 8 * ks, b1 + 128 * ks, kIdO, 1u);
+                    }
+                    if (single) {  // what the rounding left off, too
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks) {
+                            tc::mma_bf16_ts(to, ts + 64 + 8 * ks, b0 + 128 * ks, kIdO, 1u);
+                            tc::mma_bf16_ts(to + 64, ts + 64 + 8 * ks, b1 + 128 * ks, kIdO, 1u);
+                        }
+                    }
+                    tc::commit(&bar.o[s]);
+                    tc::commit(&bar.v_free[g & 1]);
+                }
+                __syncwarp();
+                return true;
+            };
+            bool ok = true;
+            for (int32_t idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
+                const int2 e = p.table[idx / H];
+                Item it;
+                it.load(p.a, e.x, e.y);
+                const int nt = uniform(it.tiles(s)), n = uniform(it.n);
+                if (nt > 0) {
+                    if (!(ok = all_wait(&bar.q_full[s], loads++ & 1))) break;
+                    tc::fence_after_sync();
+                    if (!(ok = first(g, nt == 1))) break;
+                }
+                for (int j = 0; j < n; ++j, ++g) {
+                    if (j < nt) {
+                        if (!(ok = second(g, j == 0, nt == 1))) break;
+                        if (j + 1 < nt && !(ok = first(g + 1, j + 2 == nt))) break;
+                    } else {  // the other query tile's alone: handed back once it is there (then the tile two before is)
+                        if (!(ok = all_wait(&bar.k_full[g & 1][0], g >> 1 & 1))) break;
+                        if (lane == 0) mbar_arrive(&bar.k_free[g & 1]);
+                        if (!(ok = all_wait(&bar.v_full[g & 1], g >> 1 & 1))) break;
+                        if (lane == 0) mbar_arrive(&bar.v_free[g & 1]);
                         __syncwarp();
                     }
                 }
             }
-            if (!ok) {  // gave up: the copies in flight land before the CTA ends
-                for (uint32_t e = k > kRing ? k - kRing : 0; e < k; ++e) mbar_wait(&bar.full[e % kRing], (e / kRing) & 1, kWaitLimit);
-                if (loads0 > 0) mbar_wait(&bar.q_full[0], (loads0 - 1) & 1, kWaitLimit);
-                if (loads1 > 0) mbar_wait(&bar.q_full[1], (loads1 - 1) & 1, kWaitLimit);
-            }
-        } else if (warp == 1) {
-            // -------------------------------------------------------------- MMAs
-            constexpr uint32_t kIdS = tc::idesc_bf16(T, T, false), kIdO = tc::idesc_bf16(T, 64, true);
-            const uint32_t base = smem_u32(smem);
-            const uint64_t q_desc = tc::sdesc_sw128(base, 16, 1024), ring_desc = tc::sdesc_sw128(base + OFF_RING, 16, 1024);
-            uint32_t k0 = 0, loads0 = 0, loads1 = 0, pvs0 = 0, pvs1 = 0;  // panels of the items before; query tiles, second products
-            bool ok = true;
-            for (int64_t idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
-                const int2 e = p.table[idx / H];
-                Item it;
-                it.load(p.a, e.x, e.y);
-                const int t0 = it.tiles0, t1 = it.tiles1;
-                // S_s of key tile j; the last query tile that uses the panels hands them back
-                auto first = [&](int s, int j, uint32_t &loads) {
-                    const uint32_t k = k0 + 5 * j;
-                    if (j == 0 && !all_wait(&bar.q_full[s], loads++ & 1)) return false;
-                    for (int u = 0; u < 3; ++u)
-                        if (!all_wait(&bar.full[(k + u) % kRing], ((k + u) / kRing) & 1)) return false;
-                    tc::fence_after_sync();
-                    const bool free_k = s == 1 || j >= t1, free_q = j + 1 == (s ? t1 : t0);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int u = 0; u < 3; ++u) {
-                            const uint64_t a = q_desc + ((s * kQBytes + u * PB) >> 4), b = ring_desc + ((k + u) % kRing) * (PB >> 4);
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                tc::mma_bf16(tmem + 128 * s, a + 2 * ks, b + 2 * ks, kIdS, u > 0 || ks > 0 ? 1u : 0u);
-                        }
-                        tc::commit(&bar.s[s]);
-                        if (free_k)
-                            for (int u = 0; u < 3; ++u) tc::commit(&bar.empty[(k + u) % kRing]);
-                        if (free_q) tc::commit(&bar.q_free[s]);
-                    }
-                    __syncwarp();
-                    return true;
-                };
-                // O_s += P_s V of key tile j
-                auto second = [&](int s, int j, uint32_t &pvs) {
-                    const uint32_t k = k0 + 5 * j + 3;
-                    if (!all_wait(&bar.p[s], pvs++ & 1)) return false;
-                    for (int u = 0; u < 2; ++u)
-                        if (!all_wait(&bar.full[(k + u) % kRing], ((k + u) / kRing) & 1)) return false;
-                    tc::fence_after_sync();
-                    const bool free_v = s == 1 || j >= t1;
-                    const int halves = (s ? t1 : t0) == 1 ? 2 : 1;  // what the rounding left off, too
-                    if (elect_one()) {
-                        for (int half = 0; half < halves; ++half)
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const uint64_t b = ring_desc + ((k + u) % kRing) * (PB >> 4);
-#pragma unroll
-                                for (int ks = 0; ks < 8; ++ks)
-                                    tc::mma_bf16_ts(tmem + kColO + 128 * s + 64 * u, tmem + 128 * s + 64 * half + 8 * ks, b + 128 * ks,
-                                                    kIdO, j > 0 || half > 0 || ks > 0 ? 1u : 0u);
-                            }
-                        tc::commit(&bar.o[s]);
-                        if (free_v)
-                            for (int u = 0; u < 2; ++u) tc::commit(&bar.empty[(k + u) % kRing]);
-                    }
-                    __syncwarp();
-                    return true;
-                };
-                if (t0 > 0) ok = first(0, 0, loads0);
-                if (t1 > 0 && ok) ok = first(1, 0, loads1);
-                for (int j = 0; j < it.n && ok; ++j) {
-                    if (j < t0) ok = second(0, j, pvs0) && (j + 1 >= t0 || first(0, j + 1, loads0));
-                    if (j < t1 && ok) ok = second(1, j, pvs1) && (j + 1 >= t1 || first(1, j + 1, loads1));
-                }
-                k0 += 5 * it.n;
-            }
-            if (elect_one()) tc::commit(&bar.drain);  // everything issued has completed before tensor memory is given back
-            mbar_wait(&bar.drain, 0, kWaitLimit);
+            if (elect_one()) tc::commit(&bar.drain[s]);  // everything issued has completed before tensor memory is given back
+            mbar_wait(&bar.drain[s], 0, kWaitLimit);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs) : "memory");
@@ -353,10 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
         const int s = (warp - 4) >> 2, row = tid & 127;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const uint32_t ts = tl + 128 * s, to = tl + kColO + 128 * s;
-        uint32_t k0 = 0, steps = 0;  // panels of the items before; key tiles so far (of this query tile)
-        for (int64_t idx = blockIdx.x; idx < items; idx += gridDim.x) {
+        uint32_t g0 = 0, steps = 0;  // key tiles of the items before; key tiles so far (of this query tile)
+        for (int32_t idx = blockIdx.x; idx < items; idx += gridDim.x) {
             const int2 e = p.table[idx / H];
-            const int head = static_cast<int>(idx % H);
+            const int head = idx % H;
             Item it;
             it.load(p.a, e.x, e.y);
             const int32_t nt = it.tiles(s), limit = row < it.rows(s) ? it.see(s) + row : 0;  // keys that this row sees
@@ -398,61 +443,72 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 if (grew || m == -INFINITY) m = mx;
                 const float base = m == -INFINITY ? 0.f : m;
                 const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
+                // value rows behind the sequence's last key: whatever they hold must not meet P = 0 (both query
+                // tiles write these zeros, each before its own product; a second time they change nothing)
+                const int32_t keys = it.nk - j * T;
+                if (keys < T) {
+                    const uint32_t g = g0 + j;
+                    wait(&bar.v_full[g & 1], g >> 1 & 1);
+                    for (int q = row; q < (T - keys) * 16; q += T) {
+                        const int u = q >> 3 & 1, r = keys + (q >> 4);
+                        *reinterpret_cast<uint4 *>(smem + OFF_RING + (5 * g + 3 + u) % kRing * PB + r * 128 + (q & 7) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                // scores -> probabilities, rounded, into S_s; the first 64 keys are handed over first
                 float2 sum = make_float2(0.f, 0.f), sum_r = make_float2(0.f, 0.f);
-                // scores -> probabilities, rounded, into S_s; LOW: what the rounding left off stays in z
-                auto probabilities = [&](auto low) {
+                if (nt > 1) {
+                    uint32_t pk[T / 2];
 #pragma unroll
-                    for (int c = 0; c < T; c += 32) {
-                        uint32_t pk[16];
+                    for (int c = 0; c < T / 2; c += 16) {
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            float2 x = fma2(make_float2(z[c + 2 * q], z[c + 2 * q + 1]), sc, nb);
+                        for (int q = c; q < c + 16; ++q) {
+                            float2 x = fma2(make_float2(z[2 * q], z[2 * q + 1]), sc, nb);
                             x.x = ex2_approx(x.x);
                             x.y = ex2_approx(x.y);
                             sum = add2(sum, x);
                             pk[q] = pack_bf16x2(x.x, x.y);
-                            const float2 r = make_float2(bf16_lo(pk[q]), bf16_hi(pk[q]));
-                            if constexpr (decltype(low)::value) {
-                                z[c + 2 * q] = x.x - r.x;
-                                z[c + 2 * q + 1] = x.y - r.y;
-                            } else {
-                                sum_r = add2(sum_r, r);
-                            }
                         }
-                        tc::st16(ts + c / 2, pk);
+                        tc::st16(ts + c, *reinterpret_cast<uint32_t (*)[16]>(&pk[c]));
+                        if (c == 16) {
+                            tc::wait_st();
+                            tc::fence_before_sync();
+                            mbar_arrive(&bar.p[s][0]);
+                        }
                     }
-                };
-                if (nt == 1) {
-                    probabilities(std::true_type{});
+                    tc::wait_st();
+                    tc::fence_before_sync();
+                    mbar_arrive(&bar.p[s][1]);
+                    // the sum of the rounded weights, while the tensor cores go on
 #pragma unroll
-                    for (int c = 0; c < T; c += 32) {
-                        uint32_t pk[16];
+                    for (int q = 0; q < T / 2; ++q) sum_r = add2(sum_r, make_float2(bf16_lo(pk[q]), bf16_hi(pk[q])));
+                } else {  // a single key tile: what the rounding leaves off goes into the other half of S_s
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) pk[q] = pack_bf16x2(z[c + 2 * q], z[c + 2 * q + 1]);
-                        tc::st16(ts + 64 + c / 2, pk);
+                    for (int c = 0; c < T / 2; c += 16) {
+                        uint32_t hi[16], low[16];
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            float2 x = fma2(make_float2(z[2 * (c + q)], z[2 * (c + q) + 1]), sc, nb);
+                            x.x = ex2_approx(x.x);
+                            x.y = ex2_approx(x.y);
+                            sum = add2(sum, x);
+                            hi[q] = pack_bf16x2(x.x, x.y);
+                            low[q] = pack_bf16x2(x.x - bf16_lo(hi[q]), x.y - bf16_hi(hi[q]));
+                        }
+                        tc::st16(ts + c, hi);
+                        tc::st16(ts + 64 + c, low);
                     }
                     sum_r = sum;
-                } else {
-                    probabilities(std::false_type{});
+                    tc::wait_st();
+                    tc::fence_before_sync();
+                    mbar_arrive(&bar.p[s][0]);
+                    mbar_arrive(&bar.p[s][1]);
                 }
                 l += sum.x + sum.y;
                 lr += sum_r.x + sum_r.y;
-                // value rows behind the sequence's last key: whatever they hold must not meet P = 0
-                const int32_t keys = it.nk - j * T;
-                if (keys < T && (s == 0 || j >= it.tiles0)) {
-                    const uint32_t k = k0 + 5 * j + 3;
-                    for (int u = 0; u < 2; ++u) wait(&bar.full[(k + u) % kRing], ((k + u) / kRing) & 1);
-                    for (int q = row; q < (T - keys) * 16; q += T) {
-                        const int u = q >> 3 & 1, r = keys + (q >> 4);
-                        *reinterpret_cast<uint4 *>(smem + OFF_RING + (k + u) % kRing * PB + r * 128 + (q & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                }
-                tc::wait_st();
-                tc::fence_before_sync();
-                mbar_arrive(&bar.p[s]);
             }
-            const int64_t out_row = (it.q0 + s * T + row) * H + head;
+            const int64_t out_row = static_cast<int64_t>(it.q0 + s * T + row) * H + head;
             if (nt > 0) {
                 wait(&bar.o[s], (steps - 1) & 1);
                 tc::fence_after_sync();
@@ -479,13 +535,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             }
             tc::fence_before_sync();
             if (row < it.rows(s) && p.a.lse != nullptr) p.a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-            k0 += 5 * it.n;
+            g0 += it.n;
         }
     }
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 2) tc::tmem_dealloc(tmem, 512);
+    if (warp == 3) tc::tmem_dealloc(tmem, 512);
 }
 
 // Boxes of 64 columns x 128 tokens of a bf16 [tokens][heads][cols] tensor (strides in elements), 128-byte
