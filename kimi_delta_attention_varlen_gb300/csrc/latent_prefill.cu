@@ -44,9 +44,10 @@ constexpr int kBlock = 2 * T;              // queries of a block
 constexpr int PB = T * 128;                // bytes of a panel
 constexpr int kRing = 8;                   // panels in flight
 constexpr int kQBytes = DQ / 64 * PB;      // of one query tile
-constexpr int OFF_RING = 2 * kQBytes, kSmem = OFF_RING + kRing * PB + 1024;
-constexpr int kThreads = 384;              // four service warps, two softmax warpgroups
-constexpr int kServiceRegs = 88, kSoftRegs = 208;  // 128 x 88 + 256 x 208 = 64,512 = 384 x 168 registers
+constexpr int OFF_RING = 2 * kQBytes, OFF_SHARED = OFF_RING + kRing * PB;
+constexpr int kThreads = 640;              // four service warps, two softmax warpgroups a query tile
+constexpr int kServiceRegs = 64, kSoftRegs = 104;  // 128 x 64 + 512 x 104 = 61,440 = 640 x 96 registers
+constexpr int kHalf = T / 2;               // keys of a softmax thread
 constexpr uint32_t kColO = 256;            // S_s at 128 s, O_s at 256 + 128 s
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kLazy = 8.f;
@@ -191,20 +192,27 @@ __global__ void __launch_bounds__(1024) plan_kernel(Params p)
 struct Bars {
     // by parity of the key tile: its key panels and value panels, loaded and handed back
     uint64_t k_full[2][3], k_free[2], v_full[2], v_free[2];  // k_full: by panel
-    uint64_t q_full[2], q_free[2], s[2], p[2][2], o[2], drain[2];  // by query tile; p: by half of the keys
+    uint64_t q_full[2], q_free[2], s[2], p[2], o[2], drain[2];  // by query tile
 };
+
+struct Shared {
+    Bars bar;
+    float pair[2][2][T];  // by query tile, half, row: what the two threads of a row tell each other
+    uint32_t tmem_base;
+};
+constexpr int kSmem = OFF_SHARED + sizeof(Shared);
+static_assert(kSmem <= 232448, "227 KB");
 
 __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, const __grid_constant__ Maps maps)
 {
-    extern __shared__ char smem_raw[];
-    char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) Bars bar;
-    __shared__ uint32_t tmem_base;
+    extern __shared__ __align__(1024) char smem[];  // all of it: nothing static stands before it
+    Shared &sh = *reinterpret_cast<Shared *>(smem + OFF_SHARED);
+    Bars &bar = sh.bar;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
 
     if (warp == 3) {
-        tc::tmem_alloc(&tmem_base, 512);
+        tc::tmem_alloc(&sh.tmem_base, 512);
         tc::tmem_relinquish();
     }
     if (tid == 0) {
@@ -212,14 +220,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             mbar_init(&bar.k_full[s][0], 1), mbar_init(&bar.k_full[s][1], 1), mbar_init(&bar.k_full[s][2], 1), mbar_init(&bar.k_free[s], 2), mbar_init(&bar.v_full[s], 1), mbar_init(&bar.v_free[s], 2);  // handed back by both query tiles
             mbar_init(&bar.drain[s], 1);
             mbar_init(&bar.q_full[s], 1), mbar_init(&bar.q_free[s], 1), mbar_init(&bar.s[s], 1), mbar_init(&bar.o[s], 1);
-            mbar_init(&bar.p[s][0], T), mbar_init(&bar.p[s][1], T);
+            mbar_init(&bar.p[s], 2 * T);
         }
         fence_mbar_init();
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = uniform(tmem_base);
+    const uint32_t tmem = uniform(sh.tmem_base);
     const int32_t H = p.a.h, items = uniform(*p.n_blocks) * H;  // below 2^31: checked on the host
 
     bool gave_up = false;
@@ -334,23 +342,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             // O += P V of key tile g
             auto second = [&](uint32_t g, bool fresh, bool single) {
                 const uint64_t b0 = ring_desc + (5 * g + 3) % kRing * (PB >> 4), b1 = ring_desc + (5 * g + 4) % kRing * (PB >> 4);
-                if (!all_wait(&bar.v_full[g & 1], g >> 1 & 1) || !all_wait(&bar.p[s][0], pvs & 1)) return false;
+                if (!all_wait(&bar.v_full[g & 1], g >> 1 & 1) || !all_wait(&bar.p[s], pvs++ & 1)) return false;
                 tc::fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
+                    for (int ks = 0; ks < 8; ++ks) {
                         tc::mma_bf16_ts(to, ts + 8 * ks, b0 + 128 * ks, kIdO, ks > 0 || !fresh ? 1u : 0u);
                         tc::mma_bf16_ts(to + 64, ts + 8 * ks, b1 + 128 * ks, kIdO, ks > 0 || !fresh ? 1u : 0u);
-                    }
-                }
-                __syncwarp();
-                if (!all_wait(&bar.p[s][1], pvs++ & 1)) return false;
-                tc::fence_after_sync();
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 4; ks < 8; ++ks) {
-                        tc::mma_bf16_ts(to, ts + 8 * ks, b0 + 128 * ks, kIdO, 1u);
-                        tc::mma_bf16_ts(to + 64, ts + 8 * ks, b1 + 128 * ks, kIdO, 1u);
                     }
                     if (single) {  // what the rounding left off, too
 #pragma unroll
@@ -395,34 +393,46 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs) : "memory");
         // ------------------------------------------------------- softmax, epilogue
-        const int s = (warp - 4) >> 2, row = tid & 127;
+        // Two threads a row: thread `half` has 64 of a tile's 128 keys and 64 of the output's 128 columns.
+        const int s = warp >= 12 ? 1 : 0, half = (warp >> 2) - 1 - 2 * s, row = tid & 127;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-        const uint32_t ts = tl + 128 * s, to = tl + kColO + 128 * s;
+        const uint32_t ts = tl + 128 * s, to = tl + kColO + 128 * s + kHalf * half;
+        const int pair_bar = 1 + 4 * s + (warp & 3);  // the two warps of the same rows
+        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;\n" ::"r"(pair_bar) : "memory"); };
         uint32_t g0 = 0, steps = 0;  // key tiles of the items before; key tiles so far (of this query tile)
         for (int32_t idx = blockIdx.x; idx < items; idx += gridDim.x) {
-            const int2 e = p.table[idx / H];
-            const int head = idx % H;
-            Item it;
-            it.load(p.a, e.x, e.y);
-            const int32_t nt = it.tiles(s), limit = row < it.rows(s) ? it.see(s) + row : 0;  // keys that this row sees
-            float m = -INFINITY, l = 0.f, lr = 0.f;
-            // a thread that gave up goes on without waiting
+            // through the key tiles only what they need is kept (and the item read again behind them): a row's 64
+            // scores fill the registers
+            int32_t nt, limit, nk;  // key tiles; keys that this row sees; keys of the sequence
+            {
+                const int2 e = p.table[idx / H];
+                Item it;
+                it.load(p.a, e.x, e.y);
+                nt = it.tiles(s), limit = row < it.rows(s) ? it.see(s) + row : 0, nk = it.nk;
+            }
+            float m = -INFINITY, l = 0.f, lr = 0.f;  // l, lr: of this thread's keys
+            // a thread that gave up goes on without waiting: all of them meet at every barrier
             for (int32_t j = 0; j < nt; ++j, ++steps) {
                 wait(&bar.s[s], steps & 1);
                 tc::fence_after_sync();
-                float z[T];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, *reinterpret_cast<uint32_t (*)[32]>(&z[32 * c]));
+                float z[kHalf];
+                tc::ld32(ts + kHalf * half, *reinterpret_cast<uint32_t (*)[32]>(&z[0]));
+                tc::ld32(ts + kHalf * half + 32, *reinterpret_cast<uint32_t (*)[32]>(&z[32]));
                 tc::wait_ld();
-                const int32_t left = limit - j * T;  // of this tile's keys, those before `left`
-                if (__any_sync(0xffffffffu, left < T)) {
+                const int32_t left = limit - j * T - kHalf * half;  // of this thread's keys, those before `left`
+                if (__any_sync(0xffffffffu, left < kHalf)) {
 #pragma unroll
-                    for (int c = 0; c < T; ++c) z[c] = c < left ? z[c] : -INFINITY;
+                    for (int c = 0; c < kHalf; ++c) z[c] = c < left ? z[c] : -INFINITY;
                 }
                 float mx = z[0];
 #pragma unroll
-                for (int c = 1; c + 1 < T; c += 2) mx = fmaxf(mx, fmaxf(z[c], z[c + 1]));
-                mx = fmaxf(mx, z[T - 1]) * p.scale_log2;
+                for (int c = 1; c + 1 < kHalf; c += 2) mx = fmaxf(mx, fmaxf(z[c], z[c + 1]));
+                mx = fmaxf(mx, z[kHalf - 1]);
+                sh.pair[s][half][row] = mx;
+                tc::fence_before_sync();
+                pair_sync();  // both have read their scores, too: P may overwrite them
+                tc::fence_after_sync();
+                mx = fmaxf(mx, sh.pair[s][half ^ 1][row]) * p.scale_log2;
                 const bool grew = mx > m + kLazy && m > -INFINITY;
                 if (__any_sync(0xffffffffu, grew)) {
                     const float f = grew ? ex2_approx(m - mx) : 1.f;
@@ -431,61 +441,52 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                     wait(&bar.o[s], (steps - 1) & 1);  // grew only behind the first tile of the item
                     tc::fence_after_sync();
 #pragma unroll 1
-                    for (int c = 0; c < DV; c += 32) {
-                        uint32_t o[32];
-                        tc::ld32(to + c, o);
+                    for (int c = 0; c < kHalf; c += 16) {
+                        uint32_t o[16];
+                        tc::ld16(to + c, o);
                         tc::wait_ld();
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
-                        tc::st32(to + c, o);
+                        for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+                        tc::st16(to + c, o);
                     }
                 }
                 if (grew || m == -INFINITY) m = mx;
                 const float base = m == -INFINITY ? 0.f : m;
                 const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
-                // value rows behind the sequence's last key: whatever they hold must not meet P = 0 (both query
-                // tiles write these zeros, each before its own product; a second time they change nothing)
-                const int32_t keys = it.nk - j * T;
+                // value rows behind the sequence's last key: whatever they hold must not meet P = 0 (every softmax
+                // thread of the tile writes its share of these zeros for its own product; a second time they change nothing)
+                const int32_t keys = nk - j * T;
                 if (keys < T) {
                     const uint32_t g = g0 + j;
                     wait(&bar.v_full[g & 1], g >> 1 & 1);
-                    for (int q = row; q < (T - keys) * 16; q += T) {
-                        const int u = q >> 3 & 1, r = keys + (q >> 4);
-                        *reinterpret_cast<uint4 *>(smem + OFF_RING + (5 * g + 3 + u) % kRing * PB + r * 128 + (q & 7) * 16) =
+                    for (int q = row; q < (T - keys) * 8; q += T)
+                        *reinterpret_cast<uint4 *>(smem + OFF_RING + (5 * g + 3 + half) % kRing * PB + (keys + (q >> 3)) * 128 + (q & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
-                    }
                     fence_proxy_async_smem();
                 }
-                // scores -> probabilities, rounded, into S_s; the first 64 keys are handed over first
+                // scores -> probabilities, rounded, into S_s
                 float2 sum = make_float2(0.f, 0.f), sum_r = make_float2(0.f, 0.f);
                 if (nt > 1) {
-                    uint32_t pk[T / 2];
 #pragma unroll
-                    for (int c = 0; c < T / 2; c += 16) {
+                    for (int c = 0; c < kHalf / 2; c += 16) {
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int q = c; q < c + 16; ++q) {
-                            float2 x = fma2(make_float2(z[2 * q], z[2 * q + 1]), sc, nb);
+                        for (int q = 0; q < 16; ++q) {
+                            float2 x = fma2(make_float2(z[2 * (c + q)], z[2 * (c + q) + 1]), sc, nb);
                             x.x = ex2_approx(x.x);
                             x.y = ex2_approx(x.y);
                             sum = add2(sum, x);
                             pk[q] = pack_bf16x2(x.x, x.y);
+                            sum_r = add2(sum_r, make_float2(bf16_lo(pk[q]), bf16_hi(pk[q])));
                         }
-                        tc::st16(ts + c, *reinterpret_cast<uint32_t (*)[16]>(&pk[c]));
-                        if (c == 16) {
-                            tc::wait_st();
-                            tc::fence_before_sync();
-                            mbar_arrive(&bar.p[s][0]);
-                        }
+                        tc::st16(ts + kHalf / 2 * half + c, pk);
                     }
                     tc::wait_st();
                     tc::fence_before_sync();
-                    mbar_arrive(&bar.p[s][1]);
-                    // the sum of the rounded weights, while the tensor cores go on
-#pragma unroll
-                    for (int q = 0; q < T / 2; ++q) sum_r = add2(sum_r, make_float2(bf16_lo(pk[q]), bf16_hi(pk[q])));
+                    mbar_arrive(&bar.p[s]);
                 } else {  // a single key tile: what the rounding leaves off goes into the other half of S_s
 #pragma unroll
-                    for (int c = 0; c < T / 2; c += 16) {
+                    for (int c = 0; c < kHalf / 2; c += 16) {
                         uint32_t hi[16], low[16];
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
@@ -496,35 +497,45 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                             hi[q] = pack_bf16x2(x.x, x.y);
                             low[q] = pack_bf16x2(x.x - bf16_lo(hi[q]), x.y - bf16_hi(hi[q]));
                         }
-                        tc::st16(ts + c, hi);
-                        tc::st16(ts + 64 + c, low);
+                        tc::st16(ts + kHalf / 2 * half + c, hi);
+                        tc::st16(ts + 64 + kHalf / 2 * half + c, low);
                     }
                     sum_r = sum;
                     tc::wait_st();
                     tc::fence_before_sync();
-                    mbar_arrive(&bar.p[s][0]);
-                    mbar_arrive(&bar.p[s][1]);
+                    mbar_arrive(&bar.p[s]);
                 }
                 l += sum.x + sum.y;
                 lr += sum_r.x + sum_r.y;
             }
-            const int64_t out_row = static_cast<int64_t>(it.q0 + s * T + row) * H + head;
+            pair_sync();  // the maxima have been read
+            sh.pair[s][half][row] = l;
+            pair_sync();
+            l += sh.pair[s][half ^ 1][row];
+            pair_sync();
+            sh.pair[s][half][row] = lr;
+            pair_sync();
+            lr += sh.pair[s][half ^ 1][row];
+            const int2 e = p.table[idx / H];
+            Item it;
+            it.load(p.a, e.x, e.y);
+            const int64_t out_row = static_cast<int64_t>(it.q0 + s * T + row) * H + idx % H;
             if (nt > 0) {
                 wait(&bar.o[s], (steps - 1) & 1);
                 tc::fence_after_sync();
             }
             const float inv = lr > 0.f ? 1.f / lr : 0.f;
-            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.a.out) + out_row * DV);
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.a.out) + out_row * DV + kHalf * half);
 #pragma unroll
-            for (int c = 0; c < DV; c += 32) {
-                uint32_t o[32];
+            for (int c = 0; c < kHalf; c += 16) {
+                uint32_t o[16];
                 if (nt > 0) {
-                    tc::ld32(to + c, o);
+                    tc::ld16(to + c, o);
                     tc::wait_ld();
                 }
                 if (row < it.rows(s)) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         uint32_t w[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
@@ -534,7 +545,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 }
             }
             tc::fence_before_sync();
-            if (row < it.rows(s) && p.a.lse != nullptr) p.a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            if (half == 0 && row < it.rows(s) && p.a.lse != nullptr) p.a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            pair_sync();  // the sums have been read
             g0 += it.n;
         }
     }
@@ -596,10 +608,10 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    // the register split (setmaxnreg) needs a launch with exactly 168 registers a thread
+    // the register split (setmaxnreg) needs a launch with exactly 96 registers a thread
     cudaFuncAttributes at;
     if ((e = cudaFuncGetAttributes(&at, latent_prefill_kernel)) != cudaSuccess) return e;
-    if (at.numRegs != 168) return cudaErrorInvalidConfiguration;
+    if (at.numRegs != 96) return cudaErrorInvalidConfiguration;
     const int64_t items = p.max_blocks * a.h, sms = sm_count();
     latent_prefill_kernel<<<static_cast<unsigned>(items < sms ? items : sms), kThreads, kSmem, st>>>(p, maps);
     return cudaGetLastError();
