@@ -320,29 +320,41 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             const uint32_t base = smem_u32(smem), ts = tmem + 128 * s, to = tmem + kColO + 128 * s;
             const uint64_t q_desc = tc::sdesc_sw128(base + s * kQBytes, 16, 1024), ring_desc = tc::sdesc_sw128(base + OFF_RING, 16, 1024);
             uint32_t g = 0, loads = 0, pvs = 0;  // key tiles, query tiles, second products so far
+            // panel u of S of key tile g (by one lane)
+            auto panel = [&](uint32_t g, int u) {
+                const uint64_t a = q_desc + (u * PB >> 4), b = ring_desc + (5 * g + u) % kRing * (PB >> 4);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) tc::mma_bf16(ts, a + 2 * ks, b + 2 * ks, kIdS, u > 0 || ks > 0 ? 1u : 0u);
+            };
+            auto first_done = [&](uint32_t g, bool free_q) {
+                tc::commit(&bar.s[s]);
+                tc::commit(&bar.k_free[g & 1]);
+                if (free_q) tc::commit(&bar.q_free[s]);
+            };
             // S of key tile g, panel by panel as they arrive
             auto first = [&](uint32_t g, bool free_q) {
 #pragma unroll
                 for (int u = 0; u < 3; ++u) {
                     if (!all_wait(&bar.k_full[g & 1][u], g >> 1 & 1)) return false;
                     if (elect_one()) {
-                        const uint64_t a = q_desc + (u * PB >> 4), b = ring_desc + (5 * g + u) % kRing * (PB >> 4);
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) tc::mma_bf16(ts, a + 2 * ks, b + 2 * ks, kIdS, u > 0 || ks > 0 ? 1u : 0u);
-                        if (u == 2) {
-                            tc::commit(&bar.s[s]);
-                            tc::commit(&bar.k_free[g & 1]);
-                            if (free_q) tc::commit(&bar.q_free[s]);
-                        }
+                        panel(g, u);
+                        if (u == 2) first_done(g, free_q);
                     }
                     __syncwarp();
                 }
                 return true;
             };
-            // O += P V of key tile g
-            auto second = [&](uint32_t g, bool fresh, bool single) {
+            // O += P V of key tile g and, behind it, S of key tile g + 1 (more).  A look at a barrier costs its time even
+            // where the barrier is long open, and behind the product it would leave the tensor pipe idle: so the
+            // key panels are looked at before the wait for P, and S follows at once where they are there.
+            auto second = [&](uint32_t g, bool fresh, bool single, bool more, bool free_q) {
                 const uint64_t b0 = ring_desc + (5 * g + 3) % kRing * (PB >> 4), b1 = ring_desc + (5 * g + 4) % kRing * (PB >> 4);
-                if (!all_wait(&bar.v_full[g & 1], g >> 1 & 1) || !all_wait(&bar.p[s], pvs++ & 1)) return false;
+                if (!all_wait(&bar.v_full[g & 1], g >> 1 & 1)) return false;
+                const uint32_t n = g + 1, par = n >> 1 & 1;
+                const bool there = more && __all_sync(0xffffffffu, mbar_test(&bar.k_full[n & 1][0], par) &&
+                                                                      mbar_test(&bar.k_full[n & 1][1], par) &&
+                                                                      mbar_test(&bar.k_full[n & 1][2], par));
+                if (!all_wait(&bar.p[s], pvs++ & 1)) return false;
                 tc::fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
@@ -359,9 +371,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                     }
                     tc::commit(&bar.o[s]);
                     tc::commit(&bar.v_free[g & 1]);
+                    if (there) {
+                        panel(n, 0);
+                        panel(n, 1);
+                        panel(n, 2);
+                        first_done(n, free_q);
+                    }
                 }
                 __syncwarp();
-                return true;
+                return !more || there || first(n, free_q);
             };
             bool ok = true;
             for (int32_t idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
@@ -376,8 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 }
                 for (int j = 0; j < n; ++j, ++g) {
                     if (j < nt) {
-                        if (!(ok = second(g, j == 0, nt == 1))) break;
-                        if (j + 1 < nt && !(ok = first(g + 1, j + 2 == nt))) break;
+                        if (!(ok = second(g, j == 0, nt == 1, j + 1 < nt, j + 2 == nt))) break;
                     } else {  // the other query tile's alone: handed back once it is there (then the tile two before is)
                         if (!(ok = all_wait(&bar.k_full[g & 1][0], g >> 1 & 1))) break;
                         if (lane == 0) mbar_arrive(&bar.k_free[g & 1]);
