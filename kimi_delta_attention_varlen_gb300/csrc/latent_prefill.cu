@@ -5,17 +5,24 @@
 // of 128 with a running maximum m and sum l a row.
 //
 // plan_kernel (one CTA) lists the query blocks (256 queries of one sequence), longest first by the
-// key tiles they see.  One persistent CTA per SM then takes every grid-th (block, head) pair of the
-// list.  A block is two query tiles s = 0, 1 of 128 rows that share the key and value tiles:
+// key tiles they see.  One persistent CTA per SM takes (block, head) pairs of the list: whole rounds of
+// one pair a CTA, in turn from either end (the pairs of a round are alike in length, and blocks of one
+// sequence run side by side, so their keys and values come from the L2 cache); of the last, partial
+// round all key tiles lie on one line and each CTA takes an equal stretch of it.  A pair that falls
+// into several stretches leaves unnormalised parts in the workspace, which join_kernel puts together in
+// order of their keys.  Parts cost about what kCutTiles key tiles do (queries loaded again, parts written
+// and joined: 10 us), so the last round runs whole where its longest pair is not that much longer than an
+// equal stretch.  Measured, cut against whole: 1000 queries on 16000 keys, 4 heads 62 / 244 us; 8192 queries,
+// 2 heads 73 / 122 us; four prompts of up to 2000, 8 heads 65 / 55 us (these run whole).
+// A block is two query tiles s = 0, 1 of 128 rows that share the key and value tiles:
 //   S_s   = Q_s K^T     M = 128, N = 128, K = 192 (two nope panels and the shared rope panel)
 //   O_s  += P_s V       M = 128, N = 64 twice, K = 128, P_s in tensor memory
 // Tensor memory holds S_0, S_1, O_0, O_1 (128 columns each); P_s (bf16) overlays S_s.  While the
 // softmax of one tile runs, the tensor cores do the other tile's two products.  Warps: one issues the
-// TMA copies, one the MMAs of each query tile, two warpgroups do the softmax (one row a thread) and the epilogues.
+// TMA copies, one the MMAs of each query tile; two warpgroups a query tile do the softmax (two threads a
+// row) and the epilogue.
 // Key and value panels (128 tokens x 64, 16 KB, 128-byte swizzle) pass through one ring of eight: per
-// key tile three key panels (K-major B), then two value panels (MN-major B).  The probabilities are
-// handed over in two halves, and the sums are formed behind them, so that they are off the path from
-// S_s to O_s.
+// key tile three key panels (K-major B), then two value panels (MN-major B).
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the last rescale.  The
 // probabilities are rounded to bf16, the tensor cores' operand type; the output is normalised by the
@@ -54,6 +61,8 @@ constexpr float kLazy = 8.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kStatusExpired = 7;
 constexpr int kBuckets = 1024;
+constexpr int kCutTiles = 10;
+constexpr int kReaders = 3 + 16;           // warps that read a segment
 
 enum Order { kHeadsFirst = 0, kTokensFirst = 1, kOneHead = 2 };  // (x, head, token), (x, token, head), (x, 0, token)
 
@@ -61,10 +70,16 @@ struct Params {
     LatentPrefillArgs a;
     float scale_log2;
     int32_t kn_order, v_order;  // of the map's coordinates: Order
-    int32_t *status, *n_blocks;
-    int2 *table;         // [max_blocks] (sequence, block of the sequence)
-    int32_t *seq_off;    // [num_seqs + 1] blocks before each sequence
+    int32_t *status;
+    int32_t *n_blocks, *whole;   // blocks listed; pairs that are taken whole (a multiple of the grid, or all)
+    int64_t *before;             // [max_blocks + 1] key tiles (of one head) before each block of the list, and in all
+    int2 *table;                 // [max_blocks] (sequence, block of the sequence)
+    int32_t *seq_off;            // [num_seqs + 1] blocks before each sequence
     int64_t max_blocks;
+    int32_t grid;
+    int32_t *item0, *item1;      // [grid] pair whose part is in slot 0 / 1 of the CTA, or -1
+    float4 *ml;                  // [grid][2][256] m, l, l of the rounded weights
+    float *part;                 // [grid][2][256][DV]
 };
 
 struct Maps {
@@ -104,6 +119,71 @@ struct Item {
     __device__ int32_t see(int s) const { return see0 + s * T; }
 };
 
+// The work of one CTA in order: (block, head) pairs, and a stretch [j0, j1) of the key tiles of others.
+struct Walk {
+    int32_t round, whole;   // rounds of whole pairs taken so far; pairs that are taken whole
+    int32_t next_pair, next_j;  // behind the whole pairs: where the stretch goes on
+    int64_t left;               // key tiles of the stretch to come
+    int32_t head, pair;
+    int32_t j0, j1, slot;   // slot: where a part goes, 0 if it is not its pair's first; -1: the pair is whole
+    Item it;
+
+    __device__ void begin(const Params &p, int32_t blocks)
+    {
+        round = 0, whole = *p.whole, left = 0;
+        const int32_t H = p.a.h, items = blocks * H;
+        if (whole >= items) return;
+        // the line begins with pair `whole`
+        const int64_t base = p.before[whole / H] * H + whole % H * (p.before[whole / H + 1] - p.before[whole / H]);
+        const int64_t all = p.before[blocks] * H - base, n = all < gridDim.x ? all : gridDim.x;
+        if (blockIdx.x >= n) return;
+        const int64_t w0 = all * blockIdx.x / n;
+        left = all * (blockIdx.x + 1) / n - w0;
+        int32_t lo = whole / H, hi = blocks;  // the block with before[lo] * H <= base + w0 < before[lo + 1] * H
+        while (lo + 1 < hi) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (p.before[mid] * H <= base + w0) lo = mid;
+            else hi = mid;
+        }
+        const int64_t rest = base + w0 - p.before[lo] * H, units = p.before[lo + 1] - p.before[lo];
+        next_pair = lo * H + static_cast<int32_t>(rest / units);
+        next_j = static_cast<int32_t>(rest % units);
+    }
+    // The next pair or stretch; false: none.
+    __device__ bool next(const Params &p, int32_t items)
+    {
+        const int32_t grid = gridDim.x, at = round * grid + (round & 1 ? grid - 1 - static_cast<int32_t>(blockIdx.x) : blockIdx.x);
+        const bool entire = round * grid < whole;
+        if (entire) {
+            ++round;
+            if (at >= items) return false;  // beyond the end of a last round that runs whole
+            pair = at;
+        } else {
+            if (left <= 0) return false;
+            pair = next_pair;
+        }
+        head = pair % p.a.h;
+        const int2 e = p.table[pair / p.a.h];
+        it.load(p.a, e.x, e.y);
+        j0 = 0, j1 = it.n, slot = -1;
+        if (!entire) {
+            const int32_t units = it.n > 0 ? it.n : 1;  // a block that sees nothing is still written
+            const int32_t end = left < units - next_j ? next_j + static_cast<int32_t>(left) : units;
+            if (next_j > 0 || end < units) j0 = next_j, j1 = end, slot = j0 > 0 ? 0 : 1;
+            left -= end - next_j;
+            next_j = 0;
+            ++next_pair;
+        }
+        return true;
+    }
+    // key tiles of query tile s in this stretch
+    __device__ int32_t tiles(int s) const
+    {
+        const int32_t t = it.tiles(s) < j1 ? it.tiles(s) : j1;
+        return t > j0 ? t - j0 : 0;
+    }
+};
+
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t r;
@@ -121,20 +201,21 @@ __host__ __device__ constexpr int64_t blocks_bound(int64_t total_q, int64_t num_
 // ------------------------------------------------------------------ the plan --
 __global__ void __launch_bounds__(1024) plan_kernel(Params p)
 {
-    __shared__ int32_t hist[kBuckets], sums[32];
+    __shared__ int32_t hist[kBuckets];
+    __shared__ int64_t sums[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const LatentPrefillArgs &a = p.a;
-    auto scan = [&](int32_t x, int32_t *total) {  // exclusive prefix over the CTA
-        int32_t s = x;
+    auto scan = [&](int64_t x, int64_t *total) {  // exclusive prefix over the CTA
+        int64_t s = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int32_t y = __shfl_up_sync(0xffffffffu, s, o);
+            const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += y;
         }
         __syncthreads();
         if (lane == 31) sums[warp] = s;
         __syncthreads();
-        int32_t before = 0, all = 0;
+        int64_t before = 0, all = 0;
         for (int w = 0; w < 32; ++w) {
             before += w < warp ? sums[w] : 0;
             all += sums[w];
@@ -144,7 +225,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(Params p)
     };
     if (tid == 0) *p.status = 0;
     hist[tid] = 0;
-    int32_t base = 0;
+    int64_t base = 0;
     for (int64_t b0 = 0; b0 < a.num_seqs; b0 += 1024) {
         const int64_t b = b0 + tid;
         int32_t nb = 0;
@@ -152,40 +233,82 @@ __global__ void __launch_bounds__(1024) plan_kernel(Params p)
             const int64_t n = clamp64(a.cu_q[b + 1], a.total_q) - clamp64(a.cu_q[b], a.total_q);
             nb = n > 0 ? static_cast<int32_t>((n + kBlock - 1) / kBlock) : 0;
         }
-        int32_t total;
-        const int32_t at = base + scan(nb, &total);
-        if (b < a.num_seqs) p.seq_off[b] = at;
+        int64_t total;
+        const int64_t at = base + scan(nb, &total);
+        if (b < a.num_seqs) p.seq_off[b] = static_cast<int32_t>(at);
         base += total;
     }
     // more blocks than the bound only if the offsets are not what the contract says
-    const int32_t blocks = base < p.max_blocks ? base : static_cast<int32_t>(p.max_blocks);
+    const int32_t blocks = static_cast<int32_t>(base < p.max_blocks ? base : p.max_blocks);
     if (tid == 0) *p.n_blocks = blocks;
     __syncthreads();
-    auto locate = [&](int32_t i, int2 *e) {
-        int64_t lo = 0, hi = a.num_seqs;
+    auto locate = [&](int32_t i, int2 *e) {  // block i in order of the sequences; its key tiles
+        int32_t lo = 0, hi = static_cast<int32_t>(a.num_seqs);
         while (lo + 1 < hi) {
-            const int64_t mid = (lo + hi) >> 1;
+            const int32_t mid = (lo + hi) >> 1;
             if (p.seq_off[mid] <= i) lo = mid;
             else hi = mid;
         }
-        *e = make_int2(static_cast<int>(lo), i - p.seq_off[lo]);
+        *e = make_int2(lo, i - p.seq_off[lo]);
         Item it;
         it.load(a, e->x, e->y);
-        return it.n < kBuckets ? kBuckets - 1 - it.n : 0;  // longest first
+        return it.n;
     };
+    // counting sort by key tiles, longest first; blocks of one length stay in order, so that the list, and with it
+    // the places where pairs are cut, does not depend on the order of the atomics
     int2 e;
-    for (int32_t i = tid; i < blocks; i += 1024) atomicAdd(&hist[locate(i, &e)], 1);
+    auto bucket = [&](int32_t n) { return n < kBuckets ? kBuckets - 1 - n : 0; };
+    for (int32_t i = tid; i < blocks; i += 1024) atomicAdd(&hist[bucket(locate(i, &e))], 1);
     __syncthreads();
-    int32_t total;
-    const int32_t first = scan(hist[tid], &total);
+    int64_t total;
+    const int32_t first = static_cast<int32_t>(scan(hist[tid], &total));
     __syncthreads();
     hist[tid] = first;
     __syncthreads();
-    // the order within a bucket is open: it decides which CTA takes a block, not what it computes
-    for (int32_t i = tid; i < blocks; i += 1024) {
-        const int bucket = locate(i, &e);
-        p.table[atomicAdd(&hist[bucket], 1)] = e;
+    for (int32_t i0 = 0; i0 < blocks; i0 += 1024) {
+        const int32_t i = i0 + tid, b = i < blocks ? bucket(locate(i, &e)) : -1;
+        for (int w = 0; w < 32 && i0 + 32 * w < blocks; ++w) {  // warp after warp
+            if (w == warp) {
+                const uint32_t same = __match_any_sync(0xffffffffu, b);
+                const int32_t rank = __popc(same & ((1u << lane) - 1));
+                const int32_t at = b >= 0 ? hist[b] : 0;
+                __syncwarp();
+                if (b >= 0) {
+                    p.table[at + rank] = e;
+                    if (rank == 0) hist[b] = at + __popc(same);
+                }
+            }
+            __syncthreads();
+        }
     }
+    // key tiles before each block of the list
+    int64_t units = 0;
+    for (int32_t i0 = 0; i0 < blocks; i0 += 1024) {
+        const int32_t i = i0 + tid;
+        int32_t u = 0;
+        if (i < blocks) {
+            const int2 b = p.table[i];
+            Item it;
+            it.load(a, b.x, b.y);
+            u = it.n > 0 ? it.n : 1;
+        }
+        const int64_t at = scan(u, &total);
+        if (i < blocks) p.before[i] = units + at;
+        units += total;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        p.before[blocks] = units;
+        const int32_t items = blocks * a.h, whole = items / p.grid * p.grid;
+        *p.whole = items;
+        if (whole < items) {
+            const int32_t b = whole / a.h;
+            const int64_t longest = p.before[b + 1] - p.before[b];
+            const int64_t rest = units * a.h - p.before[b] * a.h - whole % a.h * longest;
+            if (longest > rest / p.grid + kCutTiles) *p.whole = whole;
+        }
+    }
+    for (int32_t c = tid; c < p.grid; c += 1024) p.item0[c] = p.item1[c] = -1;
 }
 
 // ------------------------------------------------------------------ the kernel --
@@ -193,10 +316,22 @@ struct Bars {
     // by parity of the key tile: its key panels and value panels, loaded and handed back
     uint64_t k_full[2][3], k_free[2], v_full[2], v_free[2];  // k_full: by panel
     uint64_t q_full[2], q_free[2], s[2], p[2], o[2], drain[2];  // by query tile
+    uint64_t seg_full[2], seg_free[2];
+};
+
+// A pair, or stretch of one, as the scheduling warp hands it to the others.
+struct Segment {
+    int32_t q0, k0, nk;         // first query row, first key of the sequence, its keys
+    int32_t rows[2], tiles[2];  // by query tile: valid queries, key tiles in the stretch
+    int32_t see;                // keys that the block's first query sees
+    int32_t j0, j1;             // key tiles of the stretch
+    int32_t slot, head, pair;   // slot: as in Walk; pair -1: no more work
+    int32_t single;             // bit s: query tile s sees one key tile in all
 };
 
 struct Shared {
     Bars bar;
+    Segment seg[2];
     float pair[2][2][T];  // by query tile, half, row: what the two threads of a row tell each other
     uint32_t tmem_base;
 };
@@ -218,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar.k_full[s][0], 1), mbar_init(&bar.k_full[s][1], 1), mbar_init(&bar.k_full[s][2], 1), mbar_init(&bar.k_free[s], 2), mbar_init(&bar.v_full[s], 1), mbar_init(&bar.v_free[s], 2);  // handed back by both query tiles
-            mbar_init(&bar.drain[s], 1);
+            mbar_init(&bar.drain[s], 1), mbar_init(&bar.seg_full[s], 1), mbar_init(&bar.seg_free[s], kReaders);
             mbar_init(&bar.q_full[s], 1), mbar_init(&bar.q_free[s], 1), mbar_init(&bar.s[s], 1), mbar_init(&bar.o[s], 1);
             mbar_init(&bar.p[s], 2 * T);
         }
@@ -228,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = uniform(sh.tmem_base);
-    const int32_t H = p.a.h, items = uniform(*p.n_blocks) * H;  // below 2^31: checked on the host
+    uint32_t nseg = 0;  // segments taken
 
     bool gave_up = false;
     auto wait = [&](uint64_t *b, uint32_t parity) {
@@ -244,36 +379,46 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
         return __all_sync(0xffffffffu, wait(b, parity)) != 0;
     };
 
+    // the next segment, or nullptr behind the last one; `segment_done` (by a whole warp) gives it back
+    auto next_segment = [&]() -> const Segment * {
+        if (!all_wait(&bar.seg_full[nseg & 1], nseg >> 1 & 1)) return nullptr;
+        const Segment *g = &sh.seg[nseg & 1];
+        return uniform(g->pair) < 0 ? nullptr : g;
+    };
+    auto segment_done = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.seg_free[nseg & 1]);
+        ++nseg;
+    };
+
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kServiceRegs) : "memory");
         if (warp == 0) {
             // ------------------------------------------------------------ copies
             uint32_t g = 0, loads0 = 0, loads1 = 0;  // key tiles, query tiles so far
-            auto query = [&](int s, uint32_t &loads, const Item &it, int head) {
-                if (it.tiles(s) == 0) return true;
+            auto query = [&](const Segment &w, int s, uint32_t &loads) {
+                if (w.tiles[s] == 0) return true;
                 if (loads > 0 && !all_wait(&bar.q_free[s], (loads - 1) & 1)) return false;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&bar.q_full[s], kQBytes);
 #pragma unroll
                     for (int u = 0; u < DQ / 64; ++u)
-                        tma_load_3d(smem + s * kQBytes + u * PB, &maps.q, 64 * u, head, it.q0 + s * T, &bar.q_full[s]);
+                        tma_load_3d(smem + s * kQBytes + u * PB, &maps.q, 64 * u, w.head, w.q0 + s * T, &bar.q_full[s]);
                 }
                 __syncwarp();
                 ++loads;
                 return true;
             };
             bool ok = true;
-            for (int32_t idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
-                const int2 e = p.table[idx / H];
-                const int head = idx % H;
-                Item it;
-                it.load(p.a, e.x, e.y);
-                if (!(ok = query(0, loads0, it, head))) break;
-                for (int32_t j = 0; j < it.n; ++j, ++g) {
+            while (const Segment *seg = ok ? next_segment() : nullptr) {
+                const Segment &w = *seg;
+                if (!(ok = query(w, 0, loads0))) break;
+                const int head = w.head, j0 = w.j0, j1 = w.j1, first_key = w.k0;
+                for (int32_t j = j0; j < j1; ++j, ++g) {
                     // panel i of tile g lies in slot (5 g + i) % 8: its first key panel where tile g - 2's last one was (waited
                     // for with tile g - 1's values), the others where tile g - 2's values were, its values where tile g - 1's
                     // first keys were
-                    const int tok = it.k0 + j * T;
+                    const int tok = first_key + j * T;
                     char *const ring = smem + OFF_RING;
                     const int kn_y = p.kn_order == kTokensFirst ? tok : p.kn_order == kOneHead ? 0 : head;
                     const int kn_z = p.kn_order == kTokensFirst ? head : tok;
@@ -290,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                         tma_load_3d(ring + (5 * g + 2) % kRing * PB, &maps.kr, 0, 0, tok, &bar.k_full[g & 1][2]);
                     }
                     __syncwarp();
-                    if (j == 0 && !(ok = query(1, loads1, it, head))) break;
+                    if (j == j0 && !(ok = query(w, 1, loads1))) break;
                     if (g > 0 && !(ok = all_wait(&bar.k_free[(g - 1) & 1], (g - 1) >> 1 & 1))) break;
                     if (elect_one()) {
                         const int order = p.v_order, y = order == kTokensFirst ? tok : order == kOneHead ? 0 : head;
@@ -301,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                     }
                     __syncwarp();
                 }
+                segment_done();
             }
             if (!ok) {  // gave up: the copies in flight land before the CTA ends
                 // what tile g has under way is not told apart: a wait for what was not begun runs out, bounded like the others
@@ -382,11 +528,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 return !more || there || first(n, free_q);
             };
             bool ok = true;
-            for (int32_t idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
-                const int2 e = p.table[idx / H];
-                Item it;
-                it.load(p.a, e.x, e.y);
-                const int nt = uniform(it.tiles(s)), n = uniform(it.n);
+            while (const Segment *seg = ok ? next_segment() : nullptr) {
+                const int nt = uniform(seg->tiles[s]), n = uniform(seg->j1 - seg->j0);
+                const bool single = (uniform(seg->single) >> s & 1) != 0;
+                segment_done();
                 if (nt > 0) {
                     if (!(ok = all_wait(&bar.q_full[s], loads++ & 1))) break;
                     tc::fence_after_sync();
@@ -394,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 }
                 for (int j = 0; j < n; ++j, ++g) {
                     if (j < nt) {
-                        if (!(ok = second(g, j == 0, nt == 1, j + 1 < nt, j + 2 == nt))) break;
+                        if (!(ok = second(g, j == 0, single, j + 1 < nt, j + 2 == nt))) break;
                     } else {  // the other query tile's alone: handed back once it is there (then the tile two before is)
                         if (!(ok = all_wait(&bar.k_full[g & 1][0], g >> 1 & 1))) break;
                         if (lane == 0) mbar_arrive(&bar.k_free[g & 1]);
@@ -406,6 +551,27 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             }
             if (elect_one()) tc::commit(&bar.drain[s]);  // everything issued has completed before tensor memory is given back
             mbar_wait(&bar.drain[s], 0, kWaitLimit);
+        } else {
+            // -------------------------------------------------------- scheduling
+            const int32_t blocks = *p.n_blocks, items = blocks * p.a.h;  // below 2^31: checked on the host
+            Walk w;
+            w.begin(p, blocks);
+            for (bool more = true; more; ++nseg) {
+                more = w.next(p, items);
+                if (nseg > 1 && !all_wait(&bar.seg_free[nseg & 1], ((nseg >> 1) & 1) ^ 1)) break;
+                if (lane == 0) {
+                    Segment &g = sh.seg[nseg & 1];
+                    g.pair = -1;
+                    if (more) {
+                        g.q0 = w.it.q0, g.k0 = w.it.k0, g.nk = w.it.nk, g.see = w.it.see0;
+                        g.rows[0] = w.it.rows0, g.rows[1] = w.it.rows1, g.tiles[0] = w.tiles(0), g.tiles[1] = w.tiles(1);
+                        g.j0 = w.j0, g.j1 = w.j1, g.slot = w.slot, g.head = w.head, g.pair = w.pair;
+                        g.single = (w.it.tiles0 == 1 ? 1 : 0) | (w.it.tiles1 == 1 ? 2 : 0);
+                    }
+                    mbar_arrive(&bar.seg_full[nseg & 1]);
+                }
+                __syncwarp();
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs) : "memory");
@@ -416,19 +582,24 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
         const uint32_t ts = tl + 128 * s, to = tl + kColO + 128 * s + kHalf * half;
         const int pair_bar = 1 + 4 * s + (warp & 3);  // the two warps of the same rows
         auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;\n" ::"r"(pair_bar) : "memory"); };
-        uint32_t g0 = 0, steps = 0;  // key tiles of the items before; key tiles so far (of this query tile)
-        for (int32_t idx = blockIdx.x; idx < items; idx += gridDim.x) {
-            // through the key tiles only what they need is kept (and the item read again behind them): a row's 64
-            // scores fill the registers
-            int32_t nt, limit, nk;  // key tiles; keys that this row sees; keys of the sequence
-            {
-                const int2 e = p.table[idx / H];
-                Item it;
-                it.load(p.a, e.x, e.y);
-                nt = it.tiles(s), limit = row < it.rows(s) ? it.see(s) + row : 0, nk = it.nk;
-            }
+        auto pair_any = [&](bool v) {
+            uint32_t r;
+            asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                         : "=r"(r)
+                         : "r"(v ? 1u : 0u), "r"(pair_bar)
+                         : "memory");
+            return r != 0;
+        };
+        uint32_t g0 = 0, steps = 0;  // key tiles of the segments before; key tiles so far (of this query tile)
+        // A thread that gave up goes on without waiting, so that the two warps of a row meet at every barrier, and
+        // both leave at the next segment.
+        while (true) {
+            const Segment *seg = next_segment();
+            if (pair_any(gave_up) || seg == nullptr) break;
+            // a row's 64 scores fill the registers: what is not needed for each tile stays in the segment
+            const int32_t nt = seg->tiles[s], limit = (row < seg->rows[s] ? seg->see + s * T + row : 0) - seg->j0 * T;  // keys seen
+            const bool single = (seg->single >> s & 1) != 0;
             float m = -INFINITY, l = 0.f, lr = 0.f;  // l, lr: of this thread's keys
-            // a thread that gave up goes on without waiting: all of them meet at every barrier
             for (int32_t j = 0; j < nt; ++j, ++steps) {
                 wait(&bar.s[s], steps & 1);
                 tc::fence_after_sync();
@@ -472,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
                 // value rows behind the sequence's last key: whatever they hold must not meet P = 0 (every softmax
                 // thread of the tile writes its share of these zeros for its own product; a second time they change nothing)
-                const int32_t keys = nk - j * T;
+                const int32_t keys = seg->nk - (seg->j0 + j) * T;
                 if (keys < T) {
                     const uint32_t g = g0 + j;
                     wait(&bar.v_full[g & 1], g >> 1 & 1);
@@ -483,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 }
                 // scores -> probabilities, rounded, into S_s
                 float2 sum = make_float2(0.f, 0.f), sum_r = make_float2(0.f, 0.f);
-                if (nt > 1) {
+                if (!single) {
 #pragma unroll
                     for (int c = 0; c < kHalf / 2; c += 16) {
                         uint32_t pk[16];
@@ -533,10 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             sh.pair[s][half][row] = lr;
             pair_sync();
             lr += sh.pair[s][half ^ 1][row];
-            const int2 e = p.table[idx / H];
-            Item it;
-            it.load(p.a, e.x, e.y);
-            const int64_t out_row = static_cast<int64_t>(it.q0 + s * T + row) * H + idx % H;
+            const int32_t slot = seg->slot;
+            const int64_t out_row = static_cast<int64_t>(seg->q0 + s * T + row) * p.a.h + seg->head;
+            const int64_t part_row = (2 * static_cast<int64_t>(blockIdx.x) + slot) * kBlock + s * T + row;
+            const bool valid = row < seg->rows[s];
             if (nt > 0) {
                 wait(&bar.o[s], (steps - 1) & 1);
                 tc::fence_after_sync();
@@ -550,27 +721,73 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                     tc::ld16(to + c, o);
                     tc::wait_ld();
                 }
-                if (row < it.rows(s)) {
+                if (slot >= 0) {  // a part: as it is
+                    if (nt > 0 && valid) {
+                        uint4 *part = reinterpret_cast<uint4 *>(p.part + part_row * DV + kHalf * half + c);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) part[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    }
+                } else if (valid) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        uint32_t w[4];
+                        uint32_t v[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            w[r] = inv > 0.f ? pack_bf16x2(__uint_as_float(o[8 * q + 2 * r]) * inv, __uint_as_float(o[8 * q + 2 * r + 1]) * inv) : 0u;
-                        out[c / 8 + q] = make_uint4(w[0], w[1], w[2], w[3]);
+                            v[r] = inv > 0.f ? pack_bf16x2(__uint_as_float(o[8 * q + 2 * r]) * inv, __uint_as_float(o[8 * q + 2 * r + 1]) * inv) : 0u;
+                        out[c / 8 + q] = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
             }
             tc::fence_before_sync();
-            if (half == 0 && row < it.rows(s) && p.a.lse != nullptr) p.a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            if (half == 0 && slot >= 0) {
+                p.ml[part_row] = make_float4(m, l, lr, 0.f);
+                if (row == 0 && s == 0) (slot ? p.item1 : p.item0)[blockIdx.x] = seg->pair;
+            } else if (half == 0 && valid && p.a.lse != nullptr) {
+                p.a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            }
             pair_sync();  // the sums have been read
-            g0 += it.n;
+            g0 += seg->j1 - seg->j0;
+            segment_done();
         }
     }
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     if (warp == 3) tc::tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the pairs that fell into several shares: CTA c takes the pair whose first part is in slot
+// 1 of share c; the next parts are in slot 0 of the shares behind.  One warp a row, four columns a lane.
+__global__ void __launch_bounds__(256) join_kernel(Params p)
+{
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int c = blockIdx.x, row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int32_t pair = p.item1[c];
+    if (pair < 0) return;
+    const int2 e = p.table[pair / p.a.h];
+    Item it;
+    it.load(p.a, e.x, e.y);
+    if ((row & (T - 1)) >= it.rows(row / T)) return;
+    int32_t parts = 1;
+    while (c + parts < p.grid && p.item0[c + parts] == pair) ++parts;
+    auto at = [&](int32_t j) { return (2 * static_cast<int64_t>(c + j) + (j == 0 ? 1 : 0)) * kBlock + row; };
+    float m = -INFINITY, l = 0.f, lr = 0.f;
+    for (int32_t j = 0; j < parts; ++j) m = fmaxf(m, p.ml[at(j)].x);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int32_t j = 0; j < parts; ++j) {
+        const float4 ml = p.ml[at(j)];
+        if (ml.x == -INFINITY) continue;  // a part in which the row saw nothing (its sums may not be written)
+        const float f = ex2_approx(ml.x - m);
+        const float4 x = *reinterpret_cast<const float4 *>(p.part + at(j) * DV + 4 * lane);
+        l += f * ml.y;
+        lr += f * ml.z;
+        o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+    }
+    const float inv = lr > 0.f ? 1.f / lr : 0.f;
+    const int64_t out_row = static_cast<int64_t>(it.q0 + row) * p.a.h + pair % p.a.h;
+    uint2 v = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.a.out) + out_row * DV)[lane] = v;
+    if (lane == 0 && p.a.lse != nullptr) p.a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // Boxes of 64 columns x 128 tokens of a bf16 [tokens][heads][cols] tensor (strides in elements), 128-byte
@@ -597,22 +814,41 @@ bool encode(CUtensorMap *m, const void *base, int64_t cols, int64_t heads, int64
 
 }  // namespace
 
-size_t latent_prefill_workspace(int64_t total_q, int64_t num_seqs, int32_t)
+namespace {
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// [status and counts | blocks | offsets | who holds parts | their statistics | parts]; returns the size.
+size_t layout(char *ws, int64_t total_q, int64_t num_seqs, Params *p)
 {
-    const size_t n = static_cast<size_t>(blocks_bound(total_q, num_seqs));
-    return 256 + n * sizeof(int2) + static_cast<size_t>(num_seqs + 1) * 4;
+    const size_t n = static_cast<size_t>(blocks_bound(total_q, num_seqs)), grid = static_cast<size_t>(sm_count());
+    const size_t before = 256, table = before + (n + 1) * 8, seq = table + n * 8, items = up256(seq + (num_seqs + 1) * 4);
+    const size_t ml = up256(items + 8 * grid), part = ml + 2 * grid * kBlock * 16, end = part + 2 * grid * kBlock * DV * 4;
+    if (p != nullptr) {
+        p->max_blocks = static_cast<int64_t>(n);
+        p->grid = static_cast<int32_t>(grid);
+        p->status = reinterpret_cast<int32_t *>(ws);
+        p->n_blocks = p->status + 1;
+        p->whole = p->status + 2;
+        p->before = reinterpret_cast<int64_t *>(ws + before);
+        p->table = reinterpret_cast<int2 *>(ws + table);
+        p->seq_off = reinterpret_cast<int32_t *>(ws + seq);
+        p->item0 = reinterpret_cast<int32_t *>(ws + items);
+        p->item1 = p->item0 + grid;
+        p->ml = reinterpret_cast<float4 *>(ws + ml);
+        p->part = reinterpret_cast<float *>(ws + part);
+    }
+    return end;
 }
+}  // namespace
+
+size_t latent_prefill_workspace(int64_t total_q, int64_t num_seqs, int32_t) { return layout(nullptr, total_q, num_seqs, nullptr); }
 
 cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st)
 {
     Params p{};
     p.a = a;
     p.scale_log2 = a.scale * kLog2e;
-    p.max_blocks = blocks_bound(a.total_q, a.num_seqs);
-    p.status = static_cast<int32_t *>(a.workspace);
-    p.n_blocks = p.status + 1;
-    p.table = reinterpret_cast<int2 *>(static_cast<char *>(a.workspace) + 256);
-    p.seq_off = reinterpret_cast<int32_t *>(p.table + p.max_blocks);
+    layout(static_cast<char *>(a.workspace), a.total_q, a.num_seqs, &p);
     Maps maps{};
     int32_t plain;  // q's heads lie within a token (or there is one), k_rope has one
     if (!encode(&maps.q, a.q, DQ, a.h, a.total_q, DQ, static_cast<int64_t>(a.h) * DQ, &plain)) return cudaErrorInvalidValue;
@@ -629,9 +865,19 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st)
     cudaFuncAttributes at;
     if ((e = cudaFuncGetAttributes(&at, latent_prefill_kernel)) != cudaSuccess) return e;
     if (at.numRegs != 96) return cudaErrorInvalidConfiguration;
-    const int64_t items = p.max_blocks * a.h, sms = sm_count();
-    latent_prefill_kernel<<<static_cast<unsigned>(items < sms ? items : sms), kThreads, kSmem, st>>>(p, maps);
-    return cudaGetLastError();
+    latent_prefill_kernel<<<p.grid, kThreads, kSmem, st>>>(p, maps);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (a.total_k <= kCutTiles * T) return cudaSuccess;  // no pair is long enough to be cut
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.grid, kBlock / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel, p);
 }
 
 }  // namespace kda

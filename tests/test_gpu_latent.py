@@ -288,6 +288,19 @@ def test_prefill_longer_batch_is_repeatable():
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("heads", [3, 16])
+def test_prefill_many_prompts(heads):
+    # far more (block, head) pairs than SMs: whole pairs, longest first; the other tests' few pairs are cut into equal shares
+    nq = [130, 128, 1, 0, 300, 64, 257] * 60
+    nk = [n + (i % 5) * 77 for i, n in enumerate(nq)]
+    check_prefill(nq, nk, heads, seed=heads)
+
+
+@pytest.mark.parametrize("nq,nk,heads", [([256], [5000], 1), ([40, 600], [9000, 3000], 2), ([1, 1, 1], [20000, 1, 700], 4), ([513], [513], 1)])
+def test_prefill_pairs_cut_over_many_shares(nq, nk, heads):
+    check_prefill(nq, nk, heads, seed=len(nq) + heads)
+
+
 def test_prefill_contiguous_and_head_major_inputs_agree_on_another_stream():
     q, kn, kr, v, cu_q, cu_k = prompt_batch([150, 61], [150, 200], 5, seed=3)
     out, lse = run_prefill(q, kn, kr, v, cu_q, cu_k)
