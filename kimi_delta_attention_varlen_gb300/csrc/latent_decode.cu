@@ -11,7 +11,7 @@
 // several shares leaves unnormalised parts in the workspace, and a second kernel joins them in order
 // of their tiles (so the result does not depend on which CTA was first).
 //
-// Warps of a CTA: one issues the TMA copies, one the MMAs of each product, four do the softmax and
+// Warps of a CTA: two issue the TMA copies, one the MMAs of each product, four do the softmax and
 // the epilogue.
 //   S   = Q X^T        M = 64 (rows; fewer than 64 leave lanes unused), N = T tokens, K = dl + 64
 //   O^T = C^T P^T      M = 128 value dimensions (dl / 128 of them), N rows, K = T tokens
@@ -50,6 +50,7 @@ constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kLazy = 8.f;  // log2 of the growth that forces a rescale
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kStatusExpired = 6;
+constexpr int kJoinCtas = 6;  // a SM: as many as stay resident
 
 template <int DL_, int N_> struct Cfg {
     static constexpr int DL = DL_, N = N_;
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
         if (cta == 0) *p.status = 0;
         p.item0[cta] = p.item1[cta] = -1;
     }
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the join's CTAs may come and wait
     // this CTA's share [w0, w1) of the line: the tiles before each thread's slice of the requests
     const int64_t per = (p.a.batch + kThreads - 1) / kThreads, r_lo = per * tid;
     const int64_t r_hi = r_lo + per < p.a.batch ? r_lo + per : p.a.batch;
@@ -246,8 +248,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
         return !gave_up;
     };
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 3) {
         // ---------------------------------------------------------------- copies
+        // Warp 0 copies the queries and the first half of a tile's pairs, warp 3 the other pairs and the rope panel:
+        // small pages make many copies (16 tokens: 36 a tile), which one warp issues in about a microsecond.
+        const int part = warp == 0 ? 0 : 1, u0 = part * (C::PAIRS / 2), u1 = u0 + C::PAIRS / 2;
         const int32_t br = p.box_rows, page = static_cast<int32_t>(p.a.page);
         // page (an out-of-range coordinate, read as zeros, where the number is invalid) and row of chunk `lane`
         auto lookup = [&](const Walk &x, int32_t *pg, int32_t *row) {
@@ -260,15 +265,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
             }
         };
         auto all_wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
-        int32_t pg = 0, row = 0, k = 0, i = 0, segs = 0;
+        int32_t pg = 0, row = 0, i = 0, segs = 0;
         if (total > 0) lookup(w, &pg, &row);
         bool ok = true;  // the same in every lane
-        for (; i < total; ++i) {
+        for (; i < total && ok; ++i) {
             Walk nx = w;
             nx.next(p);
             int32_t pg_next = 0, row_next = 0;
             if (i + 1 < total) lookup(nx, &pg_next, &row_next);
-            if (i == 0 || w.first()) {
+            if (part == 0 && (i == 0 || w.first())) {
                 if (segs > 0 && !(ok = all_wait(&bar.q_free, (segs - 1) & 1))) break;
                 const int y = static_cast<int>(w.r * p.rows + w.group * N);
                 if (elect_one()) {
@@ -280,8 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
             }
             const int32_t valid = w.n - w.tile * T < T ? w.n - w.tile * T : T;
             const int32_t chunks = (valid + br - 1) / br;
-            for (int u = 0; u < C::PAIRS; ++u, ++k) {
-                const int s = k % C::RING;
+            for (int u = u0; u < u1 && ok; ++u) {
+                const int k = i * C::PAIRS + u, s = k % C::RING;
                 if (!(ok = all_wait(&bar.empty[s], ((k / C::RING) & 1) ^ 1))) break;
                 if (elect_one()) mbar_arrive_expect_tx(&bar.full[s], 2 * chunks * br * 128);
                 __syncwarp();
@@ -295,20 +300,26 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                     __syncwarp();
                 }
             }
-            const int s = i % C::ROPE;
-            if (!ok || !(ok = all_wait(&bar.rope_empty[s], ((i / C::ROPE) & 1) ^ 1))) break;
-            if (elect_one()) mbar_arrive_expect_tx(&bar.rope_full[s], chunks * br * 128);
-            __syncwarp();
-            for (int32_t c = 0; c < chunks; ++c) {
-                const int32_t z = __shfl_sync(0xffffffffu, pg, c), y = __shfl_sync(0xffffffffu, row, c);
-                if (elect_one()) tma_load_3d(smem + C::OFF_ROPE + s * C::PB + c * br * 128, &maps.cache, DL, y, z, &bar.rope_full[s]);
+            if (part == 1 && ok) {
+                const int s = i % C::ROPE;
+                if (!(ok = all_wait(&bar.rope_empty[s], ((i / C::ROPE) & 1) ^ 1))) break;
+                if (elect_one()) mbar_arrive_expect_tx(&bar.rope_full[s], chunks * br * 128);
                 __syncwarp();
+                for (int32_t c = 0; c < chunks; ++c) {
+                    const int32_t z = __shfl_sync(0xffffffffu, pg, c), y = __shfl_sync(0xffffffffu, row, c);
+                    if (elect_one()) tma_load_3d(smem + C::OFF_ROPE + s * C::PB + c * br * 128, &maps.cache, DL, y, z, &bar.rope_full[s]);
+                    __syncwarp();
+                }
             }
             w = nx, pg = pg_next, row = row_next;
         }
-        if (!ok && lane == 0) {  // gave up: the copies in flight land before the CTA ends
-            for (int32_t e = k > C::RING ? k - C::RING : 0; e < k; ++e) mbar_wait(&bar.full[e % C::RING], (e / C::RING) & 1, kWaitLimit);
-            for (int32_t e = i > C::ROPE ? i - C::ROPE : 0; e < i; ++e) mbar_wait(&bar.rope_full[e % C::ROPE], (e / C::ROPE) & 1, kWaitLimit);
+        if (!ok && lane == 0) {
+            // gave up: the copies in flight land before the CTA ends (a wait for one that was not begun runs out, bounded)
+            const int32_t k = (i + 1) * C::PAIRS;
+            for (int32_t e = k > C::RING ? k - C::RING : 0; e < k; ++e)
+                if (e % C::PAIRS >= u0 && e % C::PAIRS < u1) mbar_wait(&bar.full[e % C::RING], (e / C::RING) & 1, kWaitLimit);
+            for (int32_t e = i > C::ROPE ? i - C::ROPE : 0; part == 1 && e < i; ++e)
+                mbar_wait(&bar.rope_full[e % C::ROPE], (e / C::ROPE) & 1, kWaitLimit);
             if (segs > 0) mbar_wait(&bar.q_full, (segs - 1) & 1, kWaitLimit);
         }
     } else if (warp == 1 && total > 0) {
@@ -588,56 +599,155 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
     if (warp == 3) tc::tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of the items that fell into several shares: CTA (c, row) takes the item whose first
-// part is in slot 1 of share c; the next parts are in slot 0 of the shares behind.
+// Joins the parts of the items that fell into several shares: an item's first part is in slot 1 of some share
+// c, the next ones are in slot 0 of the shares behind.  Every CTA lists those items (a look at two words a
+// share), then takes every grid-th unit of work: eight rows of an item of few parts, one row a warp (a loaded
+// batch: about 150 items of two or three parts), or one row of an item of many, the parts dealt out to the
+// whole CTA (one long request: 32 rows of 152 parts).
+constexpr int kFewParts = 8;
+
 template <int DL, int N>
-__global__ void __launch_bounds__(512) latent_join_kernel(Params p, int32_t shares)
+__global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shares)
 {
-    constexpr int PER = DL / 128;
-    __shared__ float acc[3][DL];
-    const int c = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, sub = tid >> 7, d = tid & 127;
+    constexpr int kLanes = DL / 4, kSubs = 256 / kLanes, kAhead = 8;  // a row's float4s; parts at once; in flight per thread
+    extern __shared__ float weight[];  // [shares] weights, then per listed item: share of its first part, parts, units before it
+    int32_t *const first = reinterpret_cast<int32_t *>(weight + shares), *const parts_of = first + shares, *const before = parts_of + shares;
+    __shared__ float4 acc[kSubs][kLanes];
+    __shared__ float sum[2], top;
+    __shared__ int32_t listed, units;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t per = p.rows < N ? p.rows : N;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int32_t item = p.item1[c];
-    if (item < 0) return;
-    const int64_t r = item / p.groups;
-    const int rr = item % p.groups * N + row;
-    if (rr >= p.rows) return;
-    int32_t parts = 1;
-    while (c + parts < shares && p.item0[c + parts] == item) ++parts;
-    auto at = [&](int32_t j) { return (static_cast<int64_t>(2) * (c + j) + (j == 0 ? 1 : 0)) * N + row; };
-    float m = -INFINITY, l = 0.f, lr = 0.f;
-    for (int32_t j = 0; j < parts; ++j) m = fmaxf(m, p.ml[at(j)].x);
-    const float base = m == -INFINITY ? 0.f : m;
-    float o[PER];
+    for (int32_t j = tid; j < shares; j += 256) parts_of[j] = 1;
+    __syncthreads();
+    if (warp == 0) {
+        int32_t n = 0;
+        for (int32_t j0 = 0; j0 < shares; j0 += 32) {
+            const int32_t j = j0 + lane;
+            const bool head = j < shares && p.item1[j] >= 0, more = j < shares && p.item0[j] >= 0;
+            const uint32_t all = __ballot_sync(0xffffffffu, head);
+            const int32_t rank = n + __popc(all & ((1u << lane) - 1));  // items begun before share j
+            if (head) first[rank] = j;
+            if (more) atomicAdd(&parts_of[rank - 1], 1);
+            n += __popc(all);
+        }
+        __syncwarp();
+        int32_t sum_u = 0;
+        for (int32_t k0 = 0; k0 < n; k0 += 32) {
+            const int32_t k = k0 + lane, u = k >= n ? 0 : parts_of[k] > kFewParts ? per : (per + 7) / 8;
+            int32_t s = u;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = 0.f;
-    for (int32_t j = 0; j < parts; ++j) {
-        const float4 ml = p.ml[at(j)];
-        const float f = ex2_approx(ml.x - base);
-        l += ml.y * f;
-        lr += ml.z * f;
-    }
-#pragma unroll 4
-    for (int32_t j = sub; j < parts; j += 4) {
-        const float f = ex2_approx(p.ml[at(j)].x - base);
-        const float *x = p.part + at(j) * DL + d;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) o[e] += f * x[128 * e];
-    }
-    if (sub > 0) {
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[sub - 1][d + 128 * e] = o[e];
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t y = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += y;
+            }
+            if (k < n) before[k] = sum_u + s - u;
+            sum_u += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) listed = n, units = sum_u;
     }
     __syncthreads();
-    if (sub > 0) return;
-    const float inv = lr > 0.f ? 1.f / lr : 0.f;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (r * p.rows + rr) * DL + d;
+    for (int32_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        int32_t lo = 0, hi = listed;  // the item with before[lo] <= unit
+        while (lo + 1 < hi) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (before[mid] <= unit) lo = mid;
+            else hi = mid;
+        }
+        const int32_t c = first[lo], parts = parts_of[lo], item = p.item1[c];
+        const int64_t r = item / p.groups;
+        const int32_t row0 = item % p.groups * N;  // the group's first row
+        auto at = [&](int32_t j, int32_t row) { return (static_cast<int64_t>(2) * (c + j) + (j == 0 ? 1 : 0)) * N + row; };
+        auto store = [&](int32_t row, int32_t d, float4 o, float inv) {
+            reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.a.out) + (r * p.rows + row0 + row) * DL)[d] =
+                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        };
+        if (parts <= kFewParts) {
+            const int32_t row = (unit - before[lo]) * 8 + warp;
+            if (row >= per || row0 + row >= p.rows) continue;
+            float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            if (lane < parts) ml = p.ml[at(lane, row)];
+            float m = ml.x;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {
-        const float x = o[e] + acc[0][d + 128 * e] + acc[1][d + 128 * e] + acc[2][d + 128 * e];
-        out[128 * e] = __float2bfloat16_rn(x * inv);
+            for (int o = kFewParts / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            m = __shfl_sync(0xffffffffu, m, 0);
+            const float f = lane < parts ? ex2_approx(ml.x - (m == -INFINITY ? 0.f : m)) : 0.f;
+            float l = f * ml.y, lr = f * ml.z;
+#pragma unroll
+            for (int o = kFewParts / 2; o; o >>= 1) {
+                l += __shfl_xor_sync(0xffffffffu, l, o);
+                lr += __shfl_xor_sync(0xffffffffu, lr, o);
+            }
+            l = __shfl_sync(0xffffffffu, l, 0), lr = __shfl_sync(0xffffffffu, lr, 0);
+            const float inv = lr > 0.f ? 1.f / lr : 0.f;
+            float4 o[kLanes / 32];
+#pragma unroll
+            for (int q = 0; q < kLanes / 32; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int32_t j = 0; j < parts; ++j) {
+                const float4 *x = reinterpret_cast<const float4 *>(p.part + at(j, row) * DL) + lane;
+                const float fj = __shfl_sync(0xffffffffu, f, j);
+#pragma unroll
+                for (int q = 0; q < kLanes / 32; ++q) {
+                    const float4 y = x[32 * q];
+                    o[q].x += fj * y.x, o[q].y += fj * y.y, o[q].z += fj * y.z, o[q].w += fj * y.w;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kLanes / 32; ++q) store(row, lane + 32 * q, o[q], inv);
+            if (lane == 0 && p.a.lse != nullptr) p.a.lse[r * p.rows + row0 + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            continue;
+        }
+        const int32_t row = unit - before[lo], sub = tid / kLanes, d = tid % kLanes;
+        if (row0 + row >= p.rows) continue;
+        if (warp == 0) {
+            float m = -INFINITY, l = 0.f, lr = 0.f;
+            for (int32_t j = lane; j < parts; j += 32) m = fmaxf(m, p.ml[at(j, row)].x);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float base = m == -INFINITY ? 0.f : m;
+            for (int32_t j = lane; j < parts; j += 32) {
+                const float4 ml = p.ml[at(j, row)];
+                const float f = ex2_approx(ml.x - base);
+                weight[j] = f;
+                l += f * ml.y;
+                lr += f * ml.z;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                l += __shfl_xor_sync(0xffffffffu, l, o);
+                lr += __shfl_xor_sync(0xffffffffu, lr, o);
+            }
+            if (lane == 0) sum[0] = l, sum[1] = lr, top = m;
+        }
+        __syncthreads();
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int32_t j0 = sub; j0 < parts; j0 += kSubs * kAhead) {
+            float4 x[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (j0 + kSubs * u < parts) x[u] = *reinterpret_cast<const float4 *>(p.part + at(j0 + kSubs * u, row) * DL + 4 * d);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (j0 + kSubs * u < parts) {
+                    const float f = weight[j0 + kSubs * u];
+                    o.x += f * x[u].x, o.y += f * x[u].y, o.z += f * x[u].z, o.w += f * x[u].w;
+                }
+        }
+        acc[sub][d] = o;
+        __syncthreads();
+        if (sub == 0) {
+#pragma unroll
+            for (int q = 1; q < kSubs; ++q) {
+                const float4 y = acc[q][d];
+                o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+            }
+            store(row, d, o, sum[1] > 0.f ? 1.f / sum[1] : 0.f);
+            if (d == 0 && p.a.lse != nullptr)
+                p.a.lse[r * p.rows + row0 + row] = sum[0] > 0.f ? (top + log2f(sum[0])) * kLn2 : -INFINITY;
+        }
+        __syncthreads();  // weight, sum and acc may be written again
     }
-    if (d == 0 && p.a.lse != nullptr) p.a.lse[r * p.rows + rr] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 int rows_per_group(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
@@ -679,8 +789,9 @@ template <int DL, int N> cudaError_t launch(Params p, cudaStream_t st)
     kern<<<grid, kThreads, C::SMEM, st>>>(p, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, p.rows < N ? p.rows : N);
-    cfg.blockDim = dim3(512);
+    cfg.gridDim = dim3(grid * kJoinCtas);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = static_cast<size_t>(grid) * 16;
     cfg.stream = st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -62,6 +62,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kStatusExpired = 7;
 constexpr int kBuckets = 1024;
 constexpr int kCutTiles = 10;
+constexpr int kJoinCtas = 6;               // a SM: as many as stay resident
 constexpr int kReaders = 3 + 16;           // warps that read a segment
 
 enum Order { kHeadsFirst = 0, kTokensFirst = 1, kOneHead = 2 };  // (x, head, token), (x, token, head), (x, 0, token)
@@ -756,38 +757,62 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
     if (warp == 3) tc::tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of the pairs that fell into several shares: CTA c takes the pair whose first part is in slot
-// 1 of share c; the next parts are in slot 0 of the shares behind.  One warp a row, four columns a lane.
+// Joins the parts of the pairs that fell into several stretches: a pair's first part is in slot 1 of some CTA's
+// slots, the next ones are in slot 0 of the CTAs behind.  Every warp lists those pairs by a look at one word a CTA
+// and takes every n-th (pair, row) of n warps, four columns a lane.
 __global__ void __launch_bounds__(256) join_kernel(Params p)
 {
+    extern __shared__ int32_t heads[];  // [grid]
+    __shared__ int32_t listed;
+    const int lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int c = blockIdx.x, row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int32_t pair = p.item1[c];
-    if (pair < 0) return;
-    const int2 e = p.table[pair / p.a.h];
-    Item it;
-    it.load(p.a, e.x, e.y);
-    if ((row & (T - 1)) >= it.rows(row / T)) return;
-    int32_t parts = 1;
-    while (c + parts < p.grid && p.item0[c + parts] == pair) ++parts;
-    auto at = [&](int32_t j) { return (2 * static_cast<int64_t>(c + j) + (j == 0 ? 1 : 0)) * kBlock + row; };
-    float m = -INFINITY, l = 0.f, lr = 0.f;
-    for (int32_t j = 0; j < parts; ++j) m = fmaxf(m, p.ml[at(j)].x);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int32_t j = 0; j < parts; ++j) {
-        const float4 ml = p.ml[at(j)];
-        if (ml.x == -INFINITY) continue;  // a part in which the row saw nothing (its sums may not be written)
-        const float f = ex2_approx(ml.x - m);
-        const float4 x = *reinterpret_cast<const float4 *>(p.part + at(j) * DV + 4 * lane);
-        l += f * ml.y;
-        lr += f * ml.z;
-        o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+    if (threadIdx.x < 32) {
+        int32_t n = 0;
+        for (int32_t j0 = 0; j0 < p.grid; j0 += 32) {
+            const bool has = j0 + lane < p.grid && p.item1[j0 + lane] >= 0;
+            const uint32_t all = __ballot_sync(0xffffffffu, has);
+            if (has) heads[n + __popc(all & ((1u << lane) - 1))] = j0 + lane;
+            n += __popc(all);
+        }
+        if (lane == 0) listed = n;
     }
-    const float inv = lr > 0.f ? 1.f / lr : 0.f;
-    const int64_t out_row = static_cast<int64_t>(it.q0 + row) * p.a.h + pair % p.a.h;
-    uint2 v = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.a.out) + out_row * DV)[lane] = v;
-    if (lane == 0 && p.a.lse != nullptr) p.a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    __syncthreads();
+    for (int32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5); unit < listed * kBlock; unit += gridDim.x * 8) {
+        const int c = heads[unit / kBlock], row = unit % kBlock;
+        const int32_t pair = p.item1[c];
+        const int2 e = p.table[pair / p.a.h];
+        Item it;
+        it.load(p.a, e.x, e.y);
+        if ((row & (T - 1)) >= it.rows(row / T)) continue;
+        int32_t parts = 1;  // a pair's parts stand next to each other
+        for (int32_t j0 = c + 1; j0 < p.grid; j0 += 32) {
+            const int32_t j = j0 + lane;
+            const uint32_t mine = __ballot_sync(0xffffffffu, j < p.grid && p.item0[j] == pair);
+            parts += __popc(mine);
+            if (mine != 0xffffffffu) break;
+        }
+        auto at = [&](int32_t j) { return (2 * static_cast<int64_t>(c + j) + (j == 0 ? 1 : 0)) * kBlock + row; };
+        float m = -INFINITY, l = 0.f, lr = 0.f;
+        for (int32_t j = lane; j < parts; j += 32) m = fmaxf(m, p.ml[at(j)].x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int32_t j = 0; j < parts; ++j) {
+            const float4 ml = p.ml[at(j)];
+            if (ml.x == -INFINITY) continue;  // a part in which the row saw nothing (its sums may not be written)
+            const float f = ex2_approx(ml.x - m);
+            const float4 x = *reinterpret_cast<const float4 *>(p.part + at(j) * DV + 4 * lane);
+            l += f * ml.y;
+            lr += f * ml.z;
+            o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+        }
+        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+        const int64_t out_row = static_cast<int64_t>(it.q0 + row) * p.a.h + pair % p.a.h;
+        uint2 v = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.a.out) + out_row * DV)[lane] = v;
+        if (lane == 0 && p.a.lse != nullptr) p.a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
 }
 
 // Boxes of 64 columns x 128 tokens of a bf16 [tokens][heads][cols] tensor (strides in elements), 128-byte
@@ -869,8 +894,9 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st)
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (a.total_k <= kCutTiles * T) return cudaSuccess;  // no pair is long enough to be cut
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.grid, kBlock / 8);
+    cfg.gridDim = dim3(p.grid * kJoinCtas);
     cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.grid) * 4;
     cfg.stream = st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
