@@ -573,7 +573,7 @@ typedef struct {
  * Errors: KDA_ERR_NULL, _DTYPE (io or cache not bf16), _LAYOUT, _SHAPE (sizes
  * below 1 (batch below 0), cache h / k not 1 / dl + dr, table_stride < width),
  * _UNSUPPORTED (dl, dr, page_size), _RANGE (scale not positive and finite,
- * batch * L * h >= 2^31, width * page_size >= 2^31, L * h > 2^20), _ALIGN,
+ * batch * L * h >= 2^31, width * page_size >= 2^31, L * h > 65536), _ALIGN,
  * _WORKSPACE, _CUDA.
  * batch == 0 launches nothing.
  * ---------------------------------------------------------------------- */

@@ -443,7 +443,7 @@ int check_page_list(const kda_page_table *t, const void *req, int32_t idx_type, 
 size_t kda_latent_decode_workspace_size(int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr)
 {
     if (batch < 0 || L < 1 || h < 1 || (dl != 256 && dl != 512) || dr != 64) return 0;
-    if (static_cast<int64_t>(L) * h > (1 << 20) || static_cast<__int128>(batch) * L * h >= (INT64_C(1) << 31)) return 0;
+    if (static_cast<int64_t>(L) * h > 65536 || static_cast<__int128>(batch) * L * h >= (INT64_C(1) << 31)) return 0;
     return kda::latent_decode_workspace(batch, L, h, dl);
 }
 
@@ -460,7 +460,7 @@ int kda_latent_decode(const void *q, int32_t io_dtype, int64_t batch, int32_t L,
         c.h != 1 || c.k != static_cast<int64_t>(dl) + dr || (req == nullptr && requests < batch))
         return KDA_ERR_SHAPE;
     if ((dl != 256 && dl != 512) || dr != 64 || c.v % 8 != 0) return KDA_ERR_UNSUPPORTED;
-    if (!valid_scale(scale) || static_cast<int64_t>(L) * h > (1 << 20) || static_cast<__int128>(batch) * L * h >= (INT64_C(1) << 31) ||
+    if (!valid_scale(scale) || static_cast<int64_t>(L) * h > 65536 || static_cast<__int128>(batch) * L * h >= (INT64_C(1) << 31) ||
         static_cast<__int128>(width) * c.v >= (INT64_C(1) << 31) || c.n_rows >= (INT64_C(1) << 31) ||
         static_cast<__int128>(requests) * table_stride > (INT64_C(1) << 60))
         return KDA_ERR_RANGE;

@@ -44,6 +44,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // chunk_prep.cu
 namespace {
 
 constexpr int T = 64;  // tokens a tile
+constexpr int kItemUnits = 3;
 constexpr int kThreads = 256;
 constexpr int kSoftThreads = 128;
 constexpr uint32_t kWaitLimit = 1u << 22;
@@ -94,6 +95,11 @@ __device__ __forceinline__ int32_t length_of(const LatentDecodeArgs &a, int64_t 
 }
 
 __device__ __forceinline__ int32_t tiles_of(int32_t n) { return n > T ? (n - 1) / T + 1 : 1; }
+
+struct Edge {
+    int64_t r, tiles_before;
+    int32_t group, tile;
+};
 
 // Position on the line of tiles.
 struct Walk {
@@ -171,8 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
     __shared__ uint32_t tmem_base;
     __shared__ float corr[2][N], linv[N];  // corr: by parity of the tile, so that a late reader keeps its own
     __shared__ int64_t sums[kThreads / 32];
-    __shared__ int64_t start_r;
-    __shared__ int32_t start_rest;
+    __shared__ Edge edge[2];
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
     const int cta = blockIdx.x;
@@ -192,11 +197,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
         p.item0[cta] = p.item1[cta] = -1;
     }
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the join's CTAs may come and wait
-    // this CTA's share [w0, w1) of the line: the tiles before each thread's slice of the requests
+    // This CTA's share [w0, w1) of the line, on which a (request, group) takes its tiles and kItemUnits more: the
+    // work that comes with it whatever its length (queries, first tile's latency, epilogue).
     const int64_t per = (p.a.batch + kThreads - 1) / kThreads, r_lo = per * tid;
     const int64_t r_hi = r_lo + per < p.a.batch ? r_lo + per : p.a.batch;
-    int64_t mine = 0;
-    for (int64_t r = r_lo; r < r_hi; ++r) mine += tiles_of(length_of(p.a, slot_of(p.a, r)));
+    int64_t mine = 0;  // units of this thread's slice of the requests, of one group
+    for (int64_t r = r_lo; r < r_hi; ++r) mine += tiles_of(length_of(p.a, slot_of(p.a, r))) + kItemUnits;
     int64_t scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -214,30 +220,38 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
         all += sums[w];
     }
     all *= p.groups;
-    const int64_t shares = all < gridDim.x ? all : gridDim.x;
-    const int64_t w0 = cta < shares ? all * cta / shares : all, w1 = cta < shares ? all * (cta + 1) / shares : all;
-    const int32_t total = static_cast<int32_t>(w1 - w0);
     before *= p.groups;
-    if (w0 >= before && w0 < before + mine * p.groups) {
-        int64_t left = w0 - before, r = r_lo;
-        for (;; ++r) {
-            const int64_t t = static_cast<int64_t>(tiles_of(length_of(p.a, slot_of(p.a, r)))) * p.groups;
-            if (left < t) break;
-            left -= t;
+    const int64_t shares = all < gridDim.x ? all : gridDim.x;
+    // the ends of the share as (request, group, tile) and as a count of tiles before it
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int64_t at = cta + e <= shares ? all * (cta + e) / shares : all;
+        if (tid == 0 && at == all) edge[e] = Edge{0, all - kItemUnits * p.groups * p.a.batch, 0, 0};
+        if (at >= before && at < before + mine * p.groups) {
+            int64_t left = at - before, r = r_lo;
+            int32_t tiles;
+            for (;; ++r) {
+                tiles = tiles_of(length_of(p.a, slot_of(p.a, r)));
+                const int64_t u = static_cast<int64_t>(tiles + kItemUnits) * p.groups;
+                if (left < u) break;
+                left -= u;
+            }
+            const int32_t group = static_cast<int32_t>(left / (tiles + kItemUnits)), x = static_cast<int32_t>(left % (tiles + kItemUnits));
+            const int32_t tile = x > kItemUnits ? x - kItemUnits : 0;
+            edge[e] = Edge{r, at - left - kItemUnits * p.groups * r + static_cast<int64_t>(group) * tiles + tile, group, tile};
         }
-        start_r = r;
-        start_rest = static_cast<int32_t>(left);
     }
     __syncthreads();
     const uint32_t tmem = tmem_base;
     constexpr uint32_t kColS = 256;
 
+    const int32_t total = static_cast<int32_t>(edge[1].tiles_before - edge[0].tiles_before);
     Walk w{};
     if (total > 0) {
-        w.r = start_r;
+        w.r = edge[0].r;
         w.load(p.a);
-        w.group = start_rest / w.tiles;
-        w.tile = start_rest % w.tiles;
+        w.group = edge[0].group;
+        w.tile = edge[0].tile;
     }
     bool gave_up = false;
     auto wait = [&](uint64_t *b, uint32_t parity) {
@@ -618,17 +632,22 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t per = p.rows < N ? p.rows : N;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    for (int32_t j = tid; j < shares; j += 256) parts_of[j] = 1;
+    int32_t *const head_of = before, *const more_of = reinterpret_cast<int32_t *>(weight);  // until they are needed
+    for (int32_t j = tid; j < shares; j += 256) {
+        parts_of[j] = 1;
+        head_of[j] = p.item1[j];
+        more_of[j] = p.item0[j];
+    }
     __syncthreads();
     if (warp == 0) {
         int32_t n = 0;
         for (int32_t j0 = 0; j0 < shares; j0 += 32) {
             const int32_t j = j0 + lane;
-            const bool head = j < shares && p.item1[j] >= 0, more = j < shares && p.item0[j] >= 0;
+            const bool head = j < shares && head_of[j] >= 0;
             const uint32_t all = __ballot_sync(0xffffffffu, head);
             const int32_t rank = n + __popc(all & ((1u << lane) - 1));  // items begun before share j
             if (head) first[rank] = j;
-            if (more) atomicAdd(&parts_of[rank - 1], 1);
+            if (j < shares && more_of[j] >= 0) atomicAdd(&parts_of[rank - 1], 1);
             n += __popc(all);
         }
         __syncwarp();
@@ -786,6 +805,11 @@ template <int DL, int N> cudaError_t launch(Params p, cudaStream_t st)
     auto kern = latent_decode_kernel<DL, N>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
+    // the join keeps the main kernel's split between shared memory and L1 cache: changing it between kernels that
+    // follow each other costs microseconds
+    auto join = latent_join_kernel<DL, N>;
+    if ((e = cudaFuncSetAttribute(join, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
+        return e;
     kern<<<grid, kThreads, C::SMEM, st>>>(p, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -798,7 +822,7 @@ template <int DL, int N> cudaError_t launch(Params p, cudaStream_t st)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_join_kernel<DL, N>, p, static_cast<int32_t>(grid));
+    return cudaLaunchKernelEx(&cfg, join, p, static_cast<int32_t>(grid));
 }
 
 }  // namespace

@@ -881,9 +881,13 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st)
                           !encode(&maps.v, a.v, DV, a.h, a.total_k, a.v_head, a.v_token, &p.v_order) ||
                           !encode(&maps.kr, a.k_rope, DR, 1, a.total_k, DR, a.kr_token, &plain)))
         return cudaErrorInvalidValue;
+    // all three keep one split between shared memory and L1 cache: changing it between kernels costs microseconds
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(join_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
+        return e;
     plan_kernel<<<1, 1024, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     // the register split (setmaxnreg) needs a launch with exactly 96 registers a thread
