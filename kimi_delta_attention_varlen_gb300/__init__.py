@@ -58,8 +58,8 @@ def _itype_code(t: torch.Tensor) -> int:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle itself: building a torch.cuda.Stream takes microseconds, a small call's worth
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -78,10 +78,10 @@ def cache_descriptor(cache: torch.Tensor) -> KdaCache:
     """kda_cache for a [N, H, V, K] view with a dense inner block."""
     _need(cache.dim() == 4, "cache must be a 4-D view [N, H, V, K]")
     N, H, V, K = cache.shape
-    for d, want in ((1, V * K), (2, K), (3, 1)):
-        _need(cache.size(d) == 1 or cache.stride(d) == want,
-              "cache rows must hold a dense [H, V, K] block")
-    return KdaCache(cache.data_ptr(), _dtype_code(cache), 0, N, H, V, K, cache.stride(0))
+    row, head, vec, elem = cache.stride()
+    _need((H == 1 or head == V * K) and (V == 1 or vec == K) and (K == 1 or elem == 1),
+          "cache rows must hold a dense [H, V, K] block")
+    return KdaCache(cache.data_ptr(), _dtype_code(cache), 0, N, H, V, K, row)
 
 
 def _index_vector(idx: torch.Tensor) -> None:
@@ -407,24 +407,25 @@ def kda_latent_decode(q, cache, block_table, seq_lens, out, workspace, *, latent
     _need(q.dim() == 4, "q must be [R, L, H, dl + dr]")
     R, L, H, D = q.shape
     dl = int(latent_dim)
-    _need(q.is_contiguous() and tuple(out.shape) == (R, L, H, dl) and out.is_contiguous(),
+    _need(q.is_contiguous() and out.is_contiguous() and out.shape == (R, L, H, dl),
           "q and out must be contiguous [R, L, H, dl + dr] and [R, L, H, dl]")
     _need(out.dtype == q.dtype, "q and out share a dtype")
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and
-          (block_table.shape[1] == 1 or block_table.stride(1) == 1), "block_table must be int32 [requests, width], unit inner stride")
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2, "block_table must be int32 [requests, width]")
     B, W = block_table.shape
-    _need(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and tuple(seq_lens.shape) == (B,),
+    row, elem = block_table.stride()
+    _need(W == 1 or elem == 1, "block_table must have a unit inner stride")
+    _need(seq_lens.dtype == torch.int32 and seq_lens.is_contiguous() and seq_lens.shape == (B,),
           "seq_lens must be contiguous int32 [requests]")
     if req is not None:
         _index_vector(req)
         _need(req.numel() == R, "req must hold one row per batch entry")
     if lse is not None:
-        _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (R, L, H),
+        _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (R, L, H),
               "lse must be contiguous float32 [R, L, H]")
     _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be a uint8 tensor")
     d = cache_descriptor(cache)
     rc = lib().kda_latent_decode(_ptr(q), _dtype_code(q), R, L, H, dl, D - dl, float(scale), ctypes.byref(d),
-                                 _ptr(block_table), B, W, block_table.stride(0) if B > 1 else max(W, block_table.stride(0)),
+                                 _ptr(block_table), B, W, row if B > 1 else max(W, row),
                                  _ptr(seq_lens), _ptr(req), 0 if req is None else _itype_code(req), _ptr(out), _ptr(lse),
                                  _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "kda_latent_decode")
@@ -445,24 +446,26 @@ def kda_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, out, workspace, *, scal
     Tq, H, D = q.shape
     Tk, _, dn = k_nope.shape
     dv, dr = v.shape[2], k_rope.shape[1]
-    _need(tuple(k_nope.shape) == (Tk, H, dn) and tuple(v.shape) == (Tk, H, dv) and tuple(k_rope.shape) == (Tk, dr) and
-          D == dn + dr, "shapes must agree: q [Tq, H, dn + dr], k_nope [Tk, H, dn], k_rope [Tk, dr], v [Tk, H, dv]")
-    _need(q.is_contiguous() and out.is_contiguous() and tuple(out.shape) == (Tq, H, dv), "q and out must be contiguous")
-    for name, t in (("k_nope", k_nope), ("k_rope", k_rope), ("v", v)):
-        _need(t.shape[-1] == 1 or t.stride(-1) == 1, f"{name} must have a unit inner stride")
-    _need(len({t.dtype for t in (q, k_nope, k_rope, v, out)}) == 1, "q, k_nope, k_rope, v, out share a dtype")
+    _need(k_nope.shape == (Tk, H, dn) and v.shape == (Tk, H, dv) and k_rope.shape == (Tk, dr) and D == dn + dr,
+          "shapes must agree: q [Tq, H, dn + dr], k_nope [Tk, H, dn], k_rope [Tk, dr], v [Tk, H, dv]")
+    _need(q.is_contiguous() and out.is_contiguous() and out.shape == (Tq, H, dv), "q and out must be contiguous")
+    kn_token, kn_head, kn_elem = k_nope.stride()
+    v_token, v_head, v_elem = v.stride()
+    kr_token, kr_elem = k_rope.stride()
+    _need((dn == 1 or kn_elem == 1) and (dv == 1 or v_elem == 1) and (dr == 1 or kr_elem == 1),
+          "k_nope, k_rope and v must have a unit inner stride")
+    _need(q.dtype == k_nope.dtype == k_rope.dtype == v.dtype == out.dtype, "q, k_nope, k_rope, v, out share a dtype")
     B = cu_q.numel() - 1
-    for name, t in (("cu_q", cu_q), ("cu_k", cu_k)):
-        _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() == B + 1 and B >= 1,
-              f"{name} must be a contiguous int32 tensor of B + 1 >= 2 offsets")
+    _need(cu_q.dtype == torch.int32 and cu_q.is_contiguous() and B >= 1 and cu_k.dtype == torch.int32 and
+          cu_k.is_contiguous() and cu_k.numel() == B + 1, "cu_q and cu_k must be contiguous int32 tensors of B + 1 >= 2 offsets")
     if lse is not None:
-        _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (Tq, H),
+        _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (Tq, H),
               "lse must be contiguous float32 [Tq, H]")
     _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be a uint8 tensor")
     if scale is None:
         scale = D ** -0.5
-    rc = lib().kda_latent_prefill(_ptr(q), _dtype_code(q), _ptr(k_nope), k_nope.stride(0), k_nope.stride(1), _ptr(k_rope),
-                                  k_rope.stride(0), _ptr(v), v.stride(0), v.stride(1), _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, H,
+    rc = lib().kda_latent_prefill(_ptr(q), _dtype_code(q), _ptr(k_nope), kn_token, kn_head, _ptr(k_rope),
+                                  kr_token, _ptr(v), v_token, v_head, _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, H,
                                   dn, dr, dv, float(scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
                                   _stream(stream))
     _check(rc, "kda_latent_prefill")
@@ -490,11 +493,12 @@ def kda_pages_workspace_size(n_pages: int, count: int) -> int:
 def _same_lists(*lists) -> None:
     for t in lists:
         _index_vector(t)
-        _need(t.numel() == lists[0].numel() and t.dtype == lists[0].dtype, "index lists: same length and dtype")
+    _need(all(t.numel() == lists[0].numel() and t.dtype == lists[0].dtype for t in lists[1:]), "index lists: same length and dtype")
 
 
 def _int32_vector(name: str, t, n: int) -> None:
-    _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n, f"{name} must be a contiguous int32 tensor of {n}")
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n}")
 
 
 def kda_pages_fork(table: KdaPageTable, src, dst, stream=None) -> None:
@@ -520,8 +524,9 @@ def kda_pages_reserve(table: KdaPageTable, req, new_tokens, move_src, move_dst, 
     too short (then nothing changed); moves; pages asked for; pages free before."""
     _index_vector(req)
     n = req.numel()
-    for name, t in (("new_tokens", new_tokens), ("move_src", move_src), ("move_dst", move_dst)):
-        _int32_vector(name, t, n)
+    _int32_vector("new_tokens", new_tokens, n)
+    _int32_vector("move_src", move_src, n)
+    _int32_vector("move_dst", move_dst, n)
     _int32_vector("info", info, 4)
     _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be a uint8 tensor")
     rc = lib().kda_pages_reserve(ctypes.byref(table), _ptr(req), _itype_code(req), _ptr(new_tokens), n, _ptr(move_src),

@@ -102,6 +102,8 @@ _lib = None
 def lib():
     """Load libkda.so once and declare the C signatures."""
     global _lib
+    if _lib is not None:  # set once, when complete
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
