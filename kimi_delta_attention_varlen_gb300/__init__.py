@@ -379,13 +379,16 @@ def page_table_descriptor(block_table: torch.Tensor, seq_lens: torch.Tensor, ref
     """kda_page_table over [requests, width] block tables (unit inner stride), [requests]
     lengths and [n_pages] refcounts, all int32 on the device.  The calls write through it, so
     it keeps the tensors alive."""
-    _need(all(t.dtype == torch.int32 for t in (block_table, seq_lens, refcount)), "page tables must be int32")
-    _need(block_table.dim() == 2 and (block_table.shape[1] == 1 or block_table.stride(1) == 1),
-          "block_table must be [requests, width] with a unit inner stride")
+    _need(block_table.dtype == torch.int32 and seq_lens.dtype == torch.int32 and refcount.dtype == torch.int32,
+          "page tables must be int32")
+    _need(block_table.dim() == 2, "block_table must be [requests, width]")
     R, W = block_table.shape
-    _need(seq_lens.is_contiguous() and tuple(seq_lens.shape) == (R,), "seq_lens must be contiguous [requests]")
+    stride, elem = block_table.stride()
+    _need(W == 1 or elem == 1, "block_table must have a unit inner stride")
+    _need(seq_lens.is_contiguous() and seq_lens.shape == (R,), "seq_lens must be contiguous [requests]")
     _need(refcount.is_contiguous() and refcount.dim() == 1, "refcount must be contiguous [n_pages]")
-    stride = block_table.stride(0) if R > 1 else max(W, block_table.stride(0))
+    if R == 1:  # a stride of a size-one dimension means nothing
+        stride = max(W, stride)
     d = KdaPageTable(block_table.data_ptr(), seq_lens.data_ptr(), refcount.data_ptr(), R, W, stride, refcount.numel(),
                      int(page_size), 0)
     d.tensors = (block_table, seq_lens, refcount)

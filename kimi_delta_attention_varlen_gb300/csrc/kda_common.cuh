@@ -280,6 +280,13 @@ __device__ __forceinline__ void cp_async_wait_all()
     asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;\n" ::: "memory");
 }
 
+// ------------------------------------------- programmatic dependent launch --
+
+// Waits until the kernels before this one on the stream have completed and their writes are visible.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// Lets the next kernel on the stream come (it still waits for this one's end in after_previous()).
+__device__ __forceinline__ void before_next() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
 // ------------------------------------------------------ cache-hinted I/O --
 
 __device__ __forceinline__ uint4 ld_nc_v4(const void *p)

@@ -23,6 +23,25 @@ struct CacheDesc {
     int64_t n_rows, h, v, k, row_stride;
 };
 
+// Launches `kern` so that it may come onto the GPU while the kernel before it on the stream still runs
+// (programmatic dependent launch).  Such a kernel calls after_previous() before it touches any memory that
+// another kernel writes or reads, and before_next() where the next one may come.
+template <class Kern, class... Args>
+cudaError_t launch_overlapped(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 constexpr int kChunk = 64;  // tokens per chunk (the report's extend listing fixes 64)
 // Channels per CTA of the short convolution; the per-sequence and update kernels put these
 // channel blocks in the grid's y dimension (at most 65,535 of them).

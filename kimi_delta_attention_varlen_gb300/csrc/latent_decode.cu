@@ -193,10 +193,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
         mbar_init(&bar.p, kSoftThreads), mbar_init(&bar.o, 1);
         for (int j = 0; j < 2; ++j) mbar_init(&bar.s_free[j], kSoftThreads), mbar_init(&bar.drain[j], 1);
         fence_mbar_init();
+    }
+    before_next();
+    after_previous();
+    if (tid == 0) {
         if (cta == 0) *p.status = 0;
         p.item0[cta] = p.item1[cta] = -1;
     }
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the join's CTAs may come and wait
     // This CTA's share [w0, w1) of the line, on which a (request, group) takes its tiles and kItemUnits more: the
     // work that comes with it whatever its length (queries, first tile's latency, epilogue).
     const int64_t per = (p.a.batch + kThreads - 1) / kThreads, r_lo = per * tid;
@@ -631,7 +634,8 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
     __shared__ int32_t listed, units;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t per = p.rows < N ? p.rows : N;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    before_next();
+    after_previous();
     int32_t *const head_of = before, *const more_of = reinterpret_cast<int32_t *>(weight);  // until they are needed
     for (int32_t j = tid; j < shares; j += 256) {
         parts_of[j] = 1;
@@ -810,19 +814,8 @@ template <int DL, int N> cudaError_t launch(Params p, cudaStream_t st)
     auto join = latent_join_kernel<DL, N>;
     if ((e = cudaFuncSetAttribute(join, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
         return e;
-    kern<<<grid, kThreads, C::SMEM, st>>>(p, maps);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid * kJoinCtas);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = static_cast<size_t>(grid) * 16;
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join, p, static_cast<int32_t>(grid));
+    if ((e = launch_overlapped(kern, dim3(grid), dim3(kThreads), C::SMEM, st, p, maps)) != cudaSuccess) return e;
+    return launch_overlapped(join, dim3(grid * kJoinCtas), dim3(256), static_cast<size_t>(grid) * 16, st, p, static_cast<int32_t>(grid));
 }
 
 }  // namespace

@@ -206,6 +206,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(Params p)
     __shared__ int64_t sums[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const LatentPrefillArgs &a = p.a;
+    before_next();
+    after_previous();
     auto scan = [&](int64_t x, int64_t *total) {  // exclusive prefix over the CTA
         int64_t s = x;
 #pragma unroll
@@ -363,6 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    before_next();
+    after_previous();
     const uint32_t tmem = uniform(sh.tmem_base);
     uint32_t nseg = 0;  // segments taken
 
@@ -765,7 +769,8 @@ __global__ void __launch_bounds__(256) join_kernel(Params p)
     extern __shared__ int32_t heads[];  // [grid]
     __shared__ int32_t listed;
     const int lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    before_next();
+    after_previous();
     if (threadIdx.x < 32) {
         int32_t n = 0;
         for (int32_t j0 = 0; j0 < p.grid; j0 += 32) {
@@ -886,28 +891,16 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st)
     if ((e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess ||
         (e = cudaFuncSetAttribute(join_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
         return e;
-    plan_kernel<<<1, 1024, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_overlapped(plan_kernel, dim3(1), dim3(1024), 0, st, p)) != cudaSuccess) return e;
     e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     // the register split (setmaxnreg) needs a launch with exactly 96 registers a thread
     cudaFuncAttributes at;
     if ((e = cudaFuncGetAttributes(&at, latent_prefill_kernel)) != cudaSuccess) return e;
     if (at.numRegs != 96) return cudaErrorInvalidConfiguration;
-    latent_prefill_kernel<<<p.grid, kThreads, kSmem, st>>>(p, maps);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_overlapped(latent_prefill_kernel, dim3(p.grid), dim3(kThreads), kSmem, st, p, maps)) != cudaSuccess) return e;
     if (a.total_k <= kCutTiles * T) return cudaSuccess;  // no pair is long enough to be cut
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.grid * kJoinCtas);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = static_cast<size_t>(p.grid) * 4;
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel, p);
+    return launch_overlapped(join_kernel, dim3(p.grid * kJoinCtas), dim3(256), static_cast<size_t>(p.grid) * 4, st, p);
 }
 
 }  // namespace kda

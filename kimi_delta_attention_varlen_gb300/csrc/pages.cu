@@ -104,6 +104,8 @@ __device__ __forceinline__ int64_t length_of(const kda_page_table &t, int64_t r)
 __global__ void __launch_bounds__(128) fork_kernel(kda_page_table t, const void *src, const void *dst, int32_t itype,
                                                    int64_t count)
 {
+    before_next();
+    after_previous();
     for (int64_t i = blockIdx.x; i < count; i += gridDim.x) {
         const int64_t s = load_index(src, itype, i), d = load_index(dst, itype, i);
         if (s < 0 || s >= t.requests || d < 0 || d >= t.requests || s == d) continue;
@@ -120,6 +122,8 @@ __global__ void __launch_bounds__(128) fork_kernel(kda_page_table t, const void 
 __global__ void __launch_bounds__(128) release_kernel(kda_page_table t, const void *req, int32_t itype,
                                                       const int32_t *keep, int64_t count)
 {
+    before_next();
+    after_previous();
     for (int64_t i = blockIdx.x; i < count; i += gridDim.x) {
         const int64_t r = load_index(req, itype, i);
         if (r < 0 || r >= t.requests) continue;
@@ -141,6 +145,8 @@ __global__ void __launch_bounds__(128) release_kernel(kda_page_table t, const vo
 __global__ void __launch_bounds__(kThreads) count_kernel(kda_page_table t, Plan p, int nb, const void *req,
                                                          int32_t itype, const int32_t *new_tokens, int64_t count)
 {
+    before_next();
+    after_previous();
     __shared__ int32_t sh32[32];
     __shared__ int64_t sh64[32];
     const int tid = threadIdx.x;
@@ -241,6 +247,8 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(kda_page_table t, Plan
                                                           int32_t itype, const int32_t *new_tokens, int64_t count,
                                                           int32_t *move_src, int32_t *move_dst, int32_t *info)
 {
+    before_next();
+    after_previous();
     __shared__ int32_t sh[32];
     __shared__ uint32_t words[kWords];
     __shared__ int32_t pre[kWords];
@@ -298,6 +306,8 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(kda_page_table t, Plan
 __global__ void __launch_bounds__(kThreads) compact_rank_kernel(Plan p, int nb, int32_t n_pages, int32_t *move_src,
                                                                 int32_t *move_dst, int32_t *info)
 {
+    before_next();
+    after_previous();
     __shared__ int32_t sh[32];
     __shared__ uint32_t words[kWords];
     __shared__ int32_t pre[kWords];
@@ -342,6 +352,8 @@ __global__ void __launch_bounds__(kThreads) compact_rank_kernel(Plan p, int nb, 
 __global__ void __launch_bounds__(256) compact_apply_kernel(kda_page_table t, Plan p, int32_t *move_src,
                                                             int32_t *move_dst, int64_t capacity)
 {
+    before_next();
+    after_previous();
     const int32_t live = p.header[0], moves = p.header[1];
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
@@ -366,6 +378,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_v16(uint4 *cache, int
                                                                int64_t payload_v16, const void *src, const void *dst,
                                                                int32_t itype, int64_t count)
 {
+    before_next();
+    after_previous();
     const int64_t v0 = static_cast<int64_t>(blockIdx.x) * (kCopyThreads * kVecPerThread) + threadIdx.x;
     for (int64_t i = blockIdx.y; i < count; i += gridDim.y) {
         const int64_t s = load_index(src, itype, i), d = load_index(dst, itype, i);
@@ -386,6 +400,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_scalar(T *cache, int6
                                                                   const void *src, const void *dst, int32_t itype,
                                                                   int64_t count)
 {
+    before_next();
+    after_previous();
     const int64_t e = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
     if (e >= payload) return;
     for (int64_t i = blockIdx.y; i < count; i += gridDim.y) {
@@ -400,14 +416,19 @@ __global__ void __launch_bounds__(256) append_kernel(const V *x, int64_t x_strid
                                                      const void *req, int32_t itype, int64_t count, kda_page_table t,
                                                      V *cache, int64_t row_stride, int64_t width_v)
 {
+    before_next();
+    after_previous();
     const int lane = threadIdx.x & 31;
     const int64_t tok = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (tok >= total || tok < cu[0] || tok >= cu[count]) return;
-    int64_t lo = 0, hi = count;  // the request i with cu[i] <= tok < cu[i + 1]
-    while (lo + 1 < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (cu[mid] <= tok) lo = mid;
-        else hi = mid;
+    // the request i with cu[i] <= tok < cu[i + 1], by 33-way steps of the warp: two looks for a thousand requests
+    int64_t lo = 0, hi = count;
+    while (hi - lo > 1) {
+        const int64_t step = (hi - lo + 31) / 32, at = lo + step * lane;
+        const uint32_t below = __ballot_sync(0xffffffffu, at < hi && cu[at] <= tok);  // lane 0 always
+        const int64_t from = lo + step * (__popc(below) - 1);
+        hi = from + step < hi ? from + step : hi;
+        lo = from;
     }
     const int64_t r = load_index(req, itype, lo);
     if (r < 0 || r >= t.requests) return;
@@ -433,15 +454,13 @@ size_t pages_workspace(int64_t n_pages, int64_t count)
 cudaError_t launch_pages_fork(const kda_page_table &t, const void *src, const void *dst, int32_t itype, int64_t count,
                               cudaStream_t st)
 {
-    fork_kernel<<<row_grid(count), 128, 0, st>>>(t, src, dst, itype, count);
-    return cudaGetLastError();
+    return launch_overlapped(fork_kernel, dim3(row_grid(count)), dim3(128), 0, st, t, src, dst, itype, count);
 }
 
 cudaError_t launch_pages_release(const kda_page_table &t, const void *req, int32_t itype, const int32_t *keep,
                                  int64_t count, cudaStream_t st)
 {
-    release_kernel<<<row_grid(count), 128, 0, st>>>(t, req, itype, keep, count);
-    return cudaGetLastError();
+    return launch_overlapped(release_kernel, dim3(row_grid(count)), dim3(128), 0, st, t, req, itype, keep, count);
 }
 
 cudaError_t launch_pages_reserve(const kda_page_table &t, const void *req, int32_t itype, const int32_t *new_tokens,
@@ -450,11 +469,11 @@ cudaError_t launch_pages_reserve(const kda_page_table &t, const void *req, int32
 {
     const Plan p = plan_of(ws, t.n_pages, count);
     const int nb = static_cast<int>(blocks_of(t.n_pages));
-    count_kernel<<<nb + 1, kThreads, 0, st>>>(t, p, nb, req, itype, new_tokens, count);
+    cudaError_t e = launch_overlapped(count_kernel, dim3(nb + 1), dim3(kThreads), 0, st, t, p, nb, req, itype, new_tokens, count);
+    if (e != cudaSuccess) return e;
     const int64_t tail = (count + kThreads - 1) / kThreads;
-    assign_kernel<<<static_cast<unsigned>(nb + tail), kThreads, 0, st>>>(t, p, nb, req, itype, new_tokens, count, move_src,
-                                                                         move_dst, info);
-    return cudaGetLastError();
+    return launch_overlapped(assign_kernel, dim3(static_cast<unsigned>(nb + tail)), dim3(kThreads), 0, st, t, p, nb, req, itype,
+                             new_tokens, count, move_src, move_dst, info);
 }
 
 cudaError_t launch_pages_compact(const kda_page_table &t, int32_t *move_src, int32_t *move_dst, int64_t capacity,
@@ -462,12 +481,16 @@ cudaError_t launch_pages_compact(const kda_page_table &t, int32_t *move_src, int
 {
     const Plan p = plan_of(ws, t.n_pages, 0);
     const int nb = static_cast<int>(blocks_of(t.n_pages));
-    count_kernel<<<nb, kThreads, 0, st>>>(t, p, nb, nullptr, KDA_I32, nullptr, 0);
-    compact_rank_kernel<<<nb, kThreads, 0, st>>>(p, nb, static_cast<int32_t>(t.n_pages), move_src, move_dst, info);
+    cudaError_t e = launch_overlapped(count_kernel, dim3(nb), dim3(kThreads), 0, st, t, p, nb, static_cast<const void *>(nullptr),
+                                      static_cast<int32_t>(KDA_I32), static_cast<const int32_t *>(nullptr), INT64_C(0));
+    if (e == cudaSuccess)
+        e = launch_overlapped(compact_rank_kernel, dim3(nb), dim3(kThreads), 0, st, p, nb, static_cast<int32_t>(t.n_pages), move_src,
+                              move_dst, info);
+    if (e != cudaSuccess) return e;
     const int64_t work = t.requests * t.width > capacity ? t.requests * t.width : capacity;
     const int64_t grid = (work + 255) / 256, most = sm_count() * 8;
-    compact_apply_kernel<<<static_cast<unsigned>(grid < most ? grid : most), 256, 0, st>>>(t, p, move_src, move_dst, capacity);
-    return cudaGetLastError();
+    return launch_overlapped(compact_apply_kernel, dim3(static_cast<unsigned>(grid < most ? grid : most)), dim3(256), 0, st, t, p,
+                             move_src, move_dst, capacity);
 }
 
 cudaError_t launch_pages_copy(const CacheDesc &c, const void *src, const void *dst, int32_t itype, int64_t count,
@@ -479,15 +502,13 @@ cudaError_t launch_pages_copy(const CacheDesc &c, const void *src, const void *d
     const int64_t per_cta = vec ? kCopyThreads * kVecPerThread : kCopyThreads;
     const dim3 grid(static_cast<unsigned>((units + per_cta - 1) / per_cta), row_grid(count), 1);
     if (vec)
-        copy_pages_v16<<<grid, kCopyThreads, 0, st>>>(static_cast<uint4 *>(c.data), c.n_rows, c.row_stride * es / 16, units,
-                                                      src, dst, itype, count);
-    else if (c.dtype == KDA_F32)
-        copy_pages_scalar<<<grid, kCopyThreads, 0, st>>>(static_cast<float *>(c.data), c.n_rows, c.row_stride, units, src, dst,
-                                                         itype, count);
-    else
-        copy_pages_scalar<<<grid, kCopyThreads, 0, st>>>(static_cast<uint16_t *>(c.data), c.n_rows, c.row_stride, units, src,
-                                                         dst, itype, count);
-    return cudaGetLastError();
+        return launch_overlapped(copy_pages_v16, grid, dim3(kCopyThreads), 0, st, static_cast<uint4 *>(c.data), c.n_rows,
+                                 c.row_stride * es / 16, units, src, dst, itype, count);
+    if (c.dtype == KDA_F32)
+        return launch_overlapped(copy_pages_scalar<float>, grid, dim3(kCopyThreads), 0, st, static_cast<float *>(c.data), c.n_rows,
+                                 c.row_stride, units, src, dst, itype, count);
+    return launch_overlapped(copy_pages_scalar<uint16_t>, grid, dim3(kCopyThreads), 0, st, static_cast<uint16_t *>(c.data), c.n_rows,
+                             c.row_stride, units, src, dst, itype, count);
 }
 
 cudaError_t launch_latent_append(const void *x, int64_t x_stride, int64_t total, const int32_t *cu, const void *req,
@@ -498,15 +519,13 @@ cudaError_t launch_latent_append(const void *x, int64_t x_stride, int64_t total,
     const bool vec = ((reinterpret_cast<uintptr_t>(c.data) | reinterpret_cast<uintptr_t>(x)) & 15u) == 0 &&
                      c.row_stride * es % 16 == 0 && c.k * es % 16 == 0 && x_stride * es % 16 == 0;
     if (vec)
-        append_kernel<<<grid, 256, 0, st>>>(static_cast<const uint4 *>(x), x_stride * es / 16, total, cu, req, itype, count, t,
-                                            static_cast<uint4 *>(c.data), c.row_stride * es / 16, c.k * es / 16);
-    else if (c.dtype == KDA_F32)
-        append_kernel<<<grid, 256, 0, st>>>(static_cast<const float *>(x), x_stride, total, cu, req, itype, count, t,
-                                            static_cast<float *>(c.data), c.row_stride, c.k);
-    else
-        append_kernel<<<grid, 256, 0, st>>>(static_cast<const uint16_t *>(x), x_stride, total, cu, req, itype, count, t,
-                                            static_cast<uint16_t *>(c.data), c.row_stride, c.k);
-    return cudaGetLastError();
+        return launch_overlapped(append_kernel<uint4>, dim3(grid), dim3(256), 0, st, static_cast<const uint4 *>(x), x_stride * es / 16,
+                                 total, cu, req, itype, count, t, static_cast<uint4 *>(c.data), c.row_stride * es / 16, c.k * es / 16);
+    if (c.dtype == KDA_F32)
+        return launch_overlapped(append_kernel<float>, dim3(grid), dim3(256), 0, st, static_cast<const float *>(x), x_stride, total, cu,
+                                 req, itype, count, t, static_cast<float *>(c.data), c.row_stride, c.k);
+    return launch_overlapped(append_kernel<uint16_t>, dim3(grid), dim3(256), 0, st, static_cast<const uint16_t *>(x), x_stride, total, cu,
+                             req, itype, count, t, static_cast<uint16_t *>(c.data), c.row_stride, c.k);
 }
 
 }  // namespace kda
