@@ -593,6 +593,8 @@ int kda_pages_copy(const kda_cache *cache, const void *move_src, const void *mov
     if (rc != KDA_OK) return rc;
     if (!valid_itype(idx_type)) return KDA_ERR_DTYPE;
     if (count < 0) return KDA_ERR_SHAPE;
+    // the scalar kernel's one-dimensional grid over a row
+    if (c.h * c.v * c.k / 256 >= INT64_C(0x7fffffff)) return KDA_ERR_RANGE;
     if (count == 0) return KDA_OK;
     if ((rc = check_index_array(move_src, idx_type)) != KDA_OK) return rc;
     if ((rc = check_index_array(move_dst, idx_type)) != KDA_OK) return rc;

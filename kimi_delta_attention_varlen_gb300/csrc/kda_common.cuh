@@ -70,6 +70,9 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return d;
 }
 
+// Halfwords of u that are a bf16 infinity or NaN, as 0xffff each.
+__device__ __forceinline__ uint32_t bf16x2_not_finite(uint32_t u) { return __vcmpeq2(u & 0x7f807f80u, 0x7f807f80u); }
+
 // Load one element of an io tensor (fp32 or bf16) as fp32.
 template <typename T> __device__ __forceinline__ float load_as_f32(const T *p);
 template <> __device__ __forceinline__ float load_as_f32<float>(const float *p) { return *p; }

@@ -29,6 +29,11 @@
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than 2^8 since the last
 // rescale (the exponents are relative to that older maximum, exact in fp32 and in bf16's range).
+// Rows of a tile behind the request's last token are set to 0 in shared memory before they meet P = 0 (0
+// times what they hold need not be 0).  With draft tokens the last L - 1 tokens are not seen by every query
+// token: of their values those that are not finite are set to 0 likewise, and where there were any, the
+// epilogue adds them to the rows that do see them.
+//
 // Every wait is bounded; an expired one sets the workspace's status word (6) and ends the CTA.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -44,7 +49,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // chunk_prep.cu
 namespace {
 
 constexpr int T = 64;  // tokens a tile
-constexpr int kItemUnits = 3;
+constexpr int kItemUnits = 3;  // see the share below; 2, 3 and 4 measure alike
 constexpr int kThreads = 256;
 constexpr int kSoftThreads = 128;
 constexpr uint32_t kWaitLimit = 1u << 22;
@@ -95,6 +100,10 @@ __device__ __forceinline__ int32_t length_of(const LatentDecodeArgs &a, int64_t 
 }
 
 __device__ __forceinline__ int32_t tiles_of(int32_t n) { return n > T ? (n - 1) / T + 1 : 1; }
+
+// A row that saw nothing has the sum 0: output 0, log-sum-exp -inf.  A NaN stays one.
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+__device__ __forceinline__ float log_sum(float m, float sum) { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2; }
 
 struct Edge {
     int64_t r, tiles_before;
@@ -175,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
     char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) Bars<C> bar;
     __shared__ uint32_t tmem_base;
+    __shared__ int32_t not_finite;          // segments (from 1) of the last value that was taken out
     __shared__ float corr[2][N], linv[N];  // corr: by parity of the tile, so that a late reader keeps its own
     __shared__ int64_t sums[kThreads / 32];
     __shared__ Edge edge[2];
@@ -190,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
         for (int j = 0; j < C::RING; ++j) mbar_init(&bar.full[j], 1), mbar_init(&bar.empty[j], 1);
         for (int j = 0; j < C::ROPE; ++j) mbar_init(&bar.rope_full[j], 1), mbar_init(&bar.rope_empty[j], 1);
         mbar_init(&bar.q_full, 1), mbar_init(&bar.q_free, 1), mbar_init(&bar.s[0], 1), mbar_init(&bar.s[1], 1);
+        not_finite = 0;
         mbar_init(&bar.p, kSoftThreads), mbar_init(&bar.o, 1);
         for (int j = 0; j < 2; ++j) mbar_init(&bar.s_free[j], kSoftThreads), mbar_init(&bar.drain[j], 1);
         fence_mbar_init();
@@ -426,12 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
         float m[2], l[2], lr[2];  // l: sum of the probabilities, lr: of their bf16 roundings
         int32_t seen[2];
         int slot_out = 0;
+        int32_t segments = 0, tile0 = 0;  // tile0: the segment's first
         uint32_t passes = 0;  // of the second product, so far
         // a thread that gave up goes on without waiting: all of them meet at every barrier
         for (int32_t i = 0; i < total; ++i) {
             const bool fresh = i == 0 || w.first();
             if (fresh) {
                 slot_out = w.first() ? 1 : 0;  // where a part that is not the whole goes
+                ++segments;
+                tile0 = w.tile;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int row = w.group * N + 16 * quad + 8 * e + g;
@@ -522,6 +536,20 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                         make_uint4(0u, 0u, 0u, 0u);
                 }
             }
+            if (p.a.L > 1 && t0 + T > w.n - (p.a.L - 1)) {  // draft tokens: what is not finite must not meet P = 0 either
+                const int from = max(w.n - (p.a.L - 1) - t0, 0), to = min(w.n - t0, T);
+                for (int e = tid - 128; e < (to - from) * 2 * C::PAIRS * 8; e += kSoftThreads) {
+                    const int c = e & 7, pan = (e >> 3) % (2 * C::PAIRS), r2 = from + (e >> 3) / (2 * C::PAIRS);
+                    const int s = (i * C::PAIRS + (pan >> 1)) % C::RING;
+                    uint4 *x = reinterpret_cast<uint4 *>(smem + C::OFF_RING + (2 * s + (pan & 1)) * C::PB + r2 * 128 + c * 16);
+                    const uint4 u = *x;
+                    const uint4 bad = make_uint4(bf16x2_not_finite(u.x), bf16x2_not_finite(u.y), bf16x2_not_finite(u.z), bf16x2_not_finite(u.w));
+                    if (bad.x | bad.y | bad.z | bad.w) {
+                        not_finite = segments;
+                        *x = make_uint4(u.x & ~bad.x, u.y & ~bad.y, u.z & ~bad.z, u.w & ~bad.w);
+                    }
+                }
+            }
             fence_proxy_async_smem();
             if (soft_any(grew) && !fresh) {
 #pragma unroll 1
@@ -572,10 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                         sum_r += __shfl_xor_sync(0xffffffffu, sum_r, 2);
                         const int row = 16 * quad + 8 * e + g, rr = w.group * N + row;
                         if (t == 0) {
-                            linv[row] = sum_r > 0.f ? 1.f / sum_r : 0.f;
+                            linv[row] = inverse(sum_r);
                             if (!whole) p.ml[part * N + row] = make_float4(m[e], sum, sum_r, 0.f);
                             else if (p.a.lse != nullptr && rr < p.rows)
-                                p.a.lse[w.r * p.rows + rr] = sum > 0.f ? (m[e] + log2f(sum)) * kLn2 : -INFINITY;
+                                p.a.lse[w.r * p.rows + rr] = log_sum(m[e], sum);
                         }
                     }
                 }
@@ -585,12 +613,28 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                 soft_any(false);  // linv is complete
                 const int valid = p.rows - w.group * N < N ? p.rows - w.group * N : N;
                 const int dim = 32 * quad + lane;
+                const bool taken = not_finite == segments;
 #pragma unroll 1
                 for (int c0 = 0; c0 < C::PAIRS * N; c0 += 16) {
                     uint32_t o[16];
                     tc::ld16(tl + c0, o);
                     tc::wait_ld();
                     const int mt = c0 / N, row0 = c0 % N;
+                    if (taken) {  // draft tokens' values that were taken out, to the rows that see them
+                        const int32_t last = min(w.n, (w.tile + 1) * T);
+                        for (int32_t tok = max(w.n - (p.a.L - 1), tile0 * T); tok < last; ++tok) {
+                            const int32_t e = p.a.block_table[w.slot * p.a.table_stride + tok / p.a.page];
+                            if (e < 0 || e >= p.a.cache.n_rows) continue;
+                            const float x = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.a.cache.data)[
+                                e * p.a.cache.row_stride + tok % p.a.page * C::D + mt * 128 + dim]);
+                            if (isfinite(x)) continue;
+#pragma unroll
+                            for (int q = 0; q < 16; ++q) {
+                                const int row = w.group * N + row0 + q;
+                                if (row < p.rows && tok < w.n - (p.a.L - 1 - row / p.a.h)) o[q] = __float_as_uint(__uint_as_float(o[q]) + x);
+                            }
+                        }
+                    }
                     if (whole) {
                         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
                                              (w.r * p.rows + w.group * N + row0) * DL + mt * 128 + dim;
@@ -702,7 +746,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
                 lr += __shfl_xor_sync(0xffffffffu, lr, o);
             }
             l = __shfl_sync(0xffffffffu, l, 0), lr = __shfl_sync(0xffffffffu, lr, 0);
-            const float inv = lr > 0.f ? 1.f / lr : 0.f;
+            const float inv = inverse(lr);
             float4 o[kLanes / 32];
 #pragma unroll
             for (int q = 0; q < kLanes / 32; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -718,7 +762,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
             }
 #pragma unroll
             for (int q = 0; q < kLanes / 32; ++q) store(row, lane + 32 * q, o[q], inv);
-            if (lane == 0 && p.a.lse != nullptr) p.a.lse[r * p.rows + row0 + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            if (lane == 0 && p.a.lse != nullptr) p.a.lse[r * p.rows + row0 + row] = log_sum(m, l);
             continue;
         }
         const int32_t row = unit - before[lo], sub = tid / kLanes, d = tid % kLanes;
@@ -765,9 +809,9 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
                 const float4 y = acc[q][d];
                 o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
             }
-            store(row, d, o, sum[1] > 0.f ? 1.f / sum[1] : 0.f);
+            store(row, d, o, inverse(sum[1]));
             if (d == 0 && p.a.lse != nullptr)
-                p.a.lse[r * p.rows + row0 + row] = sum[0] > 0.f ? (top + log2f(sum[0])) * kLn2 : -INFINITY;
+                p.a.lse[r * p.rows + row0 + row] = log_sum(top, sum[0]);
         }
         __syncthreads();  // weight, sum and acc may be written again
     }

@@ -29,6 +29,10 @@
 // sum of the rounded weights, the log-sum-exp taken from the sum before rounding.  A query tile that
 // sees a single key tile has few weights to average the rounding over, so there what the rounding
 // left off goes through a second product (the other half of S_s holds it).
+// A key that a query must not see enters its product with weight 0, and 0 times an infinity or NaN is not 0.
+// So in the tiles that not every query of the block sees whole, values that are not finite are taken out
+// (set to 0 in shared memory) before the product, and where there were any, the epilogue adds them to the
+// queries that do see them.  Value rows behind the sequence's end are set to 0 likewise.
 // Every wait is bounded; an expired one sets the workspace's status word (7).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -185,6 +189,10 @@ struct Walk {
     }
 };
 
+// A row that saw nothing has the sum 0: output 0, log-sum-exp -inf.  A NaN stays one.
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+__device__ __forceinline__ float log_sum(float m, float sum) { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2; }
+
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t r;
@@ -336,6 +344,7 @@ struct Shared {
     Bars bar;
     Segment seg[2];
     float pair[2][2][T];  // by query tile, half, row: what the two threads of a row tell each other
+    uint32_t not_finite[2];  // by parity of the segment: its number + 1 once a value was taken out
     uint32_t tmem_base;
 };
 constexpr int kSmem = OFF_SHARED + sizeof(Shared);
@@ -355,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
     }
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
+            sh.not_finite[s] = 0;
             mbar_init(&bar.k_full[s][0], 1), mbar_init(&bar.k_full[s][1], 1), mbar_init(&bar.k_full[s][2], 1), mbar_init(&bar.k_free[s], 2), mbar_init(&bar.v_full[s], 1), mbar_init(&bar.v_free[s], 2);  // handed back by both query tiles
             mbar_init(&bar.drain[s], 1), mbar_init(&bar.seg_full[s], 1), mbar_init(&bar.seg_free[s], kReaders);
             mbar_init(&bar.q_full[s], 1), mbar_init(&bar.q_free[s], 1), mbar_init(&bar.s[s], 1), mbar_init(&bar.o[s], 1);
@@ -657,6 +667,26 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                             make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
+                // values that are not finite, in tiles that the block's first query does not see whole
+                if ((seg->j0 + j + 1) * T > seg->see) {
+                    const uint32_t g = g0 + j;
+                    wait(&bar.v_full[g & 1], g >> 1 & 1);
+                    char *v = smem + OFF_RING + (5 * g + 3 + half) % kRing * PB + row * 128;
+                    if (row < keys) {
+#pragma unroll 1
+                        for (int q = 0; q < 8; ++q) {  // eight rows of a warp start in eight banks
+                            uint4 *x = reinterpret_cast<uint4 *>(v + ((q + row) & 7) * 16);
+                            const uint4 u = *x;
+                            const uint4 bad = make_uint4(bf16x2_not_finite(u.x), bf16x2_not_finite(u.y), bf16x2_not_finite(u.z), bf16x2_not_finite(u.w));
+                            if (bad.x | bad.y | bad.z | bad.w) {
+                                sh.not_finite[nseg & 1] = nseg + 1;
+                                __threadfence_block();  // who finds the zeros finds the mark, too
+                                *x = make_uint4(u.x & ~bad.x, u.y & ~bad.y, u.z & ~bad.z, u.w & ~bad.w);
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
                 // scores -> probabilities, rounded, into S_s
                 float2 sum = make_float2(0.f, 0.f), sum_r = make_float2(0.f, 0.f);
                 if (!single) {
@@ -717,14 +747,29 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 wait(&bar.o[s], (steps - 1) & 1);
                 tc::fence_after_sync();
             }
-            const float inv = lr > 0.f ? 1.f / lr : 0.f;
+            const float inv = inverse(lr);
             uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.a.out) + out_row * DV + kHalf * half);
+            const bool taken = nt > 0 && *static_cast<volatile uint32_t *>(&sh.not_finite[nseg & 1]) == nseg + 1;
 #pragma unroll
             for (int c = 0; c < kHalf; c += 16) {
                 uint32_t o[16];
                 if (nt > 0) {
                     tc::ld16(to + c, o);
                     tc::wait_ld();
+                }
+                if (taken && valid) {  // values that were taken out, to the queries that see them
+                    int32_t key = seg->see / T * T;
+                    if (key < seg->j0 * T) key = seg->j0 * T;
+                    const int32_t end = min(limit + seg->j0 * T, (seg->j0 + nt) * T);
+                    for (; key < end; ++key) {
+                        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.a.v) + (seg->k0 + static_cast<int64_t>(key)) * p.a.v_token +
+                                                 seg->head * p.a.v_head + kHalf * half + c;
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const float x = __bfloat162float(v[q]);
+                            if (!isfinite(x)) o[q] = __float_as_uint(__uint_as_float(o[q]) + x);
+                        }
+                    }
                 }
                 if (slot >= 0) {  // a part: as it is
                     if (nt > 0 && valid) {
@@ -738,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                         uint32_t v[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            v[r] = inv > 0.f ? pack_bf16x2(__uint_as_float(o[8 * q + 2 * r]) * inv, __uint_as_float(o[8 * q + 2 * r + 1]) * inv) : 0u;
+                            v[r] = lr == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[8 * q + 2 * r]) * inv, __uint_as_float(o[8 * q + 2 * r + 1]) * inv);
                         out[c / 8 + q] = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
@@ -748,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 p.ml[part_row] = make_float4(m, l, lr, 0.f);
                 if (row == 0 && s == 0) (slot ? p.item1 : p.item0)[blockIdx.x] = seg->pair;
             } else if (half == 0 && valid && p.a.lse != nullptr) {
-                p.a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                p.a.lse[out_row] = log_sum(m, l);
             }
             pair_sync();  // the sums have been read
             g0 += seg->j1 - seg->j0;
@@ -805,18 +850,18 @@ __global__ void __launch_bounds__(256) join_kernel(Params p)
 #pragma unroll 4
         for (int32_t j = 0; j < parts; ++j) {
             const float4 ml = p.ml[at(j)];
-            if (ml.x == -INFINITY) continue;  // a part in which the row saw nothing (its sums may not be written)
-            const float f = ex2_approx(ml.x - m);
+            if (ml.y == 0.f) continue;  // a part in which the row saw nothing (and whose row may not be written)
+            const float f = ex2_approx(ml.x - (m == -INFINITY ? 0.f : m));
             const float4 x = *reinterpret_cast<const float4 *>(p.part + at(j) * DV + 4 * lane);
             l += f * ml.y;
             lr += f * ml.z;
             o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
         }
-        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+        const float inv = inverse(lr);
         const int64_t out_row = static_cast<int64_t>(it.q0 + row) * p.a.h + pair % p.a.h;
         uint2 v = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.a.out) + out_row * DV)[lane] = v;
-        if (lane == 0 && p.a.lse != nullptr) p.a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (lane == 0 && p.a.lse != nullptr) p.a.lse[out_row] = log_sum(m, l);
     }
 }
 

@@ -97,6 +97,21 @@ def test_decode_draft_tokens_are_causal(L, heads):
     assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, 512), f"L {L} heads {heads}")
 
 
+@pytest.mark.parametrize("n,L", [(40, 3), (130, 5), (66, 4), (20000, 6), (64, 70), (131, 70)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_decode_draft_values_that_are_not_finite_reach_only_tokens_that_see_them(n, L, bad):
+    cache, table, sl, rows = paged_latents([n], 16, 512, seed=n + L)
+    q = queries(1, L, 8, 576, seed=L)
+    tok = n - 2  # the last but one of the draft tokens' rows: the query tokens from L - 2 on see it
+    dims = [9, 300, 511]
+    q[..., dims] = 0
+    ref = decode_reference(q, lambda r, k: rows[r][:k], [n], SCALE, 512)
+    cache[table[0, tok // 16].long(), 0, tok % 16, dims] = bad  # in a latent, so in its key too: 0 * bad is no number
+    out, lse = run_decode(q, cache, table, sl, 512, SCALE)
+    assert torch.isnan(out[0, L - 2:]).all() and torch.isnan(lse[0, L - 2:]).all()
+    assert_attention(out[:, :L - 2], lse[:, :L - 2], [x[:, :L - 2] for x in ref], f"n {n} L {L}")
+
+
 @pytest.mark.parametrize("lens,heads", [([40000], 32), ([9999, 3, 25000], 16), ([6400] * 5, 64), ([20000, 1], 128)])
 def test_decode_long_contexts(lens, heads):
     # few rows: the cache axis is split and the parts are joined
@@ -274,6 +289,34 @@ def test_prefill_queries_that_see_nothing():
     q, kn, kr, v, cu_q, cu_k = prompt_batch([7], [0], 2, seed=1)
     out, lse = run_prefill(q, kn, kr, v, cu_q, cu_k)
     assert (out == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("nq,nk,tok", [([300], [300], 100), ([300], [300], 260), ([200, 40], [1500, 40], 1400), ([256], [5000], 4800),
+                                       ([70], [70], 69)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_prefill_values_that_are_not_finite_reach_only_queries_that_see_them(nq, nk, tok, bad):
+    q, kn, kr, v, cu_q, cu_k = prompt_batch(nq, nk, 2, seed=tok)
+    ref = prefill_reference(q, kn, kr, v, cu_q, cu_k, SCALE)
+    v[tok, 1, 5], v[tok, 1, 77] = bad, bad
+    out, lse = run_prefill(q, kn, kr, v, cu_q, cu_k)
+    sees = torch.zeros_like(out, dtype=torch.bool)
+    first = max(0, tok - (nk[0] - nq[0]))  # the first query of the sequence that sees the token
+    sees[first:nq[0], 1, 5] = sees[first:nq[0], 1, 77] = True
+    hit = out[sees].float()
+    assert (torch.isnan(hit) if math.isnan(bad) else hit == bad).all()
+    assert_attention(torch.where(sees, ref[0].to(DEV).to(BF), out), lse, ref, "others")
+
+
+def test_prefill_keys_that_are_not_numbers_reach_only_queries_that_see_them():
+    for tok in (3, 130, 299):
+        q, kn, kr, v, cu_q, cu_k = prompt_batch([300], [300], 2, seed=tok)
+        ref = prefill_reference(q, kn, kr, v, cu_q, cu_k, SCALE)
+        kn[tok, 1, 7] = math.nan
+        out, lse = run_prefill(q, kn, kr, v, cu_q, cu_k)
+        assert torch.isnan(out[tok:, 1]).all() and torch.isnan(lse[tok:, 1]).all()
+        fine = torch.ones(300, 2, dtype=torch.bool, device=DEV)
+        fine[tok:, 1] = False
+        assert_attention(torch.where(fine[..., None], out, ref[0].to(DEV).to(BF)), torch.where(fine, lse, ref[2].to(DEV).float()), ref, "others")
 
 
 def test_prefill_large_scores():
