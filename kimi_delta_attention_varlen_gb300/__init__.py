@@ -493,10 +493,10 @@ def kda_pages_workspace_size(n_pages: int, count: int) -> int:
     return int(lib().kda_pages_workspace_size(n_pages, count))
 
 
-def _same_lists(*lists) -> None:
-    for t in lists:
-        _index_vector(t)
-    _need(all(t.numel() == lists[0].numel() and t.dtype == lists[0].dtype for t in lists[1:]), "index lists: same length and dtype")
+def _same_lists(a, b) -> None:
+    _index_vector(a)
+    _index_vector(b)
+    _need(a.numel() == b.numel() and a.dtype == b.dtype, "index lists: same length and dtype")
 
 
 def _int32_vector(name: str, t, n: int) -> None:

@@ -19,7 +19,7 @@ constexpr int kBlockPages = 4096;            // pages ranked by one CTA
 constexpr int kThreads = 1024;
 constexpr int kWords = kBlockPages / 32;     // bitmap words of one CTA
 constexpr int kCopyThreads = 256;
-constexpr int kVecPerThread = 4;             // 16-byte vectors in flight per thread
+constexpr int kMostVecs = 8;                 // 16-byte vectors in flight per thread, at most
 
 // Workspace: a header of four words, then the arrays below (4-byte elements).
 struct Plan {
@@ -373,24 +373,27 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(kda_page_table t, Pl
     }
 }
 
-// Page copies, one tile of one page per CTA step.
+// Page copies, one tile of one page per CTA step: the page in as few equal tiles as kMostVecs vectors a thread allow
+// (a page of 64 latent rows, 73,728 bytes: three tiles of six).  With four vectors a thread, and so a half-empty last
+// tile, the call on 6000 such pages took 170 us with its plan; 157 us with equal tiles (6.1 TB/s in the copy).
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_v16(uint4 *cache, int64_t n_rows, int64_t stride_v16,
-                                                               int64_t payload_v16, const void *src, const void *dst,
+                                                               int64_t payload_v16, int32_t vecs, const void *src, const void *dst,
                                                                int32_t itype, int64_t count)
 {
     before_next();
     after_previous();
-    const int64_t v0 = static_cast<int64_t>(blockIdx.x) * (kCopyThreads * kVecPerThread) + threadIdx.x;
+    const int64_t v0 = static_cast<int64_t>(blockIdx.x) * (kCopyThreads * vecs) + threadIdx.x;
     for (int64_t i = blockIdx.y; i < count; i += gridDim.y) {
         const int64_t s = load_index(src, itype, i), d = load_index(dst, itype, i);
         if (s < 0 || s >= n_rows || d < 0 || d >= n_rows) continue;
-        uint4 buf[kVecPerThread];
+        const uint4 *from = cache + s * stride_v16 + v0;
+        uint4 *to = cache + d * stride_v16 + v0, buf[kMostVecs];
 #pragma unroll
-        for (int u = 0; u < kVecPerThread; ++u)
-            if (v0 + u * kCopyThreads < payload_v16) buf[u] = ld_nc_v4(cache + s * stride_v16 + v0 + u * kCopyThreads);
+        for (int u = 0; u < kMostVecs; ++u)
+            if (u < vecs && v0 + u * kCopyThreads < payload_v16) buf[u] = ld_nc_v4(from + u * kCopyThreads);
 #pragma unroll
-        for (int u = 0; u < kVecPerThread; ++u)
-            if (v0 + u * kCopyThreads < payload_v16) st_cs_v4(cache + d * stride_v16 + v0 + u * kCopyThreads, buf[u]);
+        for (int u = 0; u < kMostVecs; ++u)
+            if (u < vecs && v0 + u * kCopyThreads < payload_v16) st_cs_v4(to + u * kCopyThreads, buf[u]);
     }
 }
 
@@ -499,11 +502,12 @@ cudaError_t launch_pages_copy(const CacheDesc &c, const void *src, const void *d
     const int64_t es = c.dtype == KDA_F32 ? 4 : 2, payload = c.h * c.v * c.k;
     const bool vec = (reinterpret_cast<uintptr_t>(c.data) & 15u) == 0 && c.row_stride * es % 16 == 0 && payload * es % 16 == 0;
     const int64_t units = vec ? payload * es / 16 : payload;
-    const int64_t per_cta = vec ? kCopyThreads * kVecPerThread : kCopyThreads;
-    const dim3 grid(static_cast<unsigned>((units + per_cta - 1) / per_cta), row_grid(count), 1);
+    const int64_t tiles = vec ? (units + kCopyThreads * kMostVecs - 1) / (kCopyThreads * kMostVecs) : (units + kCopyThreads - 1) / kCopyThreads;
+    const int32_t vecs = static_cast<int32_t>((units + kCopyThreads * tiles - 1) / (kCopyThreads * tiles));
+    const dim3 grid(static_cast<unsigned>(tiles), row_grid(count), 1);
     if (vec)
         return launch_overlapped(copy_pages_v16, grid, dim3(kCopyThreads), 0, st, static_cast<uint4 *>(c.data), c.n_rows,
-                                 c.row_stride * es / 16, units, src, dst, itype, count);
+                                 c.row_stride * es / 16, units, vecs, src, dst, itype, count);
     if (c.dtype == KDA_F32)
         return launch_overlapped(copy_pages_scalar<float>, grid, dim3(kCopyThreads), 0, st, static_cast<float *>(c.data), c.n_rows,
                                  c.row_stride, units, src, dst, itype, count);
