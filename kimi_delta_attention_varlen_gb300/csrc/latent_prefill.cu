@@ -4,16 +4,20 @@
 // per sequence and head, causal with the queries at the end of the keys, the keys visited in tiles
 // of 128 with a running maximum m and sum l a row.
 //
-// plan_kernel (one CTA) lists the query blocks (256 queries of one sequence), longest first by the
-// key tiles they see.  One persistent CTA per SM takes (block, head) pairs of the list: whole rounds of
-// one pair a CTA, in turn from either end (the pairs of a round are alike in length, and blocks of one
-// sequence run side by side, so their keys and values come from the L2 cache); of the last, partial
-// round all key tiles lie on one line and each CTA takes an equal stretch of it.  A pair that falls
-// into several stretches leaves unnormalised parts in the workspace, which join_kernel puts together in
-// order of their keys.  Parts cost about what kCutTiles key tiles do (queries loaded again, parts written
-// and joined: 10 us), so the last round runs whole where its longest pair is not that much longer than an
-// equal stretch.  Measured, cut against whole: 1000 queries on 16000 keys, 4 heads 62 / 244 us; 8192 queries,
-// 2 heads 73 / 122 us; four prompts of up to 2000, 8 heads 65 / 55 us (these run whole).
+// plan_kernel (one CTA) lists the query blocks (256 queries of one sequence) and decides how one
+// persistent CTA per SM shares the (block, head) pairs; a scheduling warp per CTA hands them to the others.
+//   From kTurnRounds pairs a CTA on: in turn, by an atomic counter, in order of sequence, head and block,
+//     so that blocks of one sequence and head run side by side and their keys and values come from the
+//     L2 cache (a block reads 80 KB a key tile for 21 MFLOP: at the tensor cores' rate that is the HBM's).
+//     16 prompts of 512..8192 tokens, 32 heads: 3.76 ms against 4.18 ms longest first.
+//   Fewer: whole rounds of one pair a CTA, longest first and in turn from either end; of the last,
+//     partial round all key tiles lie on one line and each CTA takes an equal stretch of it.  A pair that
+//     falls into several stretches leaves unnormalised parts in the workspace, which join_kernel puts
+//     together in order of their keys.  Parts cost about what kCutTiles key tiles do (queries loaded again,
+//     parts written and joined: 10 us), so the last round runs whole where its longest pair is not that much
+//     longer than an equal stretch.  Cut against whole: 1000 queries on 16000 keys, 4 heads 62 / 244 us;
+//     8192 queries, 2 heads 73 / 122 us; four prompts of up to 2000, 8 heads 65 / 55 us (these run whole).
+// Which CTA takes a pair never changes what is computed, and where pairs are cut depends on the lengths alone.
 // A block is two query tiles s = 0, 1 of 128 rows that share the key and value tiles:
 //   S_s   = Q_s K^T     M = 128, N = 128, K = 192 (two nope panels and the shared rope panel)
 //   O_s  += P_s V       M = 128, N = 64 twice, K = 128, P_s in tensor memory
@@ -66,6 +70,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kStatusExpired = 7;
 constexpr int kBuckets = 1024;
 constexpr int kCutTiles = 10;
+constexpr int kTurnRounds = 8, kInTurn = -1;
 constexpr int kJoinCtas = 6;               // a SM: as many as stay resident
 constexpr int kReaders = 3 + 16;           // warps that read a segment
 
@@ -76,10 +81,11 @@ struct Params {
     float scale_log2;
     int32_t kn_order, v_order;  // of the map's coordinates: Order
     int32_t *status;
-    int32_t *n_blocks, *whole;   // blocks listed; pairs that are taken whole (a multiple of the grid, or all)
+    int32_t *n_blocks, *whole;   // blocks listed; pairs that are taken whole (a multiple of the grid, or all), kInTurn: see Walk
+    int32_t *taken;              // pairs taken in turn
     int64_t *before;             // [max_blocks + 1] key tiles (of one head) before each block of the list, and in all
     int2 *table;                 // [max_blocks] (sequence, block of the sequence)
-    int32_t *seq_off;            // [num_seqs + 1] blocks before each sequence
+    int32_t *seq_off, *short_off;  // [num_seqs + 1] blocks before each sequence; of them those in the first quarter of theirs
     int64_t max_blocks;
     int32_t grid;
     int32_t *item0, *item1;      // [grid] pair whose part is in slot 0 / 1 of the CTA, or -1
@@ -137,7 +143,7 @@ struct Walk {
     {
         round = 0, whole = *p.whole, left = 0;
         const int32_t H = p.a.h, items = blocks * H;
-        if (whole >= items) return;
+        if (whole == kInTurn || whole >= items) return;
         // the line begins with pair `whole`
         const int64_t base = p.before[whole / H] * H + whole % H * (p.before[whole / H + 1] - p.before[whole / H]);
         const int64_t all = p.before[blocks] * H - base, n = all < gridDim.x ? all : gridDim.x;
@@ -154,9 +160,33 @@ struct Walk {
         next_pair = lo * H + static_cast<int32_t>(rest / units);
         next_j = static_cast<int32_t>(rest % units);
     }
-    // The next pair or stretch; false: none.
+    // The next pair or stretch; false: none.  By a whole warp.
     __device__ bool next(const Params &p, int32_t items)
     {
+        if (whole == kInTurn) {
+            // whoever comes, in order of sequence, head and block, the longest first; the first quarter of each
+            // sequence's blocks, the short ones, in a second pass that evens out the end
+            pair = 0;
+            if ((threadIdx.x & 31) == 0) pair = atomicAdd(p.taken, 1);
+            pair = __shfl_sync(0xffffffffu, pair, 0);
+            if (pair >= items) return false;
+            const int32_t H = p.a.h, seqs = static_cast<int32_t>(p.a.num_seqs);
+            const int32_t many = (p.seq_off[seqs] - p.short_off[seqs]) * H;
+            const bool second = pair >= many;
+            const int32_t at = second ? pair - many : pair;
+            auto before = [&](int32_t b) { return (second ? p.short_off[b] : p.seq_off[b] - p.short_off[b]) * H; };
+            int32_t lo = 0, hi = seqs;
+            while (lo + 1 < hi) {
+                const int32_t mid = (lo + hi) >> 1;
+                if (before(mid) <= at) lo = mid;
+                else hi = mid;
+            }
+            const int32_t in_seq = at - before(lo), n = (before(lo + 1) - before(lo)) / H;
+            head = in_seq / n;
+            it.load(p.a, lo, (second ? n : p.seq_off[lo + 1] - p.seq_off[lo]) - 1 - in_seq % n);
+            j0 = 0, j1 = it.n, slot = -1;
+            return true;
+        }
         const int32_t grid = gridDim.x, at = round * grid + (round & 1 ? grid - 1 - static_cast<int32_t>(blockIdx.x) : blockIdx.x);
         const bool entire = round * grid < whole;
         if (entire) {
@@ -236,7 +266,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(Params p)
     };
     if (tid == 0) *p.status = 0;
     hist[tid] = 0;
-    int64_t base = 0;
+    int64_t base = 0, short_base = 0;
     for (int64_t b0 = 0; b0 < a.num_seqs; b0 += 1024) {
         const int64_t b = b0 + tid;
         int32_t nb = 0;
@@ -244,13 +274,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(Params p)
             const int64_t n = clamp64(a.cu_q[b + 1], a.total_q) - clamp64(a.cu_q[b], a.total_q);
             nb = n > 0 ? static_cast<int32_t>((n + kBlock - 1) / kBlock) : 0;
         }
-        int64_t total;
-        const int64_t at = base + scan(nb, &total);
-        if (b < a.num_seqs) p.seq_off[b] = static_cast<int32_t>(at);
+        int64_t total, shorts;
+        const int64_t at = base + scan(nb, &total), short_at = short_base + scan(nb / 4, &shorts);
+        if (b < a.num_seqs) p.seq_off[b] = static_cast<int32_t>(at), p.short_off[b] = static_cast<int32_t>(short_at);
         base += total;
+        short_base += shorts;
     }
-    // more blocks than the bound only if the offsets are not what the contract says
-    const int32_t blocks = static_cast<int32_t>(base < p.max_blocks ? base : p.max_blocks);
+    // more blocks than the bound only if the offsets are not what the contract says: then nothing is done
+    const int32_t blocks = static_cast<int32_t>(base <= p.max_blocks ? base : 0);
+    if (tid == 0) p.seq_off[a.num_seqs] = blocks, p.short_off[a.num_seqs] = static_cast<int32_t>(short_base);
     if (tid == 0) *p.n_blocks = blocks;
     __syncthreads();
     auto locate = [&](int32_t i, int2 *e) {  // block i in order of the sequences; its key tiles
@@ -312,7 +344,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(Params p)
         p.before[blocks] = units;
         const int32_t items = blocks * a.h, whole = items / p.grid * p.grid;
         *p.whole = items;
-        if (whole < items) {
+        *p.taken = 0;
+        if (items >= kTurnRounds * p.grid) {
+            *p.whole = kInTurn;
+        } else if (whole < items) {
             const int32_t b = whole / a.h;
             const int64_t longest = p.before[b + 1] - p.before[b];
             const int64_t rest = units * a.h - p.before[b] * a.h - whole % a.h * longest;
@@ -896,7 +931,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t layout(char *ws, int64_t total_q, int64_t num_seqs, Params *p)
 {
     const size_t n = static_cast<size_t>(blocks_bound(total_q, num_seqs)), grid = static_cast<size_t>(sm_count());
-    const size_t before = 256, table = before + (n + 1) * 8, seq = table + n * 8, items = up256(seq + (num_seqs + 1) * 4);
+    const size_t before = 256, table = before + (n + 1) * 8, seq = table + n * 8, items = up256(seq + (num_seqs + 1) * 8);
     const size_t ml = up256(items + 8 * grid), part = ml + 2 * grid * kBlock * 16, end = part + 2 * grid * kBlock * DV * 4;
     if (p != nullptr) {
         p->max_blocks = static_cast<int64_t>(n);
@@ -904,9 +939,11 @@ size_t layout(char *ws, int64_t total_q, int64_t num_seqs, Params *p)
         p->status = reinterpret_cast<int32_t *>(ws);
         p->n_blocks = p->status + 1;
         p->whole = p->status + 2;
+        p->taken = p->status + 3;
         p->before = reinterpret_cast<int64_t *>(ws + before);
         p->table = reinterpret_cast<int2 *>(ws + table);
         p->seq_off = reinterpret_cast<int32_t *>(ws + seq);
+        p->short_off = p->seq_off + num_seqs + 1;
         p->item0 = reinterpret_cast<int32_t *>(ws + items);
         p->item1 = p->item0 + grid;
         p->ml = reinterpret_cast<float4 *>(ws + ml);
