@@ -1,13 +1,19 @@
 /*
  * kda.h - C ABI of the GB300 (sm_103a) Kimi Delta Attention (KDA) hot path.
  *
- * Four operations, each an asynchronous launch on a caller-given CUDA stream:
+ * Four core operations, each an asynchronous launch on a caller-given stream:
  *
  *   kda_state_gather    per-request recurrent state gather from a paged cache
  *   kda_prefill_varlen  chunkwise (C = 64) gated delta-rule prefill over a
  *                       cu_seqlens varlen batch
  *   kda_state_scatter   final-state scatter back to cache rows
  *   kda_decode_step     one-token recurrent decode step on cache rows
+ *
+ * and around them, each documented where it is declared: the cache-indexed
+ * prefill, target verification, INT8 checkpoints, the short convolution, and
+ * what the full-attention layers between the recurrent ones need: attention
+ * over a paged latent cache (kda_latent_decode, kda_latent_prefill,
+ * kda_latent_append) and the upkeep of its pages (kda_pages_*).
  *
  * Conventions shared by every entry point
  *   - Every data pointer is a DEVICE pointer unless stated otherwise; the
@@ -566,7 +572,8 @@ typedef struct {
  *               not overlap.  Its status word: kda_prefill_workspace_status.
  * A page number outside [0, n_pages) reads as zero rows, like an invalid
  * index of kda_state_gather.  Cache rows beyond a request's length are never
- * used, whatever they hold (NaN and infinities included).  Scores, softmax
+ * used, whatever they hold (NaN and infinities included), and a value that is
+ * not finite reaches only the query tokens that see it.  Scores, softmax
  * statistics and sums are fp32; the probabilities enter the second product
  * in bf16 (the tensor cores' operand type).
  * Built: dl in {256, 512}, dr == 64, page_size a multiple of 8, bf16.
@@ -608,6 +615,7 @@ int kda_latent_decode(const void *q, int32_t io_dtype, int64_t batch, int32_t L,
  *            total_q / total_k (precondition; no key at or beyond total_k and
  *            no query at or beyond total_q is touched whatever they hold)
  *   out      [total_q, h, dv] device bf16, lse [total_q, h] fp32 or NULL
+ *            A value that is not finite reaches only the queries that see it.
  *   workspace kda_latent_prefill_workspace_size(...) bytes, as above
  * Built: dn == dv == 128, dr == 64, bf16.  Errors as kda_latent_decode
  * (_SHAPE: negative strides, a token stride of 0 with several tokens; _RANGE:
@@ -708,18 +716,19 @@ const char *kda_status_string(int32_t status);
  * thread (static storage; "no error" if none). */
 const char *kda_last_cuda_error_string(void);
 
-/* Reads the device-side status word a prefill call leaves in its workspace:
- * 0 when every internal wait completed, otherwise a non-zero code (1: a
+/* Reads the device-side status word that a prefill or a latent-attention call
+ * leaves in its workspace: 0 when every internal wait completed, otherwise a non-zero code (1: a
  * record copy awaited by the register state pass did not complete within its
  * bound; 2: a record copy or MMA awaited by the tensor-memory state pass did
  * not; 3: an input tensor copy awaited by the chunk preparation did not; 4:
  * cu_seqlens gave more chunks than total_tokens allows, a broken
  * precondition whose results are undefined, though no record beyond the
- * workspace is read).  A kernel whose wait expires stops waiting, finishes
- * without touching memory it has not been given and releases its tensor
- * memory, so the context stays usable.  This call and
- * kda_prefill_noalloc_status are the ones that synchronise: each copies 4
- * bytes on `stream` and waits. */
+ * workspace is read; 5: a wait of the fused prefill expired; 6: one of
+ * kda_latent_decode; 7: one of kda_latent_prefill).  A kernel whose wait
+ * expires stops waiting, finishes without touching memory it has not been
+ * given and releases its tensor memory, so the context stays usable.  This
+ * call and kda_prefill_noalloc_status are the ones that synchronise: each
+ * copies 4 bytes on `stream` and waits. */
 int kda_prefill_workspace_status(const void *workspace, int32_t *status_out, void *stream);
 
 /* Diagnostic of the bounded waits above (infra-level failure detection: a

@@ -1,9 +1,11 @@
 """Plain 64-bit forms of latent attention and of the page tables, and the tolerances of the
 kernels, for the tests.
 
-Tolerance of an output (bf16): the probabilities enter the second product rounded to bf16 and
-the result is rounded to bf16, each within 2^-9 relative, so |d| <= 2^-8 * sum_j p_j |x_j|; a
-quarter more covers the scores' error below and the approximate exponential.
+Tolerance of an output (bf16), 1.25 * 2^-8 * sum_j p_j |x_j|: the result's rounding to bf16 takes
+2^-8 of it at most (bf16's unit roundoff).  The quarter that is left covers the scores' error
+below, the approximate exponential and the rounding of the probabilities to bf16, which has to be
+small by the kernels' doing: normalised by the sum of the rounded weights its common part drops
+out and the rest averages over the tokens, and with few tokens a second product carries it.
 Tolerance of a score, and so of the log-sum-exp: the tensor cores add up to 36 partial sums of
 16 products in fp32, each addition within 2^-23 of the magnitudes added, so |d| <= 2^-17 *
 max_j scale * sum_c |q_c| |x_jc|; 1e-5 covers the logarithm and the sum of exponentials."""
