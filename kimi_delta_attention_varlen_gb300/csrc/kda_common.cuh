@@ -301,6 +301,17 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void *p)
     return r;
 }
 
+// The same by the coherent path, for kernels that come while the one before, which may have written the data, runs.
+__device__ __forceinline__ uint4 ld_v4(const void *p)
+{
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+
 __device__ __forceinline__ void st_cs_v4(void *p, uint4 v)
 {
     asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z),

@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_v16(uint4 *cache, int
         uint4 *to = cache + d * stride_v16 + v0, buf[kMostVecs];
 #pragma unroll
         for (int u = 0; u < kMostVecs; ++u)
-            if (u < vecs && v0 + u * kCopyThreads < payload_v16) buf[u] = ld_nc_v4(from + u * kCopyThreads);
+            if (u < vecs && v0 + u * kCopyThreads < payload_v16) buf[u] = ld_v4(from + u * kCopyThreads);
 #pragma unroll
         for (int u = 0; u < kMostVecs; ++u)
             if (u < vecs && v0 + u * kCopyThreads < payload_v16) st_cs_v4(to + u * kCopyThreads, buf[u]);
@@ -429,12 +429,12 @@ __global__ void __launch_bounds__(256) append_kernel(const V *x, int64_t x_strid
     while (hi - lo > 1) {
         const int64_t step = (hi - lo + 31) / 32, at = lo + step * lane;
         const uint32_t below = __ballot_sync(0xffffffffu, at < hi && cu[at] <= tok);  // lane 0 always
-        const int64_t from = lo + step * (__popc(below) - 1);
+        const int64_t from = lo + step * (below != 0 ? __popc(below) - 1 : 0);  // 0 only if the offsets fall somewhere
         hi = from + step < hi ? from + step : hi;
         lo = from;
     }
     const int64_t r = load_index(req, itype, lo);
-    if (r < 0 || r >= t.requests) return;
+    if (r < 0 || r >= t.requests || tok >= cu[lo + 1]) return;
     const int64_t pos = length_of(t, r) - cu[lo + 1] + tok;
     if (pos < 0) return;
     const int32_t page = t.block_table[r * t.table_stride + pos / t.page_size];

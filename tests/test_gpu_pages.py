@@ -259,3 +259,26 @@ def test_a_step_in_a_graph():
             if s >= 0:
                 assert torch.equal(cache[t], before[s])
         d.check(p, "graph")
+
+
+def test_append_with_offsets_that_fall_stays_in_the_requests_pages():
+    """Offsets that break the contract: rows of the named requests may be written, nothing else."""
+    p = Pages(40, 8, 200, 4)
+    req = list(range(36))
+    p.reserve(req, [9] * 36)
+    d = Device(p)
+    pc = wl.paged_cache(200, 1, 4, 24, torch.float32, 4 * 24 + 8, seed=2, device=DEV)
+    before = pc.backing.clone()
+    cu = [0, 9, 30, 2, 5] + [50, 4] * 16
+    x = torch.ones(60, 24, device=DEV)
+    kda.kda_latent_append(x, ints(cu), ints(req), d.desc, pc.view)
+    torch.cuda.synchronize()
+    d.check(p, "tables")
+    changed = before != pc.backing
+    after = torch.zeros_like(before, dtype=torch.bool)
+    view = after.as_strided(pc.view.shape, pc.view.stride(), pc.front)
+    for r in req:
+        for j, page in enumerate(p.rows[r]):
+            if page >= 0:
+                view[page, 0, :min(4, 9 - 4 * j)] = True
+    assert not (changed & ~after).any()
