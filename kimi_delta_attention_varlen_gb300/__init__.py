@@ -76,8 +76,9 @@ def _ptr(t):
 
 def cache_descriptor(cache: torch.Tensor) -> KdaCache:
     """kda_cache for a [N, H, V, K] view with a dense inner block."""
-    _need(cache.dim() == 4, "cache must be a 4-D view [N, H, V, K]")
-    N, H, V, K = cache.shape
+    shape = cache.shape
+    _need(len(shape) == 4, "cache must be a 4-D view [N, H, V, K]")
+    N, H, V, K = shape
     row, head, vec, elem = cache.stride()
     _need((H == 1 or head == V * K) and (V == 1 or vec == K) and (K == 1 or elem == 1),
           "cache rows must hold a dense [H, V, K] block")
@@ -477,15 +478,17 @@ def kda_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, out, workspace, *, scal
 def kda_latent_append(x, cu, req, table: KdaPageTable, cache, stream=None) -> None:
     """Rows cu[i] .. cu[i+1]-1 of x [T, D] become the last tokens of request req[i] in its pages
     (kda_pages_reserve has made room and advanced the lengths)."""
-    _need(x.dim() == 2 and (x.shape[1] == 1 or x.stride(1) == 1), "x must be [T, D] with a unit inner stride")
-    _need(x.dtype == cache.dtype and x.shape[1] == cache.shape[3], "x must have the cache's dtype and row width")
-    _index_vector(req)
-    _need(cu.dtype == torch.int32 and cu.is_contiguous() and cu.numel() == req.numel() + 1,
-          "cu must be a contiguous int32 tensor of count + 1 offsets")
+    _need(x.dim() == 2, "x must be [T, D] with a unit inner stride")
     d = cache_descriptor(cache)
-    T, D = x.shape
-    rc = lib().kda_latent_append(_ptr(x), x.stride(0) if T > 1 else max(D, x.stride(0)), T, _ptr(cu), _ptr(req),
-                                 _itype_code(req), req.numel(), ctypes.byref(table), ctypes.byref(d), _stream(stream))
+    (T, D), (row, elem) = x.shape, x.stride()
+    _need(D == 1 or elem == 1, "x must be [T, D] with a unit inner stride")
+    _need(x.dtype == cache.dtype and D == d.k, "x must have the cache's dtype and row width")
+    _index_vector(req)
+    n = req.numel()
+    if cu.dtype != torch.int32 or not cu.is_contiguous() or cu.numel() != n + 1:
+        raise ValueError("cu must be a contiguous int32 tensor of count + 1 offsets")
+    rc = lib().kda_latent_append(x.data_ptr(), row if T > 1 else max(D, row), T, cu.data_ptr(), req.data_ptr(),
+                                 _itype_code(req), n, ctypes.byref(table), ctypes.byref(d), _stream(stream))
     _check(rc, "kda_latent_append")
 
 

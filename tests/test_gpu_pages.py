@@ -282,3 +282,24 @@ def test_append_with_offsets_that_fall_stays_in_the_requests_pages():
             if page >= 0:
                 view[page, 0, :min(4, 9 - 4 * j)] = True
     assert not (changed & ~after).any()
+
+
+@pytest.mark.parametrize("n_pages,requests", [(32769, 5), (70001, 2100)])
+def test_pools_of_many_blocks(n_pages, requests):
+    """Requests that take pages from many stretches of the pool, more of them than one pass of threads, and holes."""
+    rng = random.Random(n_pages)
+    width = 2 * n_pages // requests + 2
+    p = Pages(requests, width, n_pages, 3)
+    d = Device(p)
+    for step in range(3):
+        req = rng.sample(range(requests), requests)
+        new = [rng.randrange(0, width) for _ in req]
+        got, want = d.reserve(req, new), p.reserve(req, new)
+        assert got == want
+        d.check(p, step)
+        gone = rng.sample(range(requests), requests // 3 + 1)
+        kda.kda_pages_release(d.desc, ints(gone))
+        p.release(gone)
+    info, moves = p.compact()
+    assert d.compact() == (info, moves + [(-1, -1)] * (n_pages // 2 - len(moves)))
+    d.check(p, "compact")
