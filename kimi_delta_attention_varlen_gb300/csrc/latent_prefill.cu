@@ -4,12 +4,15 @@
 // per sequence and head, causal with the queries at the end of the keys, the keys visited in tiles
 // of 128 with a running maximum m and sum l a row.
 //
-// plan_kernel (one CTA) lists the query blocks (256 queries of one sequence) and decides how one
-// persistent CTA per SM shares the (block, head) pairs; a scheduling warp per CTA hands them to the others.
+// plan_kernel (one CTA; for few blocks a warp of every CTA) lists the query blocks (256 queries of one
+// sequence) and decides how one persistent CTA per SM shares the (block, head) pairs; a scheduling warp per
+// CTA hands them to the others.
 //   From kTurnRounds pairs a CTA on: in turn, by an atomic counter, in order of sequence, head and block,
 //     so that blocks of one sequence and head run side by side and their keys and values come from the
-//     L2 cache (a block reads 80 KB a key tile for 21 MFLOP: at the tensor cores' rate that is the HBM's).
-//     16 prompts of 512..8192 tokens, 32 heads: 3.76 ms against 4.18 ms longest first.
+//     L2 cache (a block reads 80 KB a key tile for 21 MFLOP: at the tensor cores' rate that is the HBM's);
+//     the first quarter of each sequence's blocks, the short ones, come last and even out the end.
+//     16 prompts of 512..8192 tokens, 32 heads: 3.76 ms against 4.18 ms longest first.  With fewer pairs a
+//     CTA the uneven end outweighs the cache (four prompts of 4096, 32 heads, 13 pairs a CTA: 570 / 563 us).
 //   Fewer: whole rounds of one pair a CTA, longest first and in turn from either end; of the last,
 //     partial round all key tiles lie on one line and each CTA takes an equal stretch of it.  A pair that
 //     falls into several stretches leaves unnormalised parts in the workspace, which join_kernel puts
@@ -71,6 +74,7 @@ constexpr int kStatusExpired = 7;
 constexpr int kBuckets = 1024;
 constexpr int kCutTiles = 10;
 constexpr int kTurnRounds = 8, kInTurn = -1;
+constexpr int kFewBlocks = 32;             // up to these every CTA makes its own list
 constexpr int kJoinCtas = 6;               // a SM: as many as stay resident
 constexpr int kReaders = 3 + 16;           // warps that read a segment
 
@@ -83,6 +87,7 @@ struct Params {
     int32_t *status;
     int32_t *n_blocks, *whole;   // blocks listed; pairs that are taken whole (a multiple of the grid, or all), kInTurn: see Walk
     int32_t *taken;              // pairs taken in turn
+    bool few;                    // at most kFewBlocks blocks, and fewer than kTurnRounds pairs a CTA: no plan_kernel
     int64_t *before;             // [max_blocks + 1] key tiles (of one head) before each block of the list, and in all
     int2 *table;                 // [max_blocks] (sequence, block of the sequence)
     int32_t *seq_off, *short_off;  // [num_seqs + 1] blocks before each sequence; of them those in the first quarter of theirs
@@ -130,6 +135,24 @@ struct Item {
     __device__ int32_t see(int s) const { return see0 + s * T; }
 };
 
+// The list of blocks, longest first: in global memory, or in a CTA's own shared memory.
+struct List {
+    const int2 *table;      // [blocks] (sequence, block of the sequence)
+    const int64_t *before;  // [blocks + 1]
+    int32_t blocks, whole;  // as n_blocks and whole of Params
+};
+
+// Pairs that are taken whole, of a list that is not taken in turn: all, or (a multiple of the grid) all but the last round's.
+__device__ __forceinline__ int32_t whole_pairs(const int64_t *before, int32_t blocks, int32_t heads, int32_t grid)
+{
+    const int32_t items = blocks * heads, whole = items / grid * grid;
+    if (whole == items) return items;
+    const int32_t b = whole / heads;
+    const int64_t longest = before[b + 1] - before[b];
+    const int64_t rest = before[blocks] * heads - before[b] * heads - whole % heads * longest;
+    return longest > rest / grid + kCutTiles ? whole : items;
+}
+
 // The work of one CTA in order: (block, head) pairs, and a stretch [j0, j1) of the key tiles of others.
 struct Walk {
     int32_t round, whole;   // rounds of whole pairs taken so far; pairs that are taken whole
@@ -139,30 +162,31 @@ struct Walk {
     int32_t j0, j1, slot;   // slot: where a part goes, 0 if it is not its pair's first; -1: the pair is whole
     Item it;
 
-    __device__ void begin(const Params &p, int32_t blocks)
+    __device__ void begin(const Params &p, const List &l)
     {
-        round = 0, whole = *p.whole, left = 0;
-        const int32_t H = p.a.h, items = blocks * H;
+        round = 0, whole = l.whole, left = 0;
+        const int32_t H = p.a.h, blocks = l.blocks, items = blocks * H;
         if (whole == kInTurn || whole >= items) return;
         // the line begins with pair `whole`
-        const int64_t base = p.before[whole / H] * H + whole % H * (p.before[whole / H + 1] - p.before[whole / H]);
-        const int64_t all = p.before[blocks] * H - base, n = all < gridDim.x ? all : gridDim.x;
+        const int64_t base = l.before[whole / H] * H + whole % H * (l.before[whole / H + 1] - l.before[whole / H]);
+        const int64_t all = l.before[blocks] * H - base, n = all < gridDim.x ? all : gridDim.x;
         if (blockIdx.x >= n) return;
         const int64_t w0 = all * blockIdx.x / n;
         left = all * (blockIdx.x + 1) / n - w0;
         int32_t lo = whole / H, hi = blocks;  // the block with before[lo] * H <= base + w0 < before[lo + 1] * H
         while (lo + 1 < hi) {
             const int32_t mid = (lo + hi) >> 1;
-            if (p.before[mid] * H <= base + w0) lo = mid;
+            if (l.before[mid] * H <= base + w0) lo = mid;
             else hi = mid;
         }
-        const int64_t rest = base + w0 - p.before[lo] * H, units = p.before[lo + 1] - p.before[lo];
+        const int64_t rest = base + w0 - l.before[lo] * H, units = l.before[lo + 1] - l.before[lo];
         next_pair = lo * H + static_cast<int32_t>(rest / units);
         next_j = static_cast<int32_t>(rest % units);
     }
     // The next pair or stretch; false: none.  By a whole warp.
-    __device__ bool next(const Params &p, int32_t items)
+    __device__ bool next(const Params &p, const List &l)
     {
+        const int32_t items = l.blocks * p.a.h;  // below 2^31: checked on the host
         if (whole == kInTurn) {
             // whoever comes, in order of sequence, head and block, the longest first; the first quarter of each
             // sequence's blocks, the short ones, in a second pass that evens out the end
@@ -198,7 +222,7 @@ struct Walk {
             pair = next_pair;
         }
         head = pair % p.a.h;
-        const int2 e = p.table[pair / p.a.h];
+        const int2 e = l.table[pair / p.a.h];
         it.load(p.a, e.x, e.y);
         j0 = 0, j1 = it.n, slot = -1;
         if (!entire) {
@@ -238,6 +262,9 @@ __device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xfff
 __host__ __device__ constexpr int64_t blocks_bound(int64_t total_q, int64_t num_seqs) { return total_q / kBlock + num_seqs; }
 
 // ------------------------------------------------------------------ the plan --
+// Place in the list by key tiles: the longest first (beyond kBuckets in order).
+__device__ __forceinline__ int32_t bucket(int32_t n) { return n < kBuckets ? kBuckets - 1 - n : 0; }
+
 __global__ void __launch_bounds__(1024) plan_kernel(Params p)
 {
     __shared__ int32_t hist[kBuckets];
@@ -300,7 +327,6 @@ __global__ void __launch_bounds__(1024) plan_kernel(Params p)
     // counting sort by key tiles, longest first; blocks of one length stay in order, so that the list, and with it
     // the places where pairs are cut, does not depend on the order of the atomics
     int2 e;
-    auto bucket = [&](int32_t n) { return n < kBuckets ? kBuckets - 1 - n : 0; };
     for (int32_t i = tid; i < blocks; i += 1024) atomicAdd(&hist[bucket(locate(i, &e))], 1);
     __syncthreads();
     int64_t total;
@@ -342,19 +368,63 @@ __global__ void __launch_bounds__(1024) plan_kernel(Params p)
     __syncthreads();
     if (tid == 0) {
         p.before[blocks] = units;
-        const int32_t items = blocks * a.h, whole = items / p.grid * p.grid;
-        *p.whole = items;
         *p.taken = 0;
-        if (items >= kTurnRounds * p.grid) {
-            *p.whole = kInTurn;
-        } else if (whole < items) {
-            const int32_t b = whole / a.h;
-            const int64_t longest = p.before[b + 1] - p.before[b];
-            const int64_t rest = units * a.h - p.before[b] * a.h - whole % a.h * longest;
-            if (longest > rest / p.grid + kCutTiles) *p.whole = whole;
-        }
+        *p.whole = blocks * a.h >= kTurnRounds * p.grid ? kInTurn : whole_pairs(p.before, blocks, a.h, p.grid);
     }
     for (int32_t c = tid; c < p.grid; c += 1024) p.item0[c] = p.item1[c] = -1;
+}
+
+// The same list of few blocks, by one warp of every CTA into its shared memory, a block a lane: a launch and its
+// latency less (three prompts of up to 100 tokens, 32 heads: 19.0 -> 12.6 us; five of 435..777 on prefixes of up to
+// 9000, 16 heads: 270 -> 262 us).
+__device__ __forceinline__ List plan_few(const Params &p, int2 *table, int64_t *before, int32_t *units)
+{
+    const LatentPrefillArgs &a = p.a;
+    const int lane = threadIdx.x & 31;
+    int32_t nb = 0;
+    if (lane < a.num_seqs) {
+        const int64_t n = clamp64(a.cu_q[lane + 1], a.total_q) - clamp64(a.cu_q[lane], a.total_q);
+        nb = n > 0 ? static_cast<int32_t>((n + kBlock - 1) / kBlock) : 0;
+    }
+    auto scan = [&](int64_t x) {  // inclusive
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    };
+    const int64_t end = scan(nb), sum = __shfl_sync(0xffffffffu, end, 31);
+    const int32_t blocks = static_cast<int32_t>(sum <= p.max_blocks ? sum : 0), off = static_cast<int32_t>(end - nb);
+    int32_t seq = -1, first = 0;  // the last sequence that begins at or before block `lane`
+    for (int b = 0; b < a.num_seqs; ++b) {
+        const int32_t at = __shfl_sync(0xffffffffu, off, b);
+        if (at <= lane) seq = b, first = at;
+    }
+    const bool mine = lane < blocks;
+    int32_t place = INT32_MAX, n = 0;
+    if (mine) {
+        Item it;
+        it.load(a, seq, lane - first);
+        n = it.n;
+        place = bucket(n);
+    }
+    int32_t rank = 0;
+    for (int b = 0; b < blocks; ++b) {
+        const int32_t other = __shfl_sync(0xffffffffu, place, b);
+        rank += other < place || (other == place && b < lane) ? 1 : 0;
+    }
+    if (mine) {
+        table[rank] = make_int2(seq, lane - first);
+        units[rank] = n > 0 ? n : 1;
+        if (blockIdx.x == 0) p.table[rank] = make_int2(seq, lane - first);  // for the join
+    }
+    __syncwarp();
+    const int64_t through = scan(mine ? units[lane] : 0);
+    if (mine) before[lane + 1] = through;
+    if (lane == 0) before[0] = 0;
+    __syncwarp();
+    return List{table, before, blocks, whole_pairs(before, blocks, a.h, p.grid)};
 }
 
 // ------------------------------------------------------------------ the kernel --
@@ -381,6 +451,10 @@ struct Shared {
     float pair[2][2][T];  // by query tile, half, row: what the two threads of a row tell each other
     uint32_t not_finite[2];  // by parity of the segment: its number + 1 once a value was taken out
     uint32_t tmem_base;
+    List few;
+    int2 few_table[kFewBlocks];
+    int64_t few_before[kFewBlocks + 1];
+    int32_t few_units[kFewBlocks];
 };
 constexpr int kSmem = OFF_SHARED + sizeof(Shared);
 static_assert(kSmem <= 232448, "227 KB");
@@ -412,6 +486,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
     tc::fence_after_sync();
     before_next();
     after_previous();
+    if (warp == 3 && p.few) {
+        if (lane == 0) {
+            p.item0[blockIdx.x] = p.item1[blockIdx.x] = -1;
+            if (blockIdx.x == 0) *p.status = 0;
+        }
+        const List list = plan_few(p, sh.few_table, sh.few_before, sh.few_units);
+        if (lane == 0) sh.few = list;
+        __syncwarp();
+    }
     const uint32_t tmem = uniform(sh.tmem_base);
     uint32_t nseg = 0;  // segments taken
 
@@ -603,11 +686,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             mbar_wait(&bar.drain[s], 0, kWaitLimit);
         } else {
             // -------------------------------------------------------- scheduling
-            const int32_t blocks = *p.n_blocks, items = blocks * p.a.h;  // below 2^31: checked on the host
+            List list{p.table, p.before, 0, 0};
+            if (p.few) list = sh.few;
+            else list.blocks = *p.n_blocks, list.whole = *p.whole;
             Walk w;
-            w.begin(p, blocks);
+            w.begin(p, list);
             for (bool more = true; more; ++nseg) {
-                more = w.next(p, items);
+                more = w.next(p, list);
                 if (nseg > 1 && !all_wait(&bar.seg_free[nseg & 1], ((nseg >> 1) & 1) ^ 1)) break;
                 if (lane == 0) {
                     Segment &g = sh.seg[nseg & 1];
@@ -973,7 +1058,8 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st)
     if ((e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess ||
         (e = cudaFuncSetAttribute(join_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
         return e;
-    if ((e = launch_overlapped(plan_kernel, dim3(1), dim3(1024), 0, st, p)) != cudaSuccess) return e;
+    p.few = p.max_blocks <= kFewBlocks && p.max_blocks * a.h < static_cast<int64_t>(kTurnRounds) * p.grid;
+    if (!p.few && (e = launch_overlapped(plan_kernel, dim3(1), dim3(1024), 0, st, p)) != cudaSuccess) return e;
     e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     // the register split (setmaxnreg) needs a launch with exactly 96 registers a thread

@@ -379,3 +379,12 @@ def test_prefill_and_decode_are_the_same_attention():
     want = torch.einsum("hd,hde->he", lat[0, 0].double(), wv.double())
     # each side rounds its keys or queries, probabilities and outputs to bf16: a few 2^-9 of the values' size
     assert (out[-1].double() - want).abs().max() <= 6 * 2.0 ** -9 * v.double().abs().max()
+
+
+@pytest.mark.parametrize("nq,nk", [([10] * 31, [10] * 31), ([10] * 32, [10] * 32), ([0, 9] * 14 + [300], [0, 9] * 14 + [9000]),
+                                   ([40] * 39 + [500], [6000] + [40 + 130 * (i % 3) for i in range(38)] + [7000]),
+                                   ([8192, 1], [8192, 3])])
+@pytest.mark.parametrize("heads", [1, 4])
+def test_prefill_lists_of_few_and_of_many_blocks(nq, nk, heads):
+    """Batches around 32 blocks of queries, whole or cut, with empty sequences between."""
+    check_prefill(nq, nk, heads, seed=len(nq) + heads)
