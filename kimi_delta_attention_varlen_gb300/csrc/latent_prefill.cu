@@ -11,7 +11,7 @@
 //     so that blocks of one sequence and head run side by side and their keys and values come from the
 //     L2 cache (a block reads 80 KB a key tile for 21 MFLOP: at the tensor cores' rate that is the HBM's);
 //     the first quarter of each sequence's blocks, the short ones, come last and even out the end.
-//     In turn / longest first: 16 prompts of 512..8192 tokens, 32 heads (87 pairs a CTA) 3.76 / 4.18 ms; two of
+//     In turn / longest first: 16 prompts of 512..8192 tokens, 32 heads (68 pairs a CTA) 3.76 / 4.18 ms; two of
 //     8192, 32 heads (13 pairs) 1.05 / 1.08 ms; four of 4096, 32 heads (13 pairs) 570 / 563 us; twelve of
 //     300..3000 on 2000, 16 heads (9 pairs) 569 us both.
 //   Fewer: whole rounds of one pair a CTA, longest first and in turn from either end; of the last,
