@@ -23,7 +23,7 @@ constexpr int kThreads = 1024;
 constexpr int kWords = kBlockPages / 32;     // bitmap words of one block
 constexpr int kCluster = 8;                  // CTAs that count and rank together
 constexpr int kCopyThreads = 256;
-constexpr int kMostVecs = 8;                 // 16-byte vectors in flight per thread, at most
+constexpr int kMostVecs = 10;                // 16-byte vectors in flight per thread, at most
 
 // Workspace: a header of four words, then the arrays below (4-byte elements).
 struct Plan {
@@ -408,8 +408,9 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(kda_page_table t, Pl
 }
 
 // Page copies, one tile of one page per CTA step: the page in as few equal tiles as kMostVecs vectors a thread allow
-// (a page of 64 latent rows, 73,728 bytes: three tiles of six).  With four vectors a thread, and so a half-empty last
-// tile, the call on 6000 such pages took 170 us with its plan; 157 us with equal tiles (6.1 TB/s in the copy).
+// (a page of 64 latent rows, 73,728 bytes: two tiles of nine).  The call on 6000 such pages with its plan: 152.6 us
+// (6.2 TB/s in the copy); at most 8 vectors (three tiles of six) 158, 12 (two of nine, fewer CTAs an SM) 154, 16 162,
+// four with a half-empty last tile 170; a warp an SM with bulk copies through shared memory 168.
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_v16(uint4 *cache, int64_t n_rows, int64_t stride_v16,
                                                                int64_t payload_v16, int32_t vecs, const void *src, const void *dst,
                                                                int32_t itype, int64_t count)
