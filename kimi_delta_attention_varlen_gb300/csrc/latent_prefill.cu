@@ -75,6 +75,7 @@ constexpr int kStatusExpired = 7;
 constexpr int kBuckets = 1024;
 constexpr int kCutTiles = 10;
 constexpr int kTurnRounds = 8, kInTurn = -1;
+constexpr int kMostCtas = 256;
 constexpr int kFewBlocks = 32;             // up to these every CTA makes its own list
 constexpr int kJoinCtas = 6;               // a SM: as many as stay resident
 constexpr int kReaders = 3 + 16;           // warps that read a segment
@@ -157,23 +158,76 @@ __device__ __forceinline__ int32_t whole_pairs(const int64_t *before, int32_t bl
 // The work of one CTA in order: (block, head) pairs, and a stretch [j0, j1) of the key tiles of others.
 struct Walk {
     int32_t round, whole;   // rounds of whole pairs taken so far; pairs that are taken whole
-    int32_t next_pair, next_j;  // behind the whole pairs: where the stretch goes on
+    bool cut;                   // the stretch is known
+    int32_t next_pair, next_j;  // where it goes on
     int64_t left;               // key tiles of the stretch to come
     int32_t head, pair;
     int32_t j0, j1, slot;   // slot: where a part goes, 0 if it is not its pair's first; -1: the pair is whole
     Item it;
 
-    __device__ void begin(const Params &p, const List &l)
+    __device__ void begin(const List &l) { round = 0, whole = l.whole, left = 0, cut = false; }
+    // How much of the line's `all` key tiles this CTA takes, and what those before it take.
+    __device__ void share(const List &l, int32_t H, int64_t all, int64_t *start)
     {
-        round = 0, whole = l.whole, left = 0;
-        const int32_t H = p.a.h, blocks = l.blocks, items = blocks * H;
-        if (whole == kInTurn || whole >= items) return;
-        // the line begins with pair `whole`
+        const int32_t grid = gridDim.x, lane = threadIdx.x & 31;
+        auto sum = [&](int64_t x) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            return x;
+        };
+        int32_t load[kMostCtas / 32];  // key tiles of CTA 32 k + lane so far; -1: none for it here
+#pragma unroll
+        for (int k = 0; k < kMostCtas / 32; ++k) {
+            const int32_t c = 32 * k + lane;
+            load[k] = c < grid ? 0 : -1;
+            for (int32_t r = 0; r < whole / grid && c < grid; ++r) {
+                const int32_t b = (r * grid + (r & 1 ? grid - 1 - c : c)) / H;
+                load[k] += static_cast<int32_t>(l.before[b + 1] - l.before[b]);
+            }
+        }
+        int64_t level, over;  // the sum that all are filled up to, and one more for the first `over`
+        for (int32_t n_before = 0;;) {
+            int64_t have = 0, n = 0;
+#pragma unroll
+            for (int k = 0; k < kMostCtas / 32; ++k) have += load[k] >= 0 ? load[k] : 0, n += load[k] >= 0 ? 1 : 0;
+            have = sum(have), n = sum(n);
+            level = (all + have) / n, over = (all + have) % n;
+            if (n == n_before) break;
+            n_before = static_cast<int32_t>(n);
+#pragma unroll
+            for (int k = 0; k < kMostCtas / 32; ++k)
+                if (load[k] > level) load[k] = -1;
+        }
+        int64_t before = 0, mine = 0;
+        int32_t rank = 0;
+#pragma unroll
+        for (int k = 0; k < kMostCtas / 32; ++k) {
+            const uint32_t takes = __ballot_sync(0xffffffffu, load[k] >= 0);
+            const int64_t x = load[k] < 0 ? 0 : level - load[k] + (rank + __popc(takes & ((1u << lane) - 1)) < over ? 1 : 0);
+            rank += __popc(takes);
+            if (32 * k + lane < static_cast<int32_t>(blockIdx.x)) before += x;
+            if (32 * k + lane == static_cast<int32_t>(blockIdx.x)) mine = x;
+        }
+        *start = sum(before), left = sum(mine);
+    }
+    // This CTA's stretch of the line that begins with pair `whole`, by a whole warp: CTAs whose pairs were shorter take
+    // more of it, so that all have the same sum of key tiles (but for those whose pairs alone are more).
+    __device__ void stretch(const Params &p, const List &l)
+    {
+        cut = true;
+        const int32_t H = p.a.h, blocks = l.blocks, items = blocks * H, grid = gridDim.x;
+        if (whole >= items) return;
         const int64_t base = l.before[whole / H] * H + whole % H * (l.before[whole / H + 1] - l.before[whole / H]);
-        const int64_t all = l.before[blocks] * H - base, n = all < gridDim.x ? all : gridDim.x;
-        if (blockIdx.x >= n) return;
-        const int64_t w0 = all * blockIdx.x / n;
-        left = all * (blockIdx.x + 1) / n - w0;
+        const int64_t all = l.before[blocks] * H - base;
+        int64_t w0 = 0;
+        if (whole == 0) {  // no pair yet: equal stretches
+            const int64_t n = all < grid ? all : grid, c = static_cast<int32_t>(blockIdx.x) < n ? blockIdx.x : n;
+            w0 = all * c / n;
+            left = c < n ? all * (c + 1) / n - w0 : 0;
+        } else {
+            share(l, H, all, &w0);
+        }
+        if (left == 0) return;
         int32_t lo = whole / H, hi = blocks;  // the block with before[lo] * H <= base + w0 < before[lo + 1] * H
         while (lo + 1 < hi) {
             const int32_t mid = (lo + hi) >> 1;
@@ -219,6 +273,7 @@ struct Walk {
             if (at >= items) return false;  // beyond the end of a last round that runs whole
             pair = at;
         } else {
+            if (!cut) stretch(p, l);
             if (left <= 0) return false;
             pair = next_pair;
         }
@@ -432,7 +487,7 @@ __device__ __forceinline__ List plan_few(const Params &p, int2 *table, int64_t *
 struct Bars {
     // by parity of the key tile: its key panels and value panels, loaded and handed back
     uint64_t k_full[2][3], k_free[2], v_full[2], v_free[2];  // k_full: by panel
-    uint64_t q_full[2], q_free[2], s[2], p[2], o[2], drain[2];  // by query tile
+    uint64_t q_full[2], q_free[2], s[2], p[2][2], o[2], drain[2];  // by query tile
     uint64_t seg_full[2], seg_free[2];
 };
 
@@ -455,7 +510,6 @@ struct Shared {
     List few;
     int2 few_table[kFewBlocks];
     int64_t few_before[kFewBlocks + 1];
-    int32_t few_units[kFewBlocks];
 };
 constexpr int kSmem = OFF_SHARED + sizeof(Shared);
 static_assert(kSmem <= 232448, "227 KB");
@@ -478,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             mbar_init(&bar.k_full[s][0], 1), mbar_init(&bar.k_full[s][1], 1), mbar_init(&bar.k_full[s][2], 1), mbar_init(&bar.k_free[s], 2), mbar_init(&bar.v_full[s], 1), mbar_init(&bar.v_free[s], 2);  // handed back by both query tiles
             mbar_init(&bar.drain[s], 1), mbar_init(&bar.seg_full[s], 1), mbar_init(&bar.seg_free[s], kReaders);
             mbar_init(&bar.q_full[s], 1), mbar_init(&bar.q_free[s], 1), mbar_init(&bar.s[s], 1), mbar_init(&bar.o[s], 1);
-            mbar_init(&bar.p[s], 2 * T);
+            mbar_init(&bar.p[s][0], 2 * T), mbar_init(&bar.p[s][1], 2 * T);
         }
         fence_mbar_init();
     }
@@ -492,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             p.item0[blockIdx.x] = p.item1[blockIdx.x] = -1;
             if (blockIdx.x == 0) *p.status = 0;
         }
-        const List list = plan_few(p, sh.few_table, sh.few_before, sh.few_units);
+        const List list = plan_few(p, sh.few_table, sh.few_before, reinterpret_cast<int32_t *>(sh.pair));  // not in use yet
         if (lane == 0) sh.few = list;
         __syncwarp();
     }
@@ -634,13 +688,26 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 const bool there = more && __all_sync(0xffffffffu, mbar_test(&bar.k_full[n & 1][0], par) &&
                                                                       mbar_test(&bar.k_full[n & 1][1], par) &&
                                                                       mbar_test(&bar.k_full[n & 1][2], par));
-                if (!all_wait(&bar.p[s], pvs++ & 1)) return false;
+                // P comes in two parts: the first half of each thread's keys, then the second
+                if (!all_wait(&bar.p[s][0], pvs & 1)) return false;
                 tc::fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        tc::mma_bf16_ts(to, ts + 8 * ks, b0 + 128 * ks, kIdO, ks > 0 || !fresh ? 1u : 0u);
-                        tc::mma_bf16_ts(to + 64, ts + 8 * ks, b1 + 128 * ks, kIdO, ks > 0 || !fresh ? 1u : 0u);
+                    for (int i = 0; i < 4; ++i) {
+                        const int ks = 4 * (i >> 1) + (i & 1);
+                        tc::mma_bf16_ts(to, ts + 8 * ks, b0 + 128 * ks, kIdO, i > 0 || !fresh ? 1u : 0u);
+                        tc::mma_bf16_ts(to + 64, ts + 8 * ks, b1 + 128 * ks, kIdO, i > 0 || !fresh ? 1u : 0u);
+                    }
+                }
+                __syncwarp();
+                if (!all_wait(&bar.p[s][1], pvs++ & 1)) return false;
+                tc::fence_after_sync();
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int ks = 4 * (i >> 1) + (i & 1) + 2;
+                        tc::mma_bf16_ts(to, ts + 8 * ks, b0 + 128 * ks, kIdO, 1u);
+                        tc::mma_bf16_ts(to + 64, ts + 8 * ks, b1 + 128 * ks, kIdO, 1u);
                     }
                     if (single) {  // what the rounding left off, too
 #pragma unroll
@@ -691,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             if (p.few) list = sh.few;
             else list.blocks = *p.n_blocks, list.whole = *p.whole;
             Walk w;
-            w.begin(p, list);
+            w.begin(list);
             for (bool more = true; more; ++nseg) {
                 more = w.next(p, list);
                 if (nseg > 1 && !all_wait(&bar.seg_free[nseg & 1], ((nseg >> 1) & 1) ^ 1)) break;
@@ -733,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             const Segment *seg = next_segment();
             if (pair_any(gave_up) || seg == nullptr) break;
             // a row's 64 scores fill the registers: what is not needed for each tile stays in the segment
-            const int32_t nt = seg->tiles[s], limit = (row < seg->rows[s] ? seg->see + s * T + row : 0) - seg->j0 * T;  // keys seen
+            const int32_t nt = seg->tiles[s], limit = row < seg->rows[s] ? seg->see + s * T + row - seg->j0 * T : INT32_MAX / 2;  // keys seen; no query: no mask to pay for
             const bool single = (seg->single >> s & 1) != 0;
             float m = -INFINITY, l = 0.f, lr = 0.f;  // l, lr: of this thread's keys
             for (int32_t j = 0; j < nt; ++j, ++steps) {
@@ -824,10 +891,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                             sum_r = add2(sum_r, make_float2(bf16_lo(pk[q]), bf16_hi(pk[q])));
                         }
                         tc::st16(ts + kHalf / 2 * half + c, pk);
+                        tc::wait_st();
+                        tc::fence_before_sync();
+                        mbar_arrive(&bar.p[s][c >> 4]);
                     }
-                    tc::wait_st();
-                    tc::fence_before_sync();
-                    mbar_arrive(&bar.p[s]);
                 } else {  // a single key tile: what the rounding leaves off goes into the other half of S_s
 #pragma unroll
                     for (int c = 0; c < kHalf / 2; c += 16) {
@@ -847,7 +914,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                     sum_r = sum;
                     tc::wait_st();
                     tc::fence_before_sync();
-                    mbar_arrive(&bar.p[s]);
+                    mbar_arrive(&bar.p[s][0]);
+                    mbar_arrive(&bar.p[s][1]);
                 }
                 l += sum.x + sum.y;
                 lr += sum_r.x + sum_r.y;
@@ -955,25 +1023,28 @@ __global__ void __launch_bounds__(256) join_kernel(Params p)
         Item it;
         it.load(p.a, e.x, e.y);
         if ((row & (T - 1)) >= it.rows(row / T)) continue;
-        int32_t parts = 1;  // a pair's parts stand next to each other
+        int32_t last = c;  // CTAs between that took nothing hold other numbers
         for (int32_t j0 = c + 1; j0 < p.grid; j0 += 32) {
-            const int32_t j = j0 + lane;
-            const uint32_t mine = __ballot_sync(0xffffffffu, j < p.grid && p.item0[j] == pair);
-            parts += __popc(mine);
-            if (mine != 0xffffffffu) break;
+            const uint32_t mine = __ballot_sync(0xffffffffu, j0 + lane < p.grid && p.item0[j0 + lane] == pair);
+            if (mine != 0) last = j0 + 31 - __clz(mine);
         }
-        auto at = [&](int32_t j) { return (2 * static_cast<int64_t>(c + j) + (j == 0 ? 1 : 0)) * kBlock + row; };
+        auto at = [&](int32_t j) { return (2 * static_cast<int64_t>(j) + (j == c ? 1 : 0)) * kBlock + row; };
         float m = -INFINITY, l = 0.f, lr = 0.f;
-        for (int32_t j = lane; j < parts; j += 32) m = fmaxf(m, p.ml[at(j)].x);
+        for (int32_t j = c + lane; j <= last; j += 32) {
+            const float x = p.ml[at(j)].x;
+            if (j == c || p.item0[j] == pair) m = fmaxf(m, x);
+        }
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int32_t j = 0; j < parts; ++j) {
+        for (int32_t j = c; j <= last; ++j) {
+            const int32_t of = p.item0[j];
             const float4 ml = p.ml[at(j)];
-            if (ml.y == 0.f) continue;  // a part in which the row saw nothing (and whose row may not be written)
-            const float f = ex2_approx(ml.x - (m == -INFINITY ? 0.f : m));
             const float4 x = *reinterpret_cast<const float4 *>(p.part + at(j) * DV + 4 * lane);
+            // not a part of this pair, or one in which the row saw nothing (and whose row may not be written)
+            if ((j != c && of != pair) || ml.y == 0.f) continue;
+            const float f = ex2_approx(ml.x - (m == -INFINITY ? 0.f : m));
             l += f * ml.y;
             lr += f * ml.z;
             o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
@@ -1016,7 +1087,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // [status and counts | blocks | offsets | who holds parts | their statistics | parts]; returns the size.
 size_t layout(char *ws, int64_t total_q, int64_t num_seqs, Params *p)
 {
-    const size_t n = static_cast<size_t>(blocks_bound(total_q, num_seqs)), grid = static_cast<size_t>(sm_count());
+    const size_t n = static_cast<size_t>(blocks_bound(total_q, num_seqs)), grid = static_cast<size_t>(sm_count() < kMostCtas ? sm_count() : kMostCtas);
     const size_t before = 256, table = before + (n + 1) * 8, seq = table + n * 8, items = up256(seq + (num_seqs + 1) * 8);
     const size_t ml = up256(items + 8 * grid), part = ml + 2 * grid * kBlock * 16, end = part + 2 * grid * kBlock * DV * 4;
     if (p != nullptr) {
