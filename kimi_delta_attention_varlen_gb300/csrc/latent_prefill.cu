@@ -11,16 +11,17 @@
 //     so that blocks of one sequence and head run side by side and their keys and values come from the
 //     L2 cache (a block reads 80 KB a key tile for 21 MFLOP: at the tensor cores' rate that is the HBM's);
 //     the first quarter of each sequence's blocks, the short ones, come last and even out the end.
-//     In turn / longest first: 16 prompts of 512..8192 tokens, 32 heads (68 pairs a CTA) 3.76 / 4.18 ms; two of
-//     8192, 32 heads (13 pairs) 1.05 / 1.08 ms; four of 4096, 32 heads (13 pairs) 570 / 563 us; twelve of
-//     300..3000 on 2000, 16 heads (9 pairs) 569 us both.
-//   Fewer: whole rounds of one pair a CTA, longest first and in turn from either end; of the last,
-//     partial round all key tiles lie on one line and each CTA takes an equal stretch of it.  A pair that
-//     falls into several stretches leaves unnormalised parts in the workspace, which join_kernel puts
-//     together in order of their keys.  Parts cost about what kCutTiles key tiles do (queries loaded again,
-//     parts written and joined: 10 us), so the last round runs whole where its longest pair is not that much
-//     longer than an equal stretch.  Cut against whole: 1000 queries on 16000 keys, 4 heads 62 / 244 us;
-//     8192 queries, 2 heads 73 / 122 us; four prompts of up to 2000, 8 heads 65 / 55 us (these run whole).
+//     In turn / longest first: 16 prompts of 512..8192 tokens, 32 heads (68 pairs a CTA) 3.55 / 4.11 ms; two of
+//     8192, 32 heads (13 pairs) 0.98 / 1.03 ms; twelve of 300..3000 on 2000, 16 heads (9 pairs) 529 / 551 us;
+//     four of 2000, 32 heads (7 pairs) 192 / 183 us; one of 4096, 32 heads (3 pairs) 187 / 135 us.
+//   Fewer: whole rounds of one pair a CTA, longest first and in turn from either end; of the last, partial
+//     round all key tiles lie on one line, of which each CTA takes the stretch that fills its sum of key tiles up
+//     to a level common to all.  A pair that falls into several stretches leaves unnormalised parts in the
+//     workspace, which join_kernel puts together in order of their keys.  Parts cost about what kCutTiles key
+//     tiles do (queries loaded again, parts written and joined: 10 us), so the last round runs whole where its
+//     longest pair is not that much longer than an equal stretch.  Cut / whole: 1000 queries on 16000 keys, 4 heads
+//     59 / 212 us; 8192 queries, 2 heads 84 / 124 us; three of 578..777 on 7000..9000, 32 heads 285 / 332 us; four
+//     prompts of up to 2000, 8 heads 46 / 42 us, one of 4096, 32 heads 148 / 136 us (these run whole).
 // Which CTA takes a pair never changes what is computed, and where pairs are cut depends on the lengths alone.
 // A block is two query tiles s = 0, 1 of 128 rows that share the key and value tiles:
 //   S_s   = Q_s K^T     M = 128, N = 128, K = 192 (two nope panels and the shared rope panel)
@@ -31,6 +32,9 @@
 // row) and the epilogue.
 // Key and value panels (128 tokens x 64, 16 KB, 128-byte swizzle) pass through one ring of eight: per
 // key tile three key panels (K-major B), then two value panels (MN-major B).
+//
+// The probabilities of a tile are handed to the second product in two parts, so that it runs on the first while the
+// exponentials of the second are taken (16 prompts 3.80 -> 3.56 ms).
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the last rescale.  The
 // probabilities are rounded to bf16, the tensor cores' operand type; the output is normalised by the
@@ -75,7 +79,7 @@ constexpr int kStatusExpired = 7;
 constexpr int kBuckets = 1024;
 constexpr int kCutTiles = 10;
 constexpr int kTurnRounds = 8, kInTurn = -1;
-constexpr int kMostCtas = 256;
+constexpr int kMostCtas = 256;             // of the grid (one per SM)
 constexpr int kFewBlocks = 32;             // up to these every CTA makes its own list
 constexpr int kJoinCtas = 6;               // a SM: as many as stay resident
 constexpr int kReaders = 3 + 16;           // warps that read a segment
