@@ -477,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            z[e][c0 / 4 + 2 * j] = __uint_as_float(s[4 * j + 2 * e]) * p.scale_log2;
-                            z[e][c0 / 4 + 2 * j + 1] = __uint_as_float(s[4 * j + 2 * e + 1]) * p.scale_log2;
+                            z[e][c0 / 4 + 2 * j] = __uint_as_float(s[4 * j + 2 * e]);
+                            z[e][c0 / 4 + 2 * j + 1] = __uint_as_float(s[4 * j + 2 * e + 1]);
                         }
                 }
                 tc::fence_before_sync();
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
 #pragma unroll
                     for (int j = 1; j < T / 4; ++j) mx = fmaxf(mx, z[e][j]);
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * p.scale_log2;
                     float c = 1.f;
                     if (m[e] == -INFINITY) {
                         m[e] = mx;  // nothing summed yet
@@ -507,16 +507,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                     }
                     if (t == 0) corr[i & 1][16 * quad + 8 * e + g] = c;
                     const float base = m[e] == -INFINITY ? 0.f : m[e];
-                    float sum = 0.f, sum_r = 0.f;
+                    const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
+                    float2 sum = make_float2(0.f, 0.f), sum_r = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int j = 0; j < T / 8; ++j) {
-                        const float a = ex2_approx(z[e][2 * j] - base), b = ex2_approx(z[e][2 * j + 1] - base);
-                        sum += a + b;
-                        pk[e][j] = pack_bf16x2(a, b);
-                        sum_r += bf16_lo(pk[e][j]) + bf16_hi(pk[e][j]);
+                        float2 x = fma2(make_float2(z[e][2 * j], z[e][2 * j + 1]), sc, nb);
+                        x.x = ex2_approx(x.x);
+                        x.y = ex2_approx(x.y);
+                        sum = add2(sum, x);
+                        pk[e][j] = pack_bf16x2(x.x, x.y);
+                        sum_r = add2(sum_r, make_float2(bf16_lo(pk[e][j]), bf16_hi(pk[e][j])));
                     }
-                    l[e] += sum;
-                    lr[e] += sum_r;
+                    l[e] += sum.x + sum.y;
+                    lr[e] += sum_r.x + sum_r.y;
                 }
             } else {
                 mbar_arrive(&bar.s_free[i & 1]);
@@ -580,8 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                         const float base = m[e] == -INFINITY ? 0.f : m[e];
 #pragma unroll
                         for (int j = 0; j < T / 8; ++j)
-                            pk[e][j] = pack_bf16x2(ex2_approx(z[e][2 * j] - base) - bf16_lo(pk[e][j]),
-                                                   ex2_approx(z[e][2 * j + 1] - base) - bf16_hi(pk[e][j]));
+                            pk[e][j] = pack_bf16x2(ex2_approx(fmaf(z[e][2 * j], p.scale_log2, -base)) - bf16_lo(pk[e][j]),
+                                                   ex2_approx(fmaf(z[e][2 * j + 1], p.scale_log2, -base)) - bf16_hi(pk[e][j]));
                         lr[e] = l[e];
                     }
                 }
