@@ -37,8 +37,8 @@
 // What bounds it: with one token a request the cache's bytes (512 requests of 512..8192 tokens, 32 heads, dl = 512:
 // 420..440 us = 5.9..6.2 TB/s), a few short requests the latency of two launches, the first tile and the join (one of
 // 1009 tokens: 14 us), with four draft tokens and 128 heads the ring: 64 query rows leave room for two tiles, each of which
-// holds its slots for 7,000 cycles from copy to second product, 1,920 of them MMAs (33 requests of 1500..6001 tokens: 220 us
-// = 640 TFLOP/s).  64-token tiles because of the same ring: 512 requests took 617 us with 96 and 572 with 128 where they
+// holds its slots for 7,000 cycles from copy to second product, 1,920 of them MMAs (33 requests of 1500..6001 tokens: 224 us
+// = 627 TFLOP/s; with P handed over in two parts 234 us, since the slots then come back later).  64-token tiles because of the same ring: 512 requests took 617 us with 96 and 572 with 128 where they
 // took 439 with 64.  Four copying warps instead of two: 425 / 420 us, drafts alike.
 //
 // Every wait is bounded; an expired one sets the workspace's status word (6) and ends the CTA.
