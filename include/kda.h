@@ -579,9 +579,9 @@ typedef struct {
  * Built: dl in {256, 512}, dr == 64, page_size a multiple of 8, bf16.
  * Errors: KDA_ERR_NULL, _DTYPE (io or cache not bf16), _LAYOUT, _SHAPE (sizes
  * below 1 (batch below 0), cache h / k not 1 / dl + dr, table_stride < width),
- * _UNSUPPORTED (dl, dr, page_size), _RANGE (scale not positive and finite,
- * batch * L * h >= 2^31, width * page_size >= 2^31, L * h > 65536), _ALIGN,
- * _WORKSPACE, _CUDA.
+ * _UNSUPPORTED (dl, dr, page_size), _RANGE (scale not positive, or above
+ * 2.35e38, where scale * log2(e) leaves fp32; batch * L * h >= 2^31,
+ * width * page_size >= 2^31, L * h > 65536), _ALIGN, _WORKSPACE, _CUDA.
  * batch == 0 launches nothing.
  * ---------------------------------------------------------------------- */
 size_t kda_latent_decode_workspace_size(int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr);
@@ -619,9 +619,9 @@ int kda_latent_decode(const void *q, int32_t io_dtype, int64_t batch, int32_t L,
  *   workspace kda_latent_prefill_workspace_size(...) bytes, as above
  * Built: dn == dv == 128, dr == 64, bf16.  Errors as kda_latent_decode
  * (_SHAPE: negative strides, a token stride of 0 with several tokens; _RANGE:
- * scale not positive and finite, total_q or total_k >= 2^31 - 256, num_seqs >=
- * 2^24, h > 1024, (total_q / 256 + num_seqs) * h >= 2^31, a stride of 2^38
- * elements or more).
+ * the scale as there, total_q or total_k >= 2^31 - 256, num_seqs >= 2^24, h >
+ * 1024, (total_q / 256 + num_seqs) * h >= 2^31, a stride of 2^38 elements or
+ * more).
  * total_q == 0 launches nothing.
  * ---------------------------------------------------------------------- */
 size_t kda_latent_prefill_workspace_size(int64_t total_q, int64_t num_seqs, int32_t h);

@@ -410,8 +410,9 @@ int check_workspace(const void *ws, size_t have, size_t need)
     return aligned(ws, 256) && have >= need ? KDA_OK : KDA_ERR_WORKSPACE;
 }
 
-// A softmax scale: positive and finite (its running maximum is taken before the scale is applied).
-bool valid_scale(float s) { return s > 0.f && s <= 3.0e38f; }
+// A softmax scale: positive (its running maximum is taken before the scale is applied), and finite once the
+// kernels have multiplied it by log2(e) for their base-2 exponentials.
+bool valid_scale(float s) { return s > 0.f && s <= 2.35e38f; }
 
 int check_page_table(const kda_page_table *t)
 {

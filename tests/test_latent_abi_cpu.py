@@ -214,3 +214,12 @@ def test_binding_refusals():
         kda.kda_latent_append(torch.zeros(3, 576), i3, i3[:2], t, c, stream=0)
     with pytest.raises(TypeError):
         kda.kda_pages_copy(c, i3.float(), i3.float(), stream=0)
+
+
+@pytest.mark.parametrize("scale,want", [(0.0, RANGE), (-1.0, RANGE), (float("nan"), RANGE), (float("inf"), RANGE), (3.0e38, RANGE), (2.4e38, RANGE),
+                                        (2.35e38, WORKSPACE), (1e-45, WORKSPACE)])
+def test_scales(L, scale, want):
+    """The kernels multiply the scale by log2(e) in fp32: what overflows there is refused (a scale that passes goes on to
+    the workspace, which is too small here)."""
+    assert decode(L, scale=scale, ws_bytes=0) == want
+    assert prefill(L, scale=scale, ws_bytes=0) == want
