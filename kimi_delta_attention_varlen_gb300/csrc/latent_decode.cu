@@ -29,6 +29,10 @@
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than 2^8 since the last
 // rescale (the exponents are relative to that older maximum, exact in fp32 and in bf16's range).
+// The tensor cores cut every product off at 2^-25 of the sum that it joins (the bits of a 26-bit window), so a sum of N
+// may lack N 2^-25 of its size: 1.3 % after a million tokens behind one that holds half of the weight.  After kSumTiles
+// tiles of a segment the accumulator, l and lr are therefore added to fp32 sums (the accumulator in the workspace) and
+// begin again (16,384 tokens: 2^-11 at the most).
 // Rows of a tile behind the request's last token are set to 0 in shared memory before they meet P = 0 (0
 // times what they hold need not be 0).  With draft tokens the last L - 1 tokens are not seen by every query
 // token: of their values those that are not finite are set to 0 likewise, and where there were any, the
@@ -57,6 +61,7 @@ namespace {
 
 constexpr int T = 64;  // tokens a tile
 constexpr int kItemUnits = 3;  // see the share below; 2, 3 and 4 measure alike
+constexpr int kSumTiles = 256;  // tiles that the accumulator takes before it is set aside, a power of two
 constexpr int kThreads = 256;
 constexpr int kSoftThreads = 128;
 constexpr uint32_t kWaitLimit = 1u << 22;
@@ -76,7 +81,7 @@ template <int DL_, int N_> struct Cfg {
     static constexpr int RING = RING_FIT < 3 * PAIRS ? RING_FIT : 3 * PAIRS;  // pairs in flight
     static constexpr int OFF_P = Q_BYTES, OFF_ROPE = OFF_P + P_BYTES, OFF_RING = OFF_ROPE + ROPE * PB;
     static constexpr int SMEM = OFF_RING + RING * 2 * PB + 1024;
-    static_assert(RING >= PAIRS && SMEM <= 231424, "a tile fits the ring, the ring fits shared memory");
+    static_assert(RING >= PAIRS && SMEM <= 230400, "a tile fits the ring, the ring fits shared memory");
 };
 
 struct Params {
@@ -85,7 +90,7 @@ struct Params {
     float scale_log2;
     int32_t *status, *item0, *item1;  // [grid]: item whose part is in slot 0 / 1 of the CTA, or -1
     float4 *ml;                       // [grid][2][N]: m, l, l of the rounded probabilities
-    float *part;                      // [grid][2][N][dl]
+    float *part;                      // [grid][2][N][dl]; also what a segment sets aside, in its slot
 };
 
 struct Maps {
@@ -110,6 +115,8 @@ __device__ __forceinline__ int32_t tiles_of(int32_t n) { return n > T ? (n - 1) 
 
 // A row that saw nothing has the sum 0: output 0, log-sum-exp -inf.  A NaN stays one.
 __device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+// What a sum relative to the maximum `from` is worth relative to `to`.
+__device__ __forceinline__ float rebase(float from, float to) { return from == to ? 1.f : ex2_approx(from - to); }
 __device__ __forceinline__ float log_sum(float m, float sum) { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2; }
 
 struct Edge {
@@ -183,6 +190,58 @@ template <class C> struct Bars {
     uint64_t q_full, q_free, s[2], s_free[2], p, o, drain[2];
 };
 
+// The accumulator and a thread's l (x, y of `l`: rows g and g + 8) and lr (z, w) join what its segment set aside (`begun`:
+// something was) or, at the segment's end, come back with it as the whole (`back`).  By the softmax warps; sums [N][DL]:
+// this thread's dimension; kept [3][N]: the maximum that the sums are relative to, l and lr of what was set aside;
+// worth [N]: free to be written.  Returns the new l, lr.  Not inlined: it is rarely called, and its code between the
+// kernel's own cost a call of one request 0.5 us of 13.8.
+template <int DL, int N>
+__device__ __noinline__ float4 set_aside(uint32_t tl, float *sums, float (*kept)[N], float *worth, int row, float2 m, float4 l,
+                                         bool begun, bool back)
+{
+    const bool first = (threadIdx.x & 3) == 0;  // of the four threads of a row
+    if (row < N) {
+        float x[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[e] += __shfl_xor_sync(0xffffffffu, x[e], 1);
+            x[e] += __shfl_xor_sync(0xffffffffu, x[e], 2);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = row + 8 * e;
+            const float now = e ? m.y : m.x;
+            if (first) {
+                const float f = begun ? rebase(kept[0][r], now) : 0.f;
+                if (begun) x[e] = fmaf(kept[1][r], f, x[e]), x[2 + e] = fmaf(kept[2][r], f, x[2 + e]);
+                worth[r] = f;
+                kept[0][r] = now, kept[1][r] = x[e], kept[2][r] = x[2 + e];
+            }
+        }
+        l = first && back ? make_float4(x[0], x[1], x[2], x[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    soft_any(false);  // worth is complete
+#pragma unroll 1
+    for (int c0 = 0; c0 < DL / 128 * N; c0 += 16) {
+        uint32_t o[16];
+        tc::ld16(tl + c0, o);
+        tc::wait_ld();
+        float *x = sums + static_cast<int64_t>(c0 % N) * DL + c0 / N * 128;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (begun) o[e] = __float_as_uint(fmaf(x[e * DL], worth[c0 % N + e], __uint_as_float(o[e])));
+        if (back) {
+            tc::st16(tl + c0, o);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e * DL] = __uint_as_float(o[e]);
+        }
+    }
+    tc::wait_st();
+    tc::fence_before_sync();
+    return l;
+}
+
 template <int DL, int N>
 __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, const __grid_constant__ Maps maps)
 {
@@ -193,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
     __shared__ uint32_t tmem_base;
     __shared__ int32_t not_finite;          // segments (from 1) of the last value that was taken out
     __shared__ float corr[2][N], linv[N];  // corr: by parity of the tile, so that a late reader keeps its own
+    __shared__ float kept[3][N];           // set aside: maximum that it is relative to, l, lr
     __shared__ int64_t sums[kThreads / 32];
     __shared__ Edge edge[2];
     const int tid = threadIdx.x, lane = tid & 31;
@@ -408,9 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                        val_desc = tc::sdesc_sw128(base + C::OFF_RING, C::PB, 1024);
         int slot = 0;
         uint32_t passes = 0;
+        int32_t tile0 = w.tile;  // the segment's first
         bool ok = true;
         for (int32_t i = 0; i < total && ok; ++i) {
-            const uint32_t more = __all_sync(0xffffffffu, i == 0 || w.first()) ? 0u : 1u;
+            if (w.first()) tile0 = 0;
+            const uint32_t more = __all_sync(0xffffffffu, ((w.tile - tile0) & (kSumTiles - 1)) == 0) ? 0u : 1u;
             const bool two = __all_sync(0xffffffffu, w.tiles == 1) != 0;
             for (int pass = two ? 0 : 1; pass < 2; ++pass, ++passes) {
                 if (!(ok = __all_sync(0xffffffffu, wait(&bar.p, passes & 1)) != 0)) break;
@@ -446,6 +508,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
         int slot_out = 0;
         int32_t segments = 0, tile0 = 0;  // tile0: the segment's first
         uint32_t passes = 0;  // of the second product, so far
+        // worth: the half of corr that the tile does not use
+        auto aside = [&](float *worth, bool begun, bool back) {
+            wait(&bar.o, (passes - 1) & 1);
+            tc::fence_after_sync();
+            float *sums = p.part + (static_cast<int64_t>(2) * cta + slot_out) * N * DL + 32 * quad + lane;
+            const float4 x = set_aside<DL, N>(tl, sums, kept, worth, 16 * quad + g, make_float2(m[0], m[1]),
+                                              make_float4(l[0], l[1], lr[0], lr[1]), begun, back);
+            l[0] = x.x, l[1] = x.y, lr[0] = x.z, lr[1] = x.w;
+        };
         // a thread that gave up goes on without waiting: all of them meet at every barrier
         for (int32_t i = 0; i < total; ++i) {
             const bool fresh = i == 0 || w.first();
@@ -460,6 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                     l[e] = lr[e] = 0.f;
                     seen[e] = row < p.rows ? w.n - (p.a.L - 1 - row / p.a.h) : 0;
                 }
+            } else if (((w.tile - tile0) & (kSumTiles - 1)) == 0) {
+                aside(corr[(i & 1) ^ 1], w.tile - tile0 > kSumTiles, false);  // this tile's product does not add to it
             }
             wait(&bar.s[i & 1], (i >> 1) & 1);
             tc::fence_after_sync();
@@ -600,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
             if (last || i + 1 == total) {  // the segment ends here
                 const bool whole = last && slot_out == 1;
                 const int64_t part = 2 * cta + slot_out;
+                if (w.tile - tile0 >= kSumTiles) aside(corr[(i & 1) ^ 1], true, true);
                 if (active) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {

@@ -41,6 +41,10 @@
 // sum of the rounded weights, the log-sum-exp taken from the sum before rounding.  A query tile that
 // sees a single key tile has few weights to average the rounding over, so there what the rounding
 // left off goes through a second product (the other half of S_s holds it).
+// The tensor cores cut every product off at 2^-25 of the sum that it joins (the bits of a 26-bit window), so a sum of N
+// may lack N 2^-25 of its size: 1.3 % after a million keys behind one that holds half of the weight.  After kSumTiles
+// key tiles O, l and lr are therefore added to fp32 sums in the workspace and begin again (16,384 keys: 2^-11 at the
+// most).
 // A key that a query must not see enters its product with weight 0, and 0 times an infinity or NaN is not 0.
 // So in the tiles that not every query of the block sees whole, values that are not finite are taken out
 // (set to 0 in shared memory) before the product, and where there were any, the epilogue adds them to the
@@ -78,6 +82,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kStatusExpired = 7;
 constexpr int kBuckets = 1024;
 constexpr int kCutTiles = 10;
+constexpr int kSumTiles = 128;             // key tiles that O takes before it is set aside, a power of two
 constexpr int kTurnRounds = 8, kInTurn = -1;
 constexpr int kMostCtas = 256;             // of the grid (one per SM)
 constexpr int kFewBlocks = 32;             // up to these every CTA makes its own list
@@ -101,7 +106,8 @@ struct Params {
     int32_t grid;
     int32_t *item0, *item1;      // [grid] pair whose part is in slot 0 / 1 of the CTA, or -1
     float4 *ml;                  // [grid][2][256] m, l, l of the rounded weights
-    float *part;                 // [grid][2][256][DV]
+    float *part;                 // [grid][2][256][DV]; also what a pair sets aside: in its slot, a whole pair's in slot 1
+    float4 *kept;                // [grid][512] by softmax thread: the maximum that it is relative to; l, lr set aside
 };
 
 struct Maps {
@@ -305,6 +311,8 @@ struct Walk {
 
 // A row that saw nothing has the sum 0: output 0, log-sum-exp -inf.  A NaN stays one.
 __device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+// What a sum relative to the maximum `from` is worth relative to `to`.
+__device__ __forceinline__ float rebase(float from, float to) { return from == to ? 1.f : ex2_approx(from - to); }
 __device__ __forceinline__ float log_sum(float m, float sum) { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2; }
 
 __device__ __forceinline__ bool elect_one()
@@ -744,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 }
                 for (int j = 0; j < n; ++j, ++g) {
                     if (j < nt) {
-                        if (!(ok = second(g, j == 0, single, j + 1 < nt, j + 2 == nt))) break;
+                        if (!(ok = second(g, (j & (kSumTiles - 1)) == 0, single, j + 1 < nt, j + 2 == nt))) break;
                     } else {  // the other query tile's alone: handed back once it is there (then the tile two before is)
                         if (!(ok = all_wait(&bar.k_full[g & 1][0], g >> 1 & 1))) break;
                         if (lane == 0) mbar_arrive(&bar.k_free[g & 1]);
@@ -807,7 +815,42 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             const int32_t nt = seg->tiles[s], limit = row < seg->rows[s] ? seg->see + s * T + row - seg->j0 * T : INT32_MAX / 2;  // keys seen; no query: no mask to pay for
             const bool single = (seg->single >> s & 1) != 0;
             float m = -INFINITY, l = 0.f, lr = 0.f;  // l, lr: of this thread's keys
+            // O, l and lr join what was set aside (`begun`: something was), and come back as the whole (`back`)
+            auto set_aside = [&](bool begun, bool back) {
+                wait(&bar.o[s], (steps - 1) & 1);
+                tc::fence_after_sync();
+                float4 *const kept = p.kept + static_cast<int64_t>(blockIdx.x) * (4 * T) + (tid - T);
+                float4 k = make_float4(m, 0.f, 0.f, 0.f);
+                if (begun) k = *kept;
+                const float f = rebase(k.x, m);
+                l = fmaf(k.y, f, l), lr = fmaf(k.z, f, lr);
+                if (!back) {
+                    *kept = make_float4(m, l, lr, 0.f);
+                    l = lr = 0.f;
+                }
+                const int64_t sums_row = (2 * static_cast<int64_t>(blockIdx.x) + (seg->slot != 0 ? 1 : 0)) * kBlock + s * T + row;
+                float4 *sums = reinterpret_cast<float4 *>(p.part + sums_row * DV + kHalf * half);  // of this thread's columns
+#pragma unroll 1
+                for (int c = 0; c < kHalf; c += 16, sums += 4) {
+                    uint32_t o[16];
+                    tc::ld16(to + c, o);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (begun) x = sums[q];
+                        x = make_float4(fmaf(x.x, f, __uint_as_float(o[4 * q])), fmaf(x.y, f, __uint_as_float(o[4 * q + 1])),
+                                        fmaf(x.z, f, __uint_as_float(o[4 * q + 2])), fmaf(x.w, f, __uint_as_float(o[4 * q + 3])));
+                        if (!back) sums[q] = x;
+                        o[4 * q] = __float_as_uint(x.x), o[4 * q + 1] = __float_as_uint(x.y);
+                        o[4 * q + 2] = __float_as_uint(x.z), o[4 * q + 3] = __float_as_uint(x.w);
+                    }
+                    if (back) tc::st16(to + c, o);
+                }
+                tc::wait_st();
+            };
             for (int32_t j = 0; j < nt; ++j, ++steps) {
+                if (j > 0 && (j & (kSumTiles - 1)) == 0) set_aside(j > kSumTiles, false);  // the next product does not add to O
                 wait(&bar.s[s], steps & 1);
                 tc::fence_after_sync();
                 float z[kHalf];
@@ -924,6 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 l += sum.x + sum.y;
                 lr += sum_r.x + sum_r.y;
             }
+            if (nt > kSumTiles) set_aside(true, true);
             pair_sync();  // the maxima have been read
             sh.pair[s][half][row] = l;
             pair_sync();
@@ -1088,12 +1132,14 @@ bool encode(CUtensorMap *m, const void *base, int64_t cols, int64_t heads, int64
 namespace {
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// [status and counts | blocks | offsets | who holds parts | their statistics | parts]; returns the size.
+// [status and counts | blocks | offsets | who holds parts | their statistics | parts | maxima and sums set aside]; returns
+// the size.
 size_t layout(char *ws, int64_t total_q, int64_t num_seqs, Params *p)
 {
     const size_t n = static_cast<size_t>(blocks_bound(total_q, num_seqs)), grid = static_cast<size_t>(sm_count() < kMostCtas ? sm_count() : kMostCtas);
     const size_t before = 256, table = before + (n + 1) * 8, seq = table + n * 8, items = up256(seq + (num_seqs + 1) * 8);
-    const size_t ml = up256(items + 8 * grid), part = ml + 2 * grid * kBlock * 16, end = part + 2 * grid * kBlock * DV * 4;
+    const size_t ml = up256(items + 8 * grid), part = ml + 2 * grid * kBlock * 16, kept = part + 2 * grid * kBlock * DV * 4;
+    const size_t end = kept + grid * 4 * T * 16;
     if (p != nullptr) {
         p->max_blocks = static_cast<int64_t>(n);
         p->grid = static_cast<int32_t>(grid);
@@ -1109,6 +1155,7 @@ size_t layout(char *ws, int64_t total_q, int64_t num_seqs, Params *p)
         p->item1 = p->item0 + grid;
         p->ml = reinterpret_cast<float4 *>(ws + ml);
         p->part = reinterpret_cast<float *>(ws + part);
+        p->kept = reinterpret_cast<float4 *>(ws + kept);
     }
     return end;
 }
