@@ -171,10 +171,10 @@ __device__ __forceinline__ uint64_t global_ns()
 }
 
 // Wait until the barrier's phase `parity` has completed.  Bounded: gives up
-// after `limit` polls or about one second (the global timer, read every 256
+// after `limit` polls or about `seconds` (the global timer, read every 256
 // polls), whichever comes first, and returns false (the caller records the
 // failure).
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32_t limit)
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32_t limit, uint32_t seconds = 1)
 {
     const uint32_t a = smem_u32(bar);
     uint64_t t0 = 0;
@@ -191,7 +191,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32
         if ((i & 255u) == 255u) {
             const uint64_t t = global_ns();
             if (t0 == 0) t0 = t;
-            else if (t - t0 > 1000000000ull) return false;
+            else if (t - t0 > 1000000000ull * seconds) return false;
         }
     }
     return false;

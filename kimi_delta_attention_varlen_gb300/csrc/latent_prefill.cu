@@ -49,7 +49,9 @@
 // So in the tiles that not every query of the block sees whole, values that are not finite are taken out
 // (set to 0 in shared memory) before the product, and where there were any, the epilogue adds them to the
 // queries that do see them.  Value rows behind the sequence's end are set to 0 likewise.
-// Every wait is bounded; an expired one sets the workspace's status word (7).
+// Every wait is bounded; an expired one sets the workspace's status word (7).  A warp may wait for as long as a pair
+// takes: the scheduling warp for the one before the next to be read by all, a query tile without keys for the other
+// one's.  So the bound grows with the keys, a second for every 65,536 key tiles (they take 0.12 s).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -76,7 +78,8 @@ constexpr int kThreads = 640;              // four service warps, two softmax wa
 constexpr int kServiceRegs = 64, kSoftRegs = 104;  // 128 x 64 + 512 x 104 = 61,440 = 640 x 96 registers
 constexpr int kHalf = T / 2;               // keys of a softmax thread
 constexpr uint32_t kColO = 256;            // S_s at 128 s, O_s at 256 + 128 s
-constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr uint32_t kWaitLimit = 0xffffffffu;  // polls: the time bounds the waits
+constexpr int kTilesPerSecond = 1 << 16;
 constexpr float kLazy = 8.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kStatusExpired = 7;
@@ -104,6 +107,7 @@ struct Params {
     int32_t *seq_off, *short_off;  // [num_seqs + 1] blocks before each sequence; of them those in the first quarter of theirs
     int64_t max_blocks;
     int32_t grid;
+    uint32_t seconds;            // that a wait may take
     int32_t *item0, *item1;      // [grid] pair whose part is in slot 0 / 1 of the CTA, or -1
     float4 *ml;                  // [grid][2][256] m, l, l of the rounded weights
     float *part;                 // [grid][2][256][DV]; also what a pair sets aside: in its slot, a whole pair's in slot 1
@@ -567,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
 
     bool gave_up = false;
     auto wait = [&](uint64_t *b, uint32_t parity) {
-        if (!gave_up && !mbar_wait(b, parity, kWaitLimit)) {
+        if (!gave_up && !mbar_wait(b, parity, kWaitLimit, p.seconds)) {
             gave_up = true;
             atomicExch(p.status, kStatusExpired);
         }
@@ -1168,6 +1172,7 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t st)
     Params p{};
     p.a = a;
     p.scale_log2 = a.scale * kLog2e;
+    p.seconds = 1 + static_cast<uint32_t>(a.total_k / (static_cast<int64_t>(kTilesPerSecond) * T));
     layout(static_cast<char *>(a.workspace), a.total_q, a.num_seqs, &p);
     Maps maps{};
     int32_t plain;  // q's heads lie within a token (or there is one), k_rope has one

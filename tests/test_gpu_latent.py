@@ -495,3 +495,19 @@ def test_prefill_sums_set_aside_as_the_maximum_grows():
     want = (p[:, None] * x[:, :128].double()).sum(0)
     assert ((out[-1].double() - want).abs() / want).max() <= OUT_REL + 2 * Z_REL * 40
     assert (lse[-1].double() - torch.logsumexp(z, 0)).abs().max() <= LSE_ABS + Z_REL * 41
+
+
+def test_prefill_pairs_that_take_longer_than_a_second():
+    """Three sequences of one query, the first on 200 million keys, with a head a CTA: while its pair runs, the warps that
+    are done with it wait to be handed the third one."""
+    H = torch.cuda.get_device_properties(0).multi_processor_count
+    n = 200_000_000
+    ones = torch.ones(n + 2, 128, dtype=BF, device=DEV)  # keys and values in one, shared by all heads
+    k = ones[:, None].expand(-1, H, -1)
+    q = torch.randn(3, H, 192, generator=wl.generator(3, DEV), device=DEV).to(BF)
+    out, lse = run_prefill(q, k, ones[:, :64], k, [0, 1, 2, 3], [0, n, n + 1, n + 2], scale=1.0)
+    assert (out == 1).all()  # ones, whatever their weights
+    want = q.double().sum(-1) + torch.tensor([math.log(n), 0, 0], device=DEV)[:, None]
+    # a score: 192 products with 1, each addition within 2^-23 of the magnitudes added (12 partial sums of 16); the weights
+    # are 1 and their sums, in steps of 64, exact up to 2^30
+    assert ((lse.double() - want).abs() <= 12 * 2.0 ** -23 * q.double().abs().sum(-1) + 1e-5).all()
