@@ -574,8 +574,12 @@ typedef struct {
  * index of kda_state_gather.  Cache rows beyond a request's length are never
  * used, whatever they hold (NaN and infinities included), and a value that is
  * not finite reaches only the query tokens that see it.  Scores, softmax
- * statistics and sums are fp32; the probabilities enter the second product
- * in bf16 (the tensor cores' operand type).
+ * statistics and sums are fp32.  The probabilities enter the second product
+ * in bf16 (the tensor cores' operand type), normalised by the sum of what
+ * they were rounded to: beside its own rounding an output is off by 2^-7
+ * sum_j p_j |x_j| at most, where a few of many tokens hold nearly all the
+ * weight, and by far less where the roundings average out.  Query tokens that
+ * see at most 64 tokens take what the rounding leaves off as well.
  * Built: dl in {256, 512}, dr == 64, page_size a multiple of 8, bf16.
  * Errors: KDA_ERR_NULL, _DTYPE (io or cache not bf16), _LAYOUT, _SHAPE (sizes
  * below 1 (batch below 0), cache h / k not 1 / dl + dr, table_stride < width),
@@ -616,6 +620,8 @@ int kda_latent_decode(const void *q, int32_t io_dtype, int64_t batch, int32_t L,
  *            no query at or beyond total_q is touched whatever they hold)
  *   out      [total_q, h, dv] device bf16, lse [total_q, h] fp32 or NULL
  *            A value that is not finite reaches only the queries that see it.
+ *            Precision as above; queries that see at most 128 keys take what
+ *            the rounding of the probabilities leaves off as well.
  *   workspace kda_latent_prefill_workspace_size(...) bytes, as above
  * Built: dn == dv == 128, dr == 64, bf16.  Errors as kda_latent_decode
  * (_SHAPE: negative strides, a token stride of 0 with several tokens; _RANGE:

@@ -23,9 +23,11 @@
 //
 // The probabilities enter the second product in bf16, the only operand type the tensor cores take
 // beside bf16 values; the output is normalised by the sum of those rounded weights (they then sum
-// to one exactly), the log-sum-exp taken from the sum before rounding.  A request of a single tile
-// has few weights to average the rounding over, so there a second pass adds the product of what the
-// rounding left off (its own rounding is 2^-16 of the weight).
+// to one exactly), the log-sum-exp taken from the sum before rounding.  So each weight is off by 2^-8 at most, relative
+// to the others, and the output by 2^-7 sum p |x| beside its own rounding; that takes two or three weights that
+// outweigh all others and round to opposite sides, else the errors average out.  A query token that sees few tokens
+// has no more weights than that, so where one sees no second tile, a second pass adds the product of what the rounding
+// left off in the first one (its own rounding is 2^-16 of the weight).
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than 2^8 since the last
 // rescale (the exponents are relative to that older maximum, exact in fp32 and in bf16's range).
@@ -137,6 +139,8 @@ struct Walk {
     }
     __device__ bool first() const { return tile == 0; }
     __device__ bool last() const { return tile + 1 == tiles; }
+    // the first query token of the request sees this tile alone
+    __device__ bool twice(const Params &p) const { return tile == 0 && n - (p.a.L - 1) <= T; }
     __device__ void next(const Params &p)
     {
         if (++tile < tiles) return;
@@ -473,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
         for (int32_t i = 0; i < total && ok; ++i) {
             if (w.first()) tile0 = 0;
             const uint32_t more = __all_sync(0xffffffffu, ((w.tile - tile0) & (kSumTiles - 1)) == 0) ? 0u : 1u;
-            const bool two = __all_sync(0xffffffffu, w.tiles == 1) != 0;
+            const bool two = __all_sync(0xffffffffu, w.twice(p)) != 0;
             for (int pass = two ? 0 : 1; pass < 2; ++pass, ++passes) {
                 if (!(ok = __all_sync(0xffffffffu, wait(&bar.p, passes & 1)) != 0)) break;
                 tc::fence_after_sync();
@@ -649,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
             tc::fence_before_sync();
             mbar_arrive(&bar.p);
             ++passes;
-            if (w.tiles == 1) {  // the second pass: what the rounding left off
+            if (w.twice(p)) {  // the second pass: what the rounding left off
                 if (active) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {

@@ -38,9 +38,12 @@
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the last rescale.  The
 // probabilities are rounded to bf16, the tensor cores' operand type; the output is normalised by the
-// sum of the rounded weights, the log-sum-exp taken from the sum before rounding.  A query tile that
-// sees a single key tile has few weights to average the rounding over, so there what the rounding
-// left off goes through a second product (the other half of S_s holds it).
+// sum of the rounded weights, the log-sum-exp taken from the sum before rounding.  So each weight is off by 2^-8 at
+// most, relative to the others, and the output by 2^-7 sum p |v| beside its own rounding; that takes two or three
+// weights that outweigh all others and round to opposite sides, else the errors average out.  A query that sees few
+// keys has no more weights than that, so for those that see one key tile nothing is left off: in the first key tile of
+// a query tile whose first query sees no second one, what the rounding leaves off goes through a second product (the
+// other half of S_s holds it).
 // The tensor cores cut every product off at 2^-25 of the sum that it joins (the bits of a 26-bit window), so a sum of N
 // may lack N 2^-25 of its size: 1.3 % after a million keys behind one that holds half of the weight.  After kSumTiles
 // key tiles O, l and lr are therefore added to fp32 sums in the workspace and begin again (16,384 keys: 2^-11 at the
@@ -514,7 +517,7 @@ struct Segment {
     int32_t see;                // keys that the block's first query sees
     int32_t j0, j1;             // key tiles of the stretch
     int32_t slot, head, pair;   // slot: as in Walk; pair -1: no more work
-    int32_t single;             // bit s: query tile s sees one key tile in all
+    int32_t exact;              // bit s: the first key tile's weights go into query tile s with what their rounding leaves off
 };
 
 struct Shared {
@@ -697,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             // O += P V of key tile g and, behind it, S of key tile g + 1 (more).  A look at a barrier costs its time even
             // where the barrier is long open, and behind the product it would leave the tensor pipe idle: so the
             // key panels are looked at before the wait for P, and S follows at once where they are there.
-            auto second = [&](uint32_t g, bool fresh, bool single, bool more, bool free_q) {
+            auto second = [&](uint32_t g, bool fresh, bool exact, bool more, bool free_q) {
                 const uint64_t b0 = ring_desc + (5 * g + 3) % kRing * (PB >> 4), b1 = ring_desc + (5 * g + 4) % kRing * (PB >> 4);
                 if (!all_wait(&bar.v_full[g & 1], g >> 1 & 1)) return false;
                 const uint32_t n = g + 1, par = n >> 1 & 1;
@@ -725,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                         tc::mma_bf16_ts(to, ts + 8 * ks, b0 + 128 * ks, kIdO, 1u);
                         tc::mma_bf16_ts(to + 64, ts + 8 * ks, b1 + 128 * ks, kIdO, 1u);
                     }
-                    if (single) {  // what the rounding left off, too
+                    if (exact) {  // what the rounding left off, too
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks) {
                             tc::mma_bf16_ts(to, ts + 64 + 8 * ks, b0 + 128 * ks, kIdO, 1u);
@@ -747,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             bool ok = true;
             while (const Segment *seg = ok ? next_segment() : nullptr) {
                 const int nt = uniform(seg->tiles[s]), n = uniform(seg->j1 - seg->j0);
-                const bool single = (uniform(seg->single) >> s & 1) != 0;
+                const bool exact = (uniform(seg->exact) >> s & 1) != 0;
                 segment_done();
                 if (nt > 0) {
                     if (!(ok = all_wait(&bar.q_full[s], loads++ & 1))) break;
@@ -756,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 }
                 for (int j = 0; j < n; ++j, ++g) {
                     if (j < nt) {
-                        if (!(ok = second(g, (j & (kSumTiles - 1)) == 0, single, j + 1 < nt, j + 2 == nt))) break;
+                        if (!(ok = second(g, (j & (kSumTiles - 1)) == 0, exact && j == 0, j + 1 < nt, j + 2 == nt))) break;
                     } else {  // the other query tile's alone: handed back once it is there (then the tile two before is)
                         if (!(ok = all_wait(&bar.k_full[g & 1][0], g >> 1 & 1))) break;
                         if (lane == 0) mbar_arrive(&bar.k_free[g & 1]);
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                         g.q0 = w.it.q0, g.k0 = w.it.k0, g.nk = w.it.nk, g.see = w.it.see0;
                         g.rows[0] = w.it.rows0, g.rows[1] = w.it.rows1, g.tiles[0] = w.tiles(0), g.tiles[1] = w.tiles(1);
                         g.j0 = w.j0, g.j1 = w.j1, g.slot = w.slot, g.head = w.head, g.pair = w.pair;
-                        g.single = (w.it.tiles0 == 1 ? 1 : 0) | (w.it.tiles1 == 1 ? 2 : 0);
+                        g.exact = w.j0 > 0 ? 0 : (w.it.see(0) <= T ? 1 : 0) | (w.it.see(1) <= T ? 2 : 0);
                     }
                     mbar_arrive(&bar.seg_full[nseg & 1]);
                 }
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             if (pair_any(gave_up) || seg == nullptr) break;
             // a row's 64 scores fill the registers: what is not needed for each tile stays in the segment
             const int32_t nt = seg->tiles[s], limit = row < seg->rows[s] ? seg->see + s * T + row - seg->j0 * T : INT32_MAX / 2;  // keys seen; no query: no mask to pay for
-            const bool single = (seg->single >> s & 1) != 0;
+            const bool exact = (seg->exact >> s & 1) != 0;
             float m = -INFINITY, l = 0.f, lr = 0.f;  // l, lr: of this thread's keys
             // O, l and lr join what was set aside (`begun`: something was), and come back as the whole (`back`)
             auto set_aside = [&](bool begun, bool back) {
@@ -928,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                 }
                 // scores -> probabilities, rounded, into S_s
                 float2 sum = make_float2(0.f, 0.f), sum_r = make_float2(0.f, 0.f);
-                if (!single) {
+                if (!exact || j > 0) {
 #pragma unroll
                     for (int c = 0; c < kHalf / 2; c += 16) {
                         uint32_t pk[16];
@@ -946,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
                         tc::fence_before_sync();
                         mbar_arrive(&bar.p[s][c >> 4]);
                     }
-                } else {  // a single key tile: what the rounding leaves off goes into the other half of S_s
+                } else {  // what the rounding leaves off goes into the other half of S_s
 #pragma unroll
                     for (int c = 0; c < kHalf / 2; c += 16) {
                         uint32_t hi[16], low[16];

@@ -511,3 +511,23 @@ def test_prefill_pairs_that_take_longer_than_a_second():
     # a score: 192 products with 1, each addition within 2^-23 of the magnitudes added (12 partial sums of 16); the weights
     # are 1 and their sums, in steps of 64, exact up to 2^30
     assert ((lse.double() - want).abs() <= 12 * 2.0 ** -23 * q.double().abs().sum(-1) + 1e-5).all()
+
+
+# -------------------------------------------- few keys in a tile of many --
+# Two to four weights do not average their rounding to bf16 away: rows that see few keys take what it leaves off, also
+# where other rows of their tile see more than one key tile.
+
+@pytest.mark.parametrize("nq", [128, 256, 300])
+def test_prefill_rows_of_few_keys_before_rows_of_many(nq):
+    prefixes = [1, 2, 3, 4, 20, 64]
+    check_prefill([nq] * len(prefixes), [nq + n for n in prefixes], 64, seed=nq)
+
+
+@pytest.mark.parametrize("dl", [256, 512])
+@pytest.mark.parametrize("L", [65, 70, 90])
+def test_decode_draft_tokens_that_see_few_tokens(L, dl):
+    lens = [L, L + 1, L + 2, L + 3, L + 30, L + 62, L + 63, L + 64]
+    cache, table, sl, rows = paged_latents(lens, 16, dl, seed=L)
+    q = queries(len(lens), L, 32, dl + 64, seed=L)
+    out, lse = run_decode(q, cache, table, sl, dl, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, dl), f"L {L}")
