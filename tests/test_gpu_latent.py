@@ -531,3 +531,108 @@ def test_decode_draft_tokens_that_see_few_tokens(L, dl):
     q = queries(len(lens), L, 32, dl + 64, seed=L)
     out, lse = run_decode(q, cache, table, sl, dl, SCALE)
     assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, dl), f"L {L}")
+
+
+# ------------------------------------------------------- schedules, widths --
+
+@pytest.mark.parametrize("nq,nk,heads", [([777, 435, 600, 512, 700], [9000, 5000, 8000, 7111, 6500], 16),
+                                         ([200 - 3 * (i % 4) for i in range(36)], [5000 - 37 * i for i in range(36)], 6)])
+def test_prefill_last_round_cut_behind_whole_rounds(nq, nk, heads):
+    # more pairs than CTAs, fewer than eight a CTA, and long ones in the last round: each CTA takes whole pairs, then a
+    # stretch of the rest that makes up for their length; lists of at most 32 blocks, and of more
+    check_prefill(nq, nk, heads, seed=heads)
+
+
+@pytest.mark.parametrize("nq,nk", [([1024, 0, 1100, 2049, 1500, 3, 1300, 1800, 1, 769], None),
+                                   ([1025, 768, 1536, 1, 2500, 900, 1700, 1300], [1400, 768, 2000, 700, 2500, 1000, 1650, 1300])])
+def test_prefill_pairs_in_turn_with_short_blocks_last(nq, nk):
+    # at least eight pairs a CTA, and sequences long enough that the first quarter of their blocks comes in a second pass
+    heads = 32
+    nk = nk or nq
+    assert sum(-(-n // 256) for n in nq) * heads >= 8 * torch.cuda.get_device_properties(0).multi_processor_count
+    check_prefill(nq, nk, heads, seed=len(nq))
+
+
+@pytest.mark.parametrize("heads", [1, 5, 16, 17, 48, 64, 65, 128])
+def test_decode_heads_on_latents_of_256(heads):
+    lens = [1, 70, 333, 0, 2000]
+    cache, table, sl, rows = paged_latents(lens, 32, 256, seed=heads, gap=40)
+    q = queries(len(lens), 1, heads, 320, seed=heads)
+    out, lse = run_decode(q, cache, table, sl, 256, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, 256), f"heads {heads}")
+
+
+@pytest.mark.parametrize("L,heads", [(2, 32), (3, 16), (4, 128), (5, 8), (7, 1), (70, 2)])
+def test_decode_draft_tokens_on_latents_of_256(L, heads):
+    lens = [0, 1, L - 1, L, L + 1, 64 + L, 129, 700]
+    cache, table, sl, rows = paged_latents(lens, 16, 256, seed=L, width_extra=3)
+    q = queries(len(lens), L, heads, 320, seed=L)
+    out, lse = run_decode(q, cache, table, sl, 256, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, 256), f"L {L} heads {heads}")
+
+
+@pytest.mark.parametrize("lens,heads", [([40000], 32), ([9999, 3, 25000], 16), ([6400] * 5, 64), ([20000, 1], 128)])
+def test_decode_long_contexts_on_latents_of_256(lens, heads):
+    cache, table, sl, rows = paged_latents(lens, 64, 256, seed=heads)
+    q = queries(len(lens), 1, heads, 320, seed=heads)
+    out, lse = run_decode(q, cache, table, sl, 256, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, 256), "long")
+    again, lse2 = run_decode(q, cache, table, sl, 256, SCALE)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("n,L,heads", [(40, 3, 8), (130, 5, 8), (66, 4, 16), (20000, 6, 32), (64, 70, 1), (300, 4, 64)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_decode_values_that_are_not_finite_in_latents_of_256(n, L, heads, bad):
+    cache, table, sl, rows = paged_latents([n], 16, 256, seed=n + L)
+    q = queries(1, L, heads, 320, seed=L)
+    tok, dims = n - 2, [9, 130, 255]
+    q[..., dims] = 0
+    ref = decode_reference(q, lambda r, k: rows[r][:k], [n], SCALE, 256)
+    cache[table[0, tok // 16].long(), 0, tok % 16, dims] = bad
+    out, lse = run_decode(q, cache, table, sl, 256, SCALE)
+    assert torch.isnan(out[0, L - 2:]).all() and torch.isnan(lse[0, L - 2:]).all()
+    assert_attention(out[:, :L - 2], lse[:, :L - 2], [x[:, :L - 2] for x in ref], f"n {n} L {L}")
+
+
+def test_calls_in_a_row_on_one_workspace():
+    """Appends, decode steps of other sizes and prompts queued without a wait: each kernel may come while the one before
+    it runs out, and they share their workspaces."""
+    g = wl.generator(31, DEV)
+    page, N, R = 16, 600, 5
+    bt, sl, ref = torch.full((R, 100), -1, dtype=torch.int32, device=DEV), torch.zeros(R, dtype=torch.int32, device=DEV), torch.zeros(N, dtype=torch.int32, device=DEV)
+    pt = kda.page_table_descriptor(bt, sl, ref, page)
+    cache = poisoned(N, 1, page, 576)
+    ids = torch.arange(R, dtype=torch.int32, device=DEV)
+    ms, md, info = (torch.empty(n, dtype=torch.int32, device=DEV) for n in (R, R, 4))
+    pws = torch.empty(kda.kda_pages_workspace_size(N, R), dtype=torch.uint8, device=DEV)
+    steps = [[1000, 3, 0, 64, 129], [1, 1, 1, 1, 1], [200, 61, 5, 3, 0], [1, 1, 1, 1, 1], [1, 2, 3, 4, 5]]
+    forms = [(1, 32), (2, 8), (1, 128), (1, 16), (4, 64)]  # query tokens, heads
+    dws = torch.empty(max(kda.kda_latent_decode_workspace_size(R, L, H, 512, 64) for L, H in forms), dtype=torch.uint8, device=DEV)
+    prompts = [([300, 5], [300, 900], 4), ([1500], [1500], 1), ([60] * 40, [60] * 40, 3), ([1], [3000], 8), ([64, 200], [64, 200], 2)]
+    batches = [prompt_batch(nq, nk, H, seed=i) for i, (nq, nk, H) in enumerate(prompts)]
+    fws = torch.empty(max(kda.kda_latent_prefill_workspace_size(sum(nq), len(nq), H) for nq, _, H in prompts), dtype=torch.uint8, device=DEV)
+    work = []
+    for new, (L, H), (q, kn, kr, v, cu_q, cu_k) in zip(steps, forms, batches):
+        work.append(dict(new=torch.tensor(new, dtype=torch.int32, device=DEV), cu=torch.tensor([0] + new, device=DEV).cumsum(0).int(),
+                         rows=torch.randn(sum(new), 576, generator=g, device=DEV).to(BF), q=torch.randn(R, L, H, 576, generator=g, device=DEV).to(BF),
+                         out=poisoned(R, L, H, 512), lse=torch.full((R, L, H), math.nan, device=DEV),
+                         cq=torch.tensor(cu_q, dtype=torch.int32, device=DEV), ck=torch.tensor(cu_k, dtype=torch.int32, device=DEV),
+                         po=poisoned(q.shape[0], q.shape[1], 128), pl=torch.full(q.shape[:2], math.nan, device=DEV)))
+    torch.cuda.synchronize()
+    for w, (q, kn, kr, v, _, _) in zip(work, batches):
+        kda.kda_pages_reserve(pt, ids, w["new"], ms, md, info, pws)
+        kda.kda_pages_copy(cache, ms, md)
+        kda.kda_latent_append(w["rows"], w["cu"], ids, pt, cache)
+        kda.kda_latent_decode(w["q"], cache, bt, sl, w["out"], dws, latent_dim=512, scale=SCALE, lse=w["lse"])
+        kda.kda_latent_prefill(q, kn, kr, v, w["cq"], w["ck"], w["po"], fws, scale=SCALE, lse=w["pl"])
+    torch.cuda.synchronize()
+    assert int(info[0]) == 0 and kda.kda_prefill_workspace_status(dws) == 0 and kda.kda_prefill_workspace_status(fws) == 0
+    held = [torch.empty(0, 576, dtype=BF, device=DEV) for _ in range(R)]
+    for i, (w, new, (q, kn, kr, v, cu_q, cu_k)) in enumerate(zip(work, steps, batches)):
+        at = 0
+        for r, n in enumerate(new):
+            held[r] = torch.cat([held[r], w["rows"][at:at + n]])
+            at += n
+        assert_attention(w["out"], w["lse"], decode_reference(w["q"], lambda r, n: held[r][:n], [h.shape[0] for h in held], SCALE, 512), f"step {i}")
+        assert_attention(w["po"], w["pl"], prefill_reference(q, kn, kr, v, cu_q, cu_k, SCALE), f"prompts {i}")
