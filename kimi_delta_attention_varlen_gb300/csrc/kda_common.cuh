@@ -70,6 +70,14 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return d;
 }
 
+// a b + c in both bf16 halves.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
 // Halfwords of u that are a bf16 infinity or NaN, as 0xffff each.
 __device__ __forceinline__ uint32_t bf16x2_not_finite(uint32_t u) { return __vcmpeq2(u & 0x7f807f80u, 0x7f807f80u); }
 
