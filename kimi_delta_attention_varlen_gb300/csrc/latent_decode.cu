@@ -41,11 +41,12 @@
 // epilogue adds them to the rows that do see them.
 //
 // What bounds it: with one token a request the cache's bytes (512 requests of 512..8192 tokens, 32 heads, dl = 512:
-// 420..440 us = 5.9..6.2 TB/s), a few short requests the latency of two launches, the first tile and the join (one of
-// 1009 tokens: 14 us), with four draft tokens and 128 heads the ring: 64 query rows leave room for two tiles, each of which
-// holds its slots for 7,000 cycles from copy to second product, 1,920 of them MMAs (33 requests of 1500..6001 tokens: 224 us
-// = 627 TFLOP/s; with P handed over in two parts 234 us, since the slots then come back later).  64-token tiles because of the same ring: 512 requests took 617 us with 96 and 572 with 128 where they
-// took 439 with 64.  Four copying warps instead of two: 425 / 420 us, drafts alike.
+// 419..443 us = 5.9..6.2 TB/s), a few short requests the latency of two launches, the first tile and the join (one of
+// 1009 tokens: 14 us), with four draft tokens and 128 heads the ring: 64 query rows leave room for two tiles, each of
+// which holds its slots for 7,000 cycles from copy to second product, 1,920 of them MMAs (33 requests of 1500..6001
+// tokens: 218..233 us = 600..640 TFLOP/s; with P handed over in two parts 10 us more, since the slots then come back
+// later).  64-token tiles because of the same ring: 512 requests took 617 us with 96 and 572 with 128 where they took
+// 439 with 64.  Four copying warps instead of two: 425 / 420 us, drafts alike.
 //
 // Every wait is bounded; an expired one sets the workspace's status word (6) and ends the CTA.
 #include <cuda.h>
@@ -78,7 +79,7 @@ template <int DL_, int N_> struct Cfg {
     static constexpr int PB = T * 128;                                    // bytes of a panel
     static constexpr int ROPE = N == 64 ? 2 : 3;                          // rope panels in flight
     static constexpr int Q_BYTES = PANELS * N * 128, P_BYTES = N * 128;
-    // 230,400 bytes: 227 KB less the alignment slack and the barriers
+    // 230,400 bytes: 227 KB less what the kernel declares itself (2 KB at the most)
     static constexpr int RING_FIT = (230400 - Q_BYTES - P_BYTES - ROPE * PB) / (2 * PB);
     static constexpr int RING = RING_FIT < 3 * PAIRS ? RING_FIT : 3 * PAIRS;  // pairs in flight
     static constexpr int OFF_P = Q_BYTES, OFF_ROPE = OFF_P + P_BYTES, OFF_RING = OFF_ROPE + ROPE * PB;

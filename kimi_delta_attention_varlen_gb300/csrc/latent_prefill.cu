@@ -11,17 +11,18 @@
 //     so that blocks of one sequence and head run side by side and their keys and values come from the
 //     L2 cache (a block reads 80 KB a key tile for 21 MFLOP: at the tensor cores' rate that is the HBM's);
 //     the first quarter of each sequence's blocks, the short ones, come last and even out the end.
-//     In turn / longest first: 16 prompts of 512..8192 tokens, 32 heads (68 pairs a CTA) 3.55 / 4.11 ms; two of
-//     8192, 32 heads (13 pairs) 0.98 / 1.03 ms; twelve of 300..3000 on 2000, 16 heads (9 pairs) 529 / 551 us;
-//     four of 2000, 32 heads (7 pairs) 192 / 183 us; one of 4096, 32 heads (3 pairs) 187 / 135 us.
+//     In turn / longest first: 16 prompts of 512..8192 tokens, 32 heads (68 pairs a CTA) 3.47 / 4.05 ms; two of
+//     8192, 32 heads (13 pairs) 0.98 / 1.02 ms; four of 4096, 32 heads (13 pairs) 549 / 571 us; twelve of 300..3000
+//     on 2000, 16 heads (9 pairs) 496 / 535 us; four of 2000, 32 heads (7 pairs) 193 / 186 us; one of 4096, 32 heads
+//     (3 pairs) 195 / 142 us.
 //   Fewer: whole rounds of one pair a CTA, longest first and in turn from either end; of the last, partial
 //     round all key tiles lie on one line, of which each CTA takes the stretch that fills its sum of key tiles up
 //     to a level common to all.  A pair that falls into several stretches leaves unnormalised parts in the
 //     workspace, which join_kernel puts together in order of their keys.  Parts cost about what kCutTiles key
 //     tiles do (queries loaded again, parts written and joined: 10 us), so the last round runs whole where its
 //     longest pair is not that much longer than an equal stretch.  Cut / whole: 1000 queries on 16000 keys, 4 heads
-//     59 / 212 us; 8192 queries, 2 heads 84 / 124 us; three of 578..777 on 7000..9000, 32 heads 285 / 332 us; four
-//     prompts of up to 2000, 8 heads 46 / 42 us, one of 4096, 32 heads 148 / 136 us (these run whole).
+//     57 / 203 us; 8192 queries, 2 heads 75 / 116 us; three of 578..777 on 7000..9000, 32 heads 285 / 317 us; four
+//     prompts of up to 2000, 8 heads 46 / 38 us, one of 4096, 32 heads 147 / 125 us (these run whole).
 // Which CTA takes a pair never changes what is computed, and where pairs are cut depends on the lengths alone.
 // A block is two query tiles s = 0, 1 of 128 rows that share the key and value tiles:
 //   S_s   = Q_s K^T     M = 128, N = 128, K = 192 (two nope panels and the shared rope panel)
@@ -34,7 +35,10 @@
 // key tile three key panels (K-major B), then two value panels (MN-major B).
 //
 // The probabilities of a tile are handed to the second product in two parts, so that it runs on the first while the
-// exponentials of the second are taken (16 prompts 3.80 -> 3.56 ms).
+// exponentials of the second are taken (16 prompts 3.80 -> 3.56 ms when it was brought in).
+//
+// The softmax warps' registers (104 after the split, 64 of them a row's scores) do not hold everything: 60 bytes a
+// thread are spilled and 84 loaded again.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the last rescale.  The
 // probabilities are rounded to bf16, the tensor cores' operand type; the output is normalised by the
@@ -450,8 +454,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(Params p)
 }
 
 // The same list of few blocks, by one warp of every CTA into its shared memory, a block a lane: a launch and its
-// latency less (three prompts of up to 100 tokens, 32 heads: 19.0 -> 12.6 us; five of 435..777 on prefixes of up to
-// 9000, 16 heads: 270 -> 262 us).
+// latency less (three prompts of up to 100 tokens, 32 heads: 17.9 -> 10.8 us; five of 201..777 on prefixes of up to
+// 9000, 16 heads: 232 -> 224 us).
 __device__ __forceinline__ List plan_few(const Params &p, int2 *table, int64_t *before, int32_t *units)
 {
     const LatentPrefillArgs &a = p.a;
@@ -548,7 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             sh.not_finite[s] = 0;
-            mbar_init(&bar.k_full[s][0], 1), mbar_init(&bar.k_full[s][1], 1), mbar_init(&bar.k_full[s][2], 1), mbar_init(&bar.k_free[s], 2), mbar_init(&bar.v_full[s], 1), mbar_init(&bar.v_free[s], 2);  // handed back by both query tiles
+            for (int u = 0; u < 3; ++u) mbar_init(&bar.k_full[s][u], 1);
+            mbar_init(&bar.v_full[s], 1);
+            mbar_init(&bar.k_free[s], 2), mbar_init(&bar.v_free[s], 2);  // handed back by both query tiles
             mbar_init(&bar.drain[s], 1), mbar_init(&bar.seg_full[s], 1), mbar_init(&bar.seg_free[s], kReaders);
             mbar_init(&bar.q_full[s], 1), mbar_init(&bar.q_free[s], 1), mbar_init(&bar.s[s], 1), mbar_init(&bar.o[s], 1);
             mbar_init(&bar.p[s][0], 2 * T), mbar_init(&bar.p[s][1], 2 * T);
@@ -819,7 +825,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(Params p, c
             const Segment *seg = next_segment();
             if (pair_any(gave_up) || seg == nullptr) break;
             // a row's 64 scores fill the registers: what is not needed for each tile stays in the segment
-            const int32_t nt = seg->tiles[s], limit = row < seg->rows[s] ? seg->see + s * T + row - seg->j0 * T : INT32_MAX / 2;  // keys seen; no query: no mask to pay for
+            const int32_t nt = seg->tiles[s];
+            // keys seen; no query: no mask to pay for
+            const int32_t limit = row < seg->rows[s] ? seg->see + s * T + row - seg->j0 * T : INT32_MAX / 2;
             const bool exact = (seg->exact >> s & 1) != 0;
             float m = -INFINITY, l = 0.f, lr = 0.f;  // l, lr: of this thread's keys
             // O, l and lr join what was set aside (`begun`: something was), and come back as the whole (`back`)
