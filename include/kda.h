@@ -12,8 +12,11 @@
  * and around them, each documented where it is declared: the cache-indexed
  * prefill, target verification, INT8 checkpoints, the short convolution, and
  * what the full-attention layers between the recurrent ones need: attention
- * over a paged latent cache (kda_latent_decode, kda_latent_prefill,
- * kda_latent_append) and the upkeep of its pages (kda_pages_*).
+ * over a paged latent cache (kda_latent_decode, kda_latent_decode_shared for
+ * requests that begin with the same tokens, kda_latent_prefill,
+ * kda_latent_append), the same cache in 8 bits (kda_latent_append8,
+ * kda_latent_read, kda_latent_decode8) and the upkeep of its pages
+ * (kda_pages_*).
  *
  * Conventions shared by every entry point
  *   - Every data pointer is a DEVICE pointer unless stated otherwise; the
@@ -67,7 +70,8 @@ typedef enum {
     KDA_ERR_ALIGN = -9        /* a pointer is not aligned to its element size     */
 } kda_status;
 
-typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
+/* KDA_U8: bytes, for 8-bit latent pages; only the calls that name them take it. */
+typedef enum { KDA_F32 = 0, KDA_BF16 = 1, KDA_U8 = 2 } kda_dtype;
 typedef enum { KDA_I32 = 0, KDA_I64 = 1 } kda_itype;
 
 /* A paged recurrent-state cache [n_rows, h, v, k] with a row stride.
@@ -657,6 +661,100 @@ int kda_latent_append(const void *x, int64_t x_stride, int64_t total, const int3
                       const kda_cache *cache, void *stream);
 
 /* ------------------------------------------------------------------------
+ * kda_latent_decode_shared
+ *
+ * kda_latent_decode for a batch whose entries come in groups that begin with
+ * the same tokens in the same pages (parallel samples of a prompt, a common
+ * system prompt): the attention to those tokens is computed once for all query
+ * rows of a group together, so their pages are read once and not once a
+ * request, and joined with each entry's own rest.
+ *   cu_groups [groups + 1] device int32, from 0, non-decreasing, ending at
+ *             batch (precondition; entries outside all groups share nothing):
+ *             entries cu_groups[g] .. cu_groups[g + 1] - 1 are group g
+ *   shared    [groups] device int32: how many tokens the group has in common.
+ *             The first shared[g] / page_size (rounded down) entries of its
+ *             requests' block table rows are the same, as kda_pages_fork leaves
+ *             them (precondition; which member's row is read is not specified).
+ *             More than a member has, or a negative number, does no harm.
+ * Everything else - the other arguments, what comes out, precision, values that
+ * are not finite, empty and invalid requests, sizes built and errors - is as for
+ * kda_latent_decode; results differ from its by the order of summation.
+ *   workspace kda_latent_decode_shared_workspace_size(...) bytes, 256-byte
+ *             aligned.  Errors beside those: KDA_ERR_SHAPE (groups < 1),
+ *             _RANGE (groups >= 2^24).
+ * ---------------------------------------------------------------------- */
+size_t kda_latent_decode_shared_workspace_size(int64_t batch, int64_t groups, int32_t L, int32_t h,
+                                               int32_t dl, int32_t dr);
+int kda_latent_decode_shared(const void *q, int32_t io_dtype, int64_t batch, int32_t L, int32_t h,
+                             int32_t dl, int32_t dr, float scale, const kda_cache *cache,
+                             const int32_t *block_table, int64_t requests, int64_t width,
+                             int64_t table_stride, const int32_t *seq_lens, const void *req,
+                             int32_t idx_type, const int32_t *cu_groups, const int32_t *shared,
+                             int64_t groups, void *out, float *lse, void *workspace, size_t ws_bytes,
+                             void *stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit latent pages
+ *
+ * A kda_cache of bytes (dtype KDA_U8) [n_pages, 1, page_size, dl + 2 dr + 4]:
+ * a page holds, one behind the other,
+ *   codes  [page_size][dl]  e4m3 (4 exponent bits, 3 of fraction, no infinity)
+ *   rope   [page_size][dr]  bf16
+ *   scales [page_size]      fp32
+ * and stands for the rows [c | r] with c = code * scale, r = rope * scale.  A
+ * token's scale is one power of two 2^e, so c is exact in bf16 and the rope key
+ * loses nothing by being kept in its units.  dl = 512: 644 bytes a token where
+ * a bf16 row has 1,152.  n_pages, page_size and the pages' 16-byte alignment as
+ * for bf16 pages (page_size a multiple of 8); kda_pages_copy takes them too.
+ *
+ * kda_latent_append8  kda_latent_append into 8-bit pages, quantising:
+ *     e     = the smallest integer >= -64 with max |c| <= 448 * 2^e and
+ *             max |r| <= 2^64 * 2^e (over the token's finite values)
+ *     code  = c * 2^-e to the nearest e4m3 value, ties to even (relative step
+ *             2^-3, from 2^-6 * 2^e down the fixed step 2^-9 * 2^e); NaN and
+ *             infinities become NaN
+ *     rope  = r * 2^-e to the nearest bf16 value, ties to even
+ *   x        [total, dl + dr] device, x_dtype (bf16 or fp32), rows x_stride
+ *            elements apart; 16-byte aligned rows
+ *   cu, req, count, table as for kda_latent_append
+ * kda_latent_read     rows of cached tokens, dense, from 8-bit or bf16 pages:
+ *   out row cu[i] + e = the row of token first[i] + e of request req[i], for
+ *   e < cu[i + 1] - cu[i] (first == NULL: from token 0), in bf16.  Rows of an
+ *   invalid request, of a negative position, of one at or beyond the request's
+ *   length and of an invalid page are zeros.  Rows outside cu[0] .. cu[count]
+ *   and the gaps between rows are not touched.
+ *   cu       [count + 1] device int32, non-decreasing, cu[0] >= 0
+ *   req      [count] device int32 / int64 (the same request may appear twice)
+ *   first    [count] device int32, or NULL
+ *   out      [total, dl + dr] device bf16, rows out_stride elements apart;
+ *            16-byte aligned rows; no row at or beyond total is written
+ * kda_latent_decode8  kda_latent_decode on 8-bit pages.  Scores, softmax
+ *   statistics and sums are fp32; the products are exact in their operands: a
+ *   query enters as two e4m3 parts (its bf16 digits; what lies 2^-22 below the
+ *   row's largest value is rounded), a weight as three (2^-12 of the weight; the
+ *   last part ends 2^-21 below the largest weight of any 16,384 tokens).  Other
+ *   arguments, results, non-finite values and errors as for kda_latent_decode.
+ * Errors: as for the bf16 calls; KDA_ERR_DTYPE when the cache is not KDA_U8 (for
+ * kda_latent_read: KDA_U8 or bf16), KDA_ERR_SHAPE when its k is not that of dl
+ * and dr, KDA_ERR_UNSUPPORTED outside dl in {256, 512}, dr == 64, page_size a
+ * multiple of 8, KDA_ERR_ALIGN for rows of x or out and pages not 16-byte
+ * aligned.
+ * ---------------------------------------------------------------------- */
+int kda_latent_append8(const void *x, int32_t x_dtype, int64_t x_stride, int64_t total, int32_t dl,
+                       int32_t dr, const int32_t *cu, const void *req, int32_t idx_type, int64_t count,
+                       const kda_page_table *table, const kda_cache *cache, void *stream);
+int kda_latent_read(const kda_cache *cache, int32_t dl, int32_t dr, const int32_t *cu, const void *req,
+                    int32_t idx_type, int64_t count, const int32_t *first, const kda_page_table *table,
+                    void *out, int64_t out_stride, int64_t total, void *stream);
+size_t kda_latent_decode8_workspace_size(int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr);
+int kda_latent_decode8(const void *q, int32_t io_dtype, int64_t batch, int32_t L, int32_t h,
+                       int32_t dl, int32_t dr, float scale, const kda_cache *cache,
+                       const int32_t *block_table, int64_t requests, int64_t width,
+                       int64_t table_stride, const int32_t *seq_lens, const void *req,
+                       int32_t idx_type, void *out, float *lse, void *workspace, size_t ws_bytes,
+                       void *stream);
+
+/* ------------------------------------------------------------------------
  * Page upkeep.  The calls below change the tables (block_table, seq_lens,
  * refcount) of a kda_page_table and name the page copies that go with the
  * change as pairs (move_src, move_dst); kda_pages_copy then carries them out
@@ -692,8 +790,8 @@ int kda_latent_append(const void *x, int64_t x_stride, int64_t total, const int3
  *                    then -1.  info: 0; moves; live pages; free pages.
  * kda_pages_copy     cache row move_dst[i] = cache row move_src[i] (the
  *                    payload; gaps are not touched) where both are in
- *                    [0, n_rows), on any kda_cache: latent pages or recurrent
- *                    states.  Preconditions: destinations unique, none is a
+ *                    [0, n_rows), on any kda_cache: latent pages (of 8 bits
+ *                    too) or recurrent states.  Preconditions: destinations unique, none is a
  *                    source.
  * workspace: kda_pages_workspace_size(n_pages, count) bytes (count 0 for
  * kda_pages_compact), 256-byte aligned, contents on entry do not matter.

@@ -12,6 +12,10 @@ arguments - every step of the computation runs in the library's CUDA kernels.
     kda_latent_decode(q, cache, block_table, seq_lens, out, workspace, latent_dim=...)
     kda_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, out, workspace, ...)
     kda_latent_append(x, cu, req, table, cache)
+    kda_latent_decode_shared(q, cache, block_table, seq_lens, cu_groups, shared, out, workspace, latent_dim=...)
+    kda_latent_append8(x, cu, req, table, cache, latent_dim=...)
+    kda_latent_read(cache, cu, req, table, out, latent_dim=...)
+    kda_latent_decode8(q, cache, block_table, seq_lens, out, workspace, latent_dim=...)
     kda_pages_{fork,release,reserve,compact,copy}(...)
 
 `cache` is a 4-D tensor view [N, H, V, K] whose inner [H, V, K] block is dense
@@ -24,7 +28,7 @@ import ctypes
 
 import torch
 
-from ._abi import (EXPORTED, KDA_BF16, KDA_F32, KDA_I32, KDA_I64, LIB_PATH, KdaCache, KdaError,
+from ._abi import (EXPORTED, KDA_BF16, KDA_F32, KDA_I32, KDA_I64, KDA_U8, LIB_PATH, KdaCache, KdaError,
                    KdaPageTable, _check, lib)
 
 __all__ = [
@@ -34,7 +38,8 @@ __all__ = [
     "kda_prefill_noalloc_status", "kda_decode_step",
     "kda_ckpt_store_int8", "kda_ckpt_load_int8", "kda_conv1d_varlen", "kda_conv1d_update", "kda_target_verify",
     "kda_latent_decode_workspace_size", "kda_latent_decode", "kda_latent_prefill_workspace_size", "kda_latent_prefill",
-    "kda_latent_append", "kda_pages_workspace_size", "kda_pages_fork", "kda_pages_release", "kda_pages_reserve",
+    "kda_latent_append", "kda_latent_decode_shared_workspace_size", "kda_latent_decode_shared", "kda_latent_append8", "kda_latent_read",
+    "kda_latent_decode8_workspace_size", "kda_latent_decode8", "kda_pages_workspace_size", "kda_pages_fork", "kda_pages_release", "kda_pages_reserve",
     "kda_pages_compact", "kda_pages_copy", "page_table_descriptor",
     "kda_status_string", "kda_prefill_workspace_status", "kda_selftest_bounded_wait", "cache_descriptor",
     "KdaError", "EXPORTED", "LIB_PATH",
@@ -74,15 +79,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def cache_descriptor(cache: torch.Tensor) -> KdaCache:
-    """kda_cache for a [N, H, V, K] view with a dense inner block."""
+def cache_descriptor(cache: torch.Tensor, pages8: bool = False) -> KdaCache:
+    """kda_cache for a [N, H, V, K] view with a dense inner block (pages8: uint8 is taken too)."""
     shape = cache.shape
     _need(len(shape) == 4, "cache must be a 4-D view [N, H, V, K]")
     N, H, V, K = shape
     row, head, vec, elem = cache.stride()
     _need((H == 1 or head == V * K) and (V == 1 or vec == K) and (K == 1 or elem == 1),
           "cache rows must hold a dense [H, V, K] block")
-    return KdaCache(cache.data_ptr(), _dtype_code(cache), 0, N, H, V, K, row)
+    code = KDA_U8 if pages8 and cache.dtype == torch.uint8 else _dtype_code(cache)
+    return KdaCache(cache.data_ptr(), code, 0, N, H, V, K, row)
 
 
 def _index_vector(idx: torch.Tensor) -> None:
@@ -400,14 +406,9 @@ def kda_latent_decode_workspace_size(batch: int, L: int, h: int, dl: int, dr: in
     return int(lib().kda_latent_decode_workspace_size(batch, L, h, dl, dr))
 
 
-def kda_latent_decode(q, cache, block_table, seq_lens, out, workspace, *, latent_dim: int, scale: float, req=None,
-                      lse=None, stream=None) -> None:
-    """Absorbed latent attention over paged latents: q [R, L, H, dl + dr] (bf16, queries in the
-    latent space) against the tokens of each request; out [R, L, H, dl] bf16, lse [R, L, H]
-    fp32 or None.  cache: a [n_pages, 1, page, dl + dr] bf16 view; block_table [requests,
-    width] and seq_lens [requests] int32; req [R] int32/int64 picks the rows (None: r).  With
-    L > 1 the query tokens are the request's last L (causal).  `scale` is the model's softmax
-    scale (that of its expanded head size, so it has no default here)."""
+def _decode_arguments(q, cache, block_table, seq_lens, out, workspace, latent_dim, scale, req, lse, pages8=False):
+    """The checked arguments that the three forms of latent decode share: up to idx_type, and from out to the
+    workspace's size (with what has to stay alive until the call)."""
     _need(q.dim() == 4, "q must be [R, L, H, dl + dr]")
     R, L, H, D = q.shape
     dl = int(latent_dim)
@@ -427,12 +428,51 @@ def kda_latent_decode(q, cache, block_table, seq_lens, out, workspace, *, latent
         _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (R, L, H),
               "lse must be contiguous float32 [R, L, H]")
     _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be a uint8 tensor")
-    d = cache_descriptor(cache)
-    rc = lib().kda_latent_decode(_ptr(q), _dtype_code(q), R, L, H, dl, D - dl, float(scale), ctypes.byref(d),
-                                 _ptr(block_table), B, W, row if B > 1 else max(W, row),
-                                 _ptr(seq_lens), _ptr(req), 0 if req is None else _itype_code(req), _ptr(out), _ptr(lse),
-                                 _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(rc, "kda_latent_decode")
+    d = cache_descriptor(cache, pages8)
+    return ((_ptr(q), _dtype_code(q), R, L, H, dl, D - dl, float(scale), ctypes.byref(d), _ptr(block_table), B, W,
+             row if B > 1 else max(W, row), _ptr(seq_lens), _ptr(req), 0 if req is None else _itype_code(req)),
+            (_ptr(out), _ptr(lse), _ptr(workspace), workspace.numel()))
+
+
+def kda_latent_decode(q, cache, block_table, seq_lens, out, workspace, *, latent_dim: int, scale: float, req=None,
+                      lse=None, stream=None) -> None:
+    """Absorbed latent attention over paged latents: q [R, L, H, dl + dr] (bf16, queries in the
+    latent space) against the tokens of each request; out [R, L, H, dl] bf16, lse [R, L, H]
+    fp32 or None.  cache: a [n_pages, 1, page, dl + dr] bf16 view; block_table [requests,
+    width] and seq_lens [requests] int32; req [R] int32/int64 picks the rows (None: r).  With
+    L > 1 the query tokens are the request's last L (causal).  `scale` is the model's softmax
+    scale (that of its expanded head size, so it has no default here)."""
+    head, tail = _decode_arguments(q, cache, block_table, seq_lens, out, workspace, latent_dim, scale, req, lse)
+    _check(lib().kda_latent_decode(*head, *tail, _stream(stream)), "kda_latent_decode")
+
+
+def kda_latent_decode_shared_workspace_size(batch: int, groups: int, L: int, h: int, dl: int, dr: int) -> int:
+    return int(lib().kda_latent_decode_shared_workspace_size(batch, groups, L, h, dl, dr))
+
+
+def kda_latent_decode_shared(q, cache, block_table, seq_lens, cu_groups, shared, out, workspace, *, latent_dim: int,
+                             scale: float, req=None, lse=None, stream=None) -> None:
+    """kda_latent_decode for entries in groups that begin with the same tokens in the same pages: entries
+    cu_groups[g] .. cu_groups[g+1]-1 (int32 [groups + 1]) have the first shared[g] (int32 [groups]) tokens in
+    common, of which the whole pages are attended to once for the group."""
+    head, tail = _decode_arguments(q, cache, block_table, seq_lens, out, workspace, latent_dim, scale, req, lse)
+    _need(cu_groups.dtype == torch.int32 and cu_groups.is_contiguous() and cu_groups.dim() == 1 and cu_groups.numel() >= 2,
+          "cu_groups must be a contiguous int32 tensor of groups + 1 >= 2 offsets")
+    G = cu_groups.numel() - 1
+    _int32_vector("shared", shared, G)
+    _check(lib().kda_latent_decode_shared(*head, _ptr(cu_groups), _ptr(shared), G, *tail, _stream(stream)),
+           "kda_latent_decode_shared")
+
+
+def kda_latent_decode8_workspace_size(batch: int, L: int, h: int, dl: int, dr: int) -> int:
+    return int(lib().kda_latent_decode8_workspace_size(batch, L, h, dl, dr))
+
+
+def kda_latent_decode8(q, cache, block_table, seq_lens, out, workspace, *, latent_dim: int, scale: float, req=None,
+                       lse=None, stream=None) -> None:
+    """kda_latent_decode on 8-bit pages: cache a [n_pages, 1, page, dl + 2 dr + 4] uint8 view."""
+    head, tail = _decode_arguments(q, cache, block_table, seq_lens, out, workspace, latent_dim, scale, req, lse, pages8=True)
+    _check(lib().kda_latent_decode8(*head, *tail, _stream(stream)), "kda_latent_decode8")
 
 
 def kda_latent_prefill_workspace_size(total_q: int, num_seqs: int, h: int) -> int:
@@ -490,6 +530,40 @@ def kda_latent_append(x, cu, req, table: KdaPageTable, cache, stream=None) -> No
     rc = lib().kda_latent_append(x.data_ptr(), row if T > 1 else max(D, row), T, cu.data_ptr(), req.data_ptr(),
                                  _itype_code(req), n, ctypes.byref(table), ctypes.byref(d), _stream(stream))
     _check(rc, "kda_latent_append")
+
+
+def kda_latent_append8(x, cu, req, table: KdaPageTable, cache, *, latent_dim: int, stream=None) -> None:
+    """kda_latent_append into 8-bit pages: rows of x [T, dl + dr] (bf16 or fp32) are quantised as they are written.
+    cache: a [n_pages, 1, page, dl + 2 dr + 4] uint8 view."""
+    _need(x.dim() == 2, "x must be [T, D] with a unit inner stride")
+    d = cache_descriptor(cache, pages8=True)
+    (T, D), (row, elem) = x.shape, x.stride()
+    _need(D == 1 or elem == 1, "x must be [T, D] with a unit inner stride")
+    _index_vector(req)
+    n = req.numel()
+    _int32_vector("cu", cu, n + 1)
+    dl = int(latent_dim)
+    rc = lib().kda_latent_append8(x.data_ptr(), _dtype_code(x), row if T > 1 else max(D, row), T, dl, D - dl, cu.data_ptr(),
+                                  req.data_ptr(), _itype_code(req), n, ctypes.byref(table), ctypes.byref(d), _stream(stream))
+    _check(rc, "kda_latent_append8")
+
+
+def kda_latent_read(cache, cu, req, table: KdaPageTable, out, *, latent_dim: int, first=None, stream=None) -> None:
+    """Rows cu[i] .. cu[i+1]-1 of out [T, dl + dr] (bf16) become the rows of the tokens from first[i] (int32; None: 0) on
+    of request req[i], from 8-bit or bf16 pages; zeros where there is no such token."""
+    _need(out.dim() == 2 and out.dtype == torch.bfloat16, "out must be bfloat16 [T, D] with a unit inner stride")
+    d = cache_descriptor(cache, pages8=True)
+    (T, D), (row, elem) = out.shape, out.stride()
+    _need(D == 1 or elem == 1, "out must be bfloat16 [T, D] with a unit inner stride")
+    _index_vector(req)
+    n = req.numel()
+    _int32_vector("cu", cu, n + 1)
+    if first is not None:
+        _int32_vector("first", first, n)
+    dl = int(latent_dim)
+    rc = lib().kda_latent_read(ctypes.byref(d), dl, D - dl, cu.data_ptr(), req.data_ptr(), _itype_code(req), n, _ptr(first),
+                               ctypes.byref(table), out.data_ptr(), row if T > 1 else max(D, row), T, _stream(stream))
+    _check(rc, "kda_latent_read")
 
 
 def kda_pages_workspace_size(n_pages: int, count: int) -> int:
@@ -555,9 +629,9 @@ def kda_pages_compact(table: KdaPageTable, move_src, move_dst, info, workspace, 
 
 
 def kda_pages_copy(cache, move_src, move_dst, stream=None) -> None:
-    """cache[move_dst[i]] = cache[move_src[i]] where both are valid rows (latent pages or states)."""
+    """cache[move_dst[i]] = cache[move_src[i]] where both are valid rows (latent pages, 8-bit ones too, or states)."""
     _same_lists(move_src, move_dst)
-    d = cache_descriptor(cache)
+    d = cache_descriptor(cache, pages8=True)
     rc = lib().kda_pages_copy(ctypes.byref(d), _ptr(move_src), _ptr(move_dst), _itype_code(move_src), move_src.numel(),
                               _stream(stream))
     _check(rc, "kda_pages_copy")

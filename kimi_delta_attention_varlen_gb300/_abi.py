@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(HERE, "_build", "libkda.so")
 
 KDA_F32 = 0
 KDA_BF16 = 1
+KDA_U8 = 2
 KDA_I32 = 0
 KDA_I64 = 1
 KDA_NOALLOC_SCRATCH_BYTES = 128 << 20  # include/kda.h
@@ -44,6 +45,12 @@ EXPORTED = (
     "kda_latent_prefill_workspace_size",
     "kda_latent_prefill",
     "kda_latent_append",
+    "kda_latent_decode_shared_workspace_size",
+    "kda_latent_decode_shared",
+    "kda_latent_append8",
+    "kda_latent_read",
+    "kda_latent_decode8_workspace_size",
+    "kda_latent_decode8",
     "kda_pages_workspace_size",
     "kda_pages_fork",
     "kda_pages_release",
@@ -163,6 +170,18 @@ def lib():
         L.kda_latent_prefill.restype = ctypes.c_int
         L.kda_latent_append.argtypes = [vp, i64, i64, vp, vp, i32, i64, table_p, cache_p, vp]
         L.kda_latent_append.restype = ctypes.c_int
+        L.kda_latent_decode_shared_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32]
+        L.kda_latent_decode_shared_workspace_size.restype = sz
+        L.kda_latent_decode_shared.argtypes = L.kda_latent_decode.argtypes[:16] + [vp, vp, i64, vp, vp, vp, sz, vp]
+        L.kda_latent_decode_shared.restype = ctypes.c_int
+        L.kda_latent_append8.argtypes = [vp, i32, i64, i64, i32, i32, vp, vp, i32, i64, table_p, cache_p, vp]
+        L.kda_latent_append8.restype = ctypes.c_int
+        L.kda_latent_read.argtypes = [cache_p, i32, i32, vp, vp, i32, i64, vp, table_p, vp, i64, i64, vp]
+        L.kda_latent_read.restype = ctypes.c_int
+        L.kda_latent_decode8_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+        L.kda_latent_decode8_workspace_size.restype = sz
+        L.kda_latent_decode8.argtypes = L.kda_latent_decode.argtypes
+        L.kda_latent_decode8.restype = ctypes.c_int
         L.kda_pages_workspace_size.argtypes = [i64, i64]
         L.kda_pages_workspace_size.restype = sz
         L.kda_pages_fork.argtypes = [table_p, vp, vp, i32, i64, vp]

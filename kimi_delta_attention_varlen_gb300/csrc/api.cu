@@ -22,7 +22,7 @@ int cuda_status(cudaError_t e)
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-int64_t esize(int32_t dtype) { return dtype == KDA_F32 ? 4 : 2; }
+int64_t esize(int32_t dtype) { return dtype == KDA_F32 ? 4 : dtype == KDA_BF16 ? 2 : 1; }
 
 bool valid_dtype(int32_t d) { return d == KDA_F32 || d == KDA_BF16; }
 
@@ -34,11 +34,11 @@ bool built_head_size(int32_t dk, int32_t dv) { return dk == dv && (dk == 32 || d
 bool compact_form(int32_t io_dtype, int32_t dk) { return io_dtype == KDA_BF16 && dk == 128; }
 
 // Layout predicate of the state-copy page ("Automatic dispatch"): fp32/bf16,
-// n_rows > 0, positive inner sizes, rows that do not overlap.
-int check_cache(const kda_cache *c, kda::CacheDesc *out)
+// n_rows > 0, positive inner sizes, rows that do not overlap.  pages8: 8-bit latent pages are taken too.
+int check_cache(const kda_cache *c, kda::CacheDesc *out, bool pages8 = false)
 {
     if (c == nullptr || c->data == nullptr) return KDA_ERR_NULL;
-    if (!valid_dtype(c->dtype)) return KDA_ERR_DTYPE;
+    if (!valid_dtype(c->dtype) && !(pages8 && c->dtype == KDA_U8)) return KDA_ERR_DTYPE;
     if (c->reserved != 0) return KDA_ERR_LAYOUT;
     if (c->n_rows <= 0 || c->h <= 0 || c->v <= 0 || c->k <= 0) return KDA_ERR_LAYOUT;
     const int64_t lim = INT64_C(1) << 40;
@@ -448,32 +448,144 @@ size_t kda_latent_decode_workspace_size(int64_t batch, int32_t L, int32_t h, int
     return kda::latent_decode_workspace(batch, L, h, dl);
 }
 
-int kda_latent_decode(const void *q, int32_t io_dtype, int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr,
-                      float scale, const kda_cache *cache, const int32_t *block_table, int64_t requests, int64_t width,
-                      int64_t table_stride, const int32_t *seq_lens, const void *req, int32_t idx_type, void *out,
-                      float *lse, void *workspace, size_t ws_bytes, void *stream)
+namespace {
+// What the forms of latent decode check alike: pages of `width_k` elements of `dtype`.  KDA_OK and a.batch == 0: nothing
+// to launch.
+int check_latent_decode(const void *q, int32_t io_dtype, int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr, float scale,
+                        const kda_cache *cache, int32_t dtype, int64_t width_k, const int32_t *block_table, int64_t requests,
+                        int64_t width, int64_t table_stride, const int32_t *seq_lens, const void *req, int32_t idx_type, void *out,
+                        float *lse, void *workspace, kda::LatentDecodeArgs *a)
 {
     kda::CacheDesc c{};
-    int rc = check_cache(cache, &c);
+    const int rc = check_cache(cache, &c, dtype == KDA_U8);
     if (rc != KDA_OK) return rc;
-    if (io_dtype != KDA_BF16 || c.dtype != KDA_BF16 || (req != nullptr && !valid_itype(idx_type))) return KDA_ERR_DTYPE;
+    if (io_dtype != KDA_BF16 || c.dtype != dtype || (req != nullptr && !valid_itype(idx_type))) return KDA_ERR_DTYPE;
     if (batch < 0 || L < 1 || h < 1 || dl < 1 || dr < 1 || requests < 1 || width < 1 || table_stride < width ||
-        c.h != 1 || c.k != static_cast<int64_t>(dl) + dr || (req == nullptr && requests < batch))
+        c.h != 1 || c.k != width_k || (req == nullptr && requests < batch))
         return KDA_ERR_SHAPE;
     if ((dl != 256 && dl != 512) || dr != 64 || c.v % 8 != 0) return KDA_ERR_UNSUPPORTED;
     if (!valid_scale(scale) || static_cast<int64_t>(L) * h > 65536 || static_cast<__int128>(batch) * L * h >= (INT64_C(1) << 31) ||
         static_cast<__int128>(width) * c.v >= (INT64_C(1) << 31) || c.n_rows >= (INT64_C(1) << 31) ||
         static_cast<__int128>(requests) * table_stride > (INT64_C(1) << 60))
         return KDA_ERR_RANGE;
+    *a = kda::LatentDecodeArgs{q, batch, L, h, dl, dr, scale, c, block_table, requests, width, table_stride, c.v, seq_lens, req,
+                               idx_type, out, lse, workspace};
     if (batch == 0) return KDA_OK;
     if (q == nullptr || block_table == nullptr || seq_lens == nullptr || out == nullptr) return KDA_ERR_NULL;
-    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(c.data, 16) || c.row_stride % 8 != 0 || !aligned(lse, 4) ||
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(c.data, 16) || c.row_stride * esize(dtype) % 16 != 0 || !aligned(lse, 4) ||
         !aligned(block_table, 4) || !aligned(seq_lens, 4) || (req != nullptr && !aligned(req, idx_type == KDA_I32 ? 4 : 8)))
         return KDA_ERR_ALIGN;
+    return KDA_OK;
+}
+
+int64_t row8(int64_t dl, int64_t dr) { return dl + 2 * dr + 4; }  // bytes of an 8-bit token
+}  // namespace
+
+int kda_latent_decode(const void *q, int32_t io_dtype, int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr,
+                      float scale, const kda_cache *cache, const int32_t *block_table, int64_t requests, int64_t width,
+                      int64_t table_stride, const int32_t *seq_lens, const void *req, int32_t idx_type, void *out,
+                      float *lse, void *workspace, size_t ws_bytes, void *stream)
+{
+    kda::LatentDecodeArgs a{};
+    int rc = check_latent_decode(q, io_dtype, batch, L, h, dl, dr, scale, cache, KDA_BF16, static_cast<int64_t>(dl) + dr, block_table,
+                                 requests, width, table_stride, seq_lens, req, idx_type, out, lse, workspace, &a);
+    if (rc != KDA_OK || batch == 0) return rc;
     if ((rc = check_workspace(workspace, ws_bytes, kda::latent_decode_workspace(batch, L, h, dl))) != KDA_OK) return rc;
-    kda::LatentDecodeArgs a{q, batch, L, h, dl, dr, scale, c, block_table, requests, width, table_stride, c.v, seq_lens, req,
-                            idx_type, out, lse, workspace};
     return cuda_status(kda::launch_latent_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_latent_decode_shared_workspace_size(int64_t batch, int64_t groups, int32_t L, int32_t h, int32_t dl, int32_t dr)
+{
+    if (groups < 1 || groups >= (1 << 24) || kda_latent_decode_workspace_size(batch, L, h, dl, dr) == 0) return 0;
+    return kda::latent_shared_workspace(batch, groups, L, h, dl);
+}
+
+int kda_latent_decode_shared(const void *q, int32_t io_dtype, int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr,
+                             float scale, const kda_cache *cache, const int32_t *block_table, int64_t requests, int64_t width,
+                             int64_t table_stride, const int32_t *seq_lens, const void *req, int32_t idx_type,
+                             const int32_t *cu_groups, const int32_t *shared, int64_t groups, void *out, float *lse,
+                             void *workspace, size_t ws_bytes, void *stream)
+{
+    kda::LatentDecodeArgs a{};
+    int rc = check_latent_decode(q, io_dtype, batch, L, h, dl, dr, scale, cache, KDA_BF16, static_cast<int64_t>(dl) + dr, block_table,
+                                 requests, width, table_stride, seq_lens, req, idx_type, out, lse, workspace, &a);
+    if (rc != KDA_OK) return rc;
+    if (groups < 1) return KDA_ERR_SHAPE;
+    if (groups >= (1 << 24)) return KDA_ERR_RANGE;
+    if (batch == 0) return KDA_OK;
+    if (cu_groups == nullptr || shared == nullptr) return KDA_ERR_NULL;
+    if (!aligned(cu_groups, 4) || !aligned(shared, 4)) return KDA_ERR_ALIGN;
+    if ((rc = check_workspace(workspace, ws_bytes, kda::latent_shared_workspace(batch, groups, L, h, dl))) != KDA_OK) return rc;
+    return cuda_status(kda::launch_latent_decode_shared(a, kda::SharedGroups{cu_groups, shared, groups},
+                                                        static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_latent_decode8_workspace_size(int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr)
+{
+    if (kda_latent_decode_workspace_size(batch, L, h, dl, dr) == 0) return 0;
+    return kda::latent_decode8_workspace(batch, L, h, dl);
+}
+
+int kda_latent_decode8(const void *q, int32_t io_dtype, int64_t batch, int32_t L, int32_t h, int32_t dl, int32_t dr,
+                       float scale, const kda_cache *cache, const int32_t *block_table, int64_t requests, int64_t width,
+                       int64_t table_stride, const int32_t *seq_lens, const void *req, int32_t idx_type, void *out,
+                       float *lse, void *workspace, size_t ws_bytes, void *stream)
+{
+    kda::LatentDecodeArgs a{};
+    int rc = check_latent_decode(q, io_dtype, batch, L, h, dl, dr, scale, cache, KDA_U8, row8(dl, dr), block_table, requests, width,
+                                 table_stride, seq_lens, req, idx_type, out, lse, workspace, &a);
+    if (rc != KDA_OK || batch == 0) return rc;
+    if ((rc = check_workspace(workspace, ws_bytes, kda::latent_decode8_workspace(batch, L, h, dl))) != KDA_OK) return rc;
+    return cuda_status(kda::launch_latent_decode8(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+// Rows of latents outside the pages: `total` of them, `stride` elements apart.
+int check_latent_rows(const kda::CacheDesc &c, const kda_page_table *table, int32_t dl, int32_t dr, const void *rows, int32_t dtype,
+                      int64_t stride, int64_t total, const int32_t *cu, int64_t count)
+{
+    if (total < 0 || dl < 1 || dr < 1 || c.h != 1 || c.k != (c.dtype == KDA_U8 ? row8(dl, dr) : static_cast<int64_t>(dl) + dr) ||
+        c.v != table->page_size || c.n_rows < table->n_pages || stride < static_cast<int64_t>(dl) + dr)
+        return KDA_ERR_SHAPE;
+    if ((dl != 256 && dl != 512) || dr != 64 || c.v % 8 != 0) return KDA_ERR_UNSUPPORTED;
+    if (total >= (INT64_C(1) << 31) || static_cast<__int128>(total) * stride > (INT64_C(1) << 60)) return KDA_ERR_RANGE;
+    if (total == 0 || count == 0) return KDA_OK;
+    if (rows == nullptr || cu == nullptr) return KDA_ERR_NULL;
+    if (!aligned(rows, 16) || stride * esize(dtype) % 16 != 0 || !aligned(c.data, 16) || c.row_stride * esize(c.dtype) % 16 != 0 ||
+        !aligned(cu, 4))
+        return KDA_ERR_ALIGN;
+    return KDA_OK;
+}
+}  // namespace
+
+int kda_latent_append8(const void *x, int32_t x_dtype, int64_t x_stride, int64_t total, int32_t dl, int32_t dr, const int32_t *cu,
+                       const void *req, int32_t idx_type, int64_t count, const kda_page_table *table, const kda_cache *cache,
+                       void *stream)
+{
+    kda::CacheDesc c{};
+    int rc = check_cache(cache, &c, true);
+    if (rc != KDA_OK) return rc;
+    if ((rc = check_page_list(table, req, idx_type, count)) != KDA_OK) return rc;
+    if (!valid_dtype(x_dtype) || c.dtype != KDA_U8) return KDA_ERR_DTYPE;
+    if ((rc = check_latent_rows(c, table, dl, dr, x, x_dtype, x_stride, total, cu, count)) != KDA_OK) return rc;
+    if (total == 0 || count == 0) return KDA_OK;
+    const kda::LatentRowsArgs a{const_cast<void *>(x), x_dtype, x_stride, total, dl, cu, req, idx_type, count, nullptr, *table, c};
+    return cuda_status(kda::launch_latent_append8(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kda_latent_read(const kda_cache *cache, int32_t dl, int32_t dr, const int32_t *cu, const void *req, int32_t idx_type, int64_t count,
+                    const int32_t *first, const kda_page_table *table, void *out, int64_t out_stride, int64_t total, void *stream)
+{
+    kda::CacheDesc c{};
+    int rc = check_cache(cache, &c, true);
+    if (rc != KDA_OK) return rc;
+    if ((rc = check_page_list(table, req, idx_type, count)) != KDA_OK) return rc;
+    if (c.dtype == KDA_F32) return KDA_ERR_DTYPE;
+    if ((rc = check_latent_rows(c, table, dl, dr, out, KDA_BF16, out_stride, total, cu, count)) != KDA_OK) return rc;
+    if (total == 0 || count == 0) return KDA_OK;
+    if (!aligned(first, 4)) return KDA_ERR_ALIGN;
+    const kda::LatentRowsArgs a{out, KDA_BF16, out_stride, total, dl, cu, req, idx_type, count, first, *table, c};
+    return cuda_status(kda::launch_latent_read(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kda_latent_prefill_workspace_size(int64_t total_q, int64_t num_seqs, int32_t h)
@@ -590,7 +702,7 @@ int kda_pages_copy(const kda_cache *cache, const void *move_src, const void *mov
                    void *stream)
 {
     kda::CacheDesc c{};
-    int rc = check_cache(cache, &c);
+    int rc = check_cache(cache, &c, true);
     if (rc != KDA_OK) return rc;
     if (!valid_itype(idx_type)) return KDA_ERR_DTYPE;
     if (count < 0) return KDA_ERR_SHAPE;

@@ -134,6 +134,35 @@ struct LatentDecodeArgs {
 size_t latent_decode_workspace(int64_t batch, int32_t L, int32_t h, int32_t dl);
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t st);
 
+// Groups of batch entries whose requests hold the same first pages.
+struct SharedGroups {
+    const int32_t *cu, *shared;  // [groups + 1], [groups]
+    int64_t groups;
+};
+size_t latent_shared_workspace(int64_t batch, int64_t groups, int32_t L, int32_t h, int32_t dl);
+cudaError_t launch_latent_decode_shared(const LatentDecodeArgs &a, const SharedGroups &g, cudaStream_t st);
+
+// The same over 8-bit pages (the cache in bytes).
+size_t latent_decode8_workspace(int64_t batch, int32_t L, int32_t h, int32_t dl);
+cudaError_t launch_latent_decode8(const LatentDecodeArgs &a, cudaStream_t st);
+
+// Rows of latents and the tokens of a list of requests that they go to (append8) or come from (read).
+struct LatentRowsArgs {
+    void *rows;  // [total, dl + 64], only read by append8
+    int32_t dtype;
+    int64_t stride, total;  // elements between rows
+    int32_t dl;
+    const int32_t *cu;
+    const void *req;
+    int32_t idx_type;
+    int64_t count;
+    const int32_t *first;  // read: nullable
+    kda_page_table table;
+    CacheDesc cache;
+};
+cudaError_t launch_latent_append8(const LatentRowsArgs &a, cudaStream_t st);
+cudaError_t launch_latent_read(const LatentRowsArgs &a, cudaStream_t st);
+
 // Expanded latent attention over a varlen batch (dn = dv = 128, dr = 64, bf16).
 struct LatentPrefillArgs {
     const void *q, *k_nope, *k_rope, *v;

@@ -14,6 +14,7 @@
 // The copies move whole page payloads in 16-byte vectors at the HBM rate.
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "page_lists.cuh"
 
 namespace kda {
 namespace {
@@ -49,11 +50,6 @@ Plan plan_of(void *ws, int64_t n_pages, int64_t count)
     p.first = p.prefix + count + 1;
     p.rank = p.prefix;
     return p;
-}
-
-__device__ __forceinline__ int64_t load_index(const void *p, int32_t itype, int64_t i)
-{
-    return itype == KDA_I32 ? static_cast<int64_t>(static_cast<const int32_t *>(p)[i]) : static_cast<const int64_t *>(p)[i];
 }
 
 __device__ __forceinline__ int32_t warp_sum(int32_t x)
@@ -97,13 +93,6 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *sh, int64_t *t
 }
 
 __device__ __forceinline__ int64_t pages_of(int64_t tokens, int64_t page) { return (tokens + page - 1) / page; }
-
-// Length of a request as the table can hold it.
-__device__ __forceinline__ int64_t length_of(const kda_page_table &t, int64_t r)
-{
-    const int64_t n = t.seq_lens[r], most = t.width * t.page_size;
-    return n < 0 ? 0 : n > most ? most : n;
-}
 
 __global__ void __launch_bounds__(128) fork_kernel(kda_page_table t, const void *src, const void *dst, int32_t itype,
                                                    int64_t count)
@@ -459,15 +448,7 @@ __global__ void __launch_bounds__(256) append_kernel(const V *x, int64_t x_strid
     const int lane = threadIdx.x & 31;
     const int64_t tok = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (tok >= total || tok < cu[0] || tok >= cu[count]) return;
-    // the request i with cu[i] <= tok < cu[i + 1], by 33-way steps of the warp: two looks for a thousand requests
-    int64_t lo = 0, hi = count;
-    while (hi - lo > 1) {
-        const int64_t step = (hi - lo + 31) / 32, at = lo + step * lane;
-        const uint32_t below = __ballot_sync(0xffffffffu, at < hi && cu[at] <= tok);  // lane 0 always
-        const int64_t from = lo + step * (below != 0 ? __popc(below) - 1 : 0);  // 0 only if the offsets fall somewhere
-        hi = from + step < hi ? from + step : hi;
-        lo = from;
-    }
+    const int64_t lo = entry_of(cu, count, tok);
     const int64_t r = load_index(req, itype, lo);
     if (r < 0 || r >= t.requests || tok >= cu[lo + 1]) return;
     const int64_t pos = length_of(t, r) - cu[lo + 1] + tok;
@@ -527,7 +508,7 @@ cudaError_t launch_pages_compact(const kda_page_table &t, int32_t *move_src, int
 cudaError_t launch_pages_copy(const CacheDesc &c, const void *src, const void *dst, int32_t itype, int64_t count,
                               cudaStream_t st)
 {
-    const int64_t es = c.dtype == KDA_F32 ? 4 : 2, payload = c.h * c.v * c.k;
+    const int64_t es = c.dtype == KDA_F32 ? 4 : c.dtype == KDA_BF16 ? 2 : 1, payload = c.h * c.v * c.k;
     const bool vec = (reinterpret_cast<uintptr_t>(c.data) & 15u) == 0 && c.row_stride * es % 16 == 0 && payload * es % 16 == 0;
     const int64_t units = vec ? payload * es / 16 : payload;
     const int64_t tiles = vec ? (units + kCopyThreads * kMostVecs - 1) / (kCopyThreads * kMostVecs) : (units + kCopyThreads - 1) / kCopyThreads;
@@ -538,6 +519,9 @@ cudaError_t launch_pages_copy(const CacheDesc &c, const void *src, const void *d
                                  c.row_stride * es / 16, units, vecs, src, dst, itype, count);
     if (c.dtype == KDA_F32)
         return launch_overlapped(copy_pages_scalar<float>, grid, dim3(kCopyThreads), 0, st, static_cast<float *>(c.data), c.n_rows,
+                                 c.row_stride, units, src, dst, itype, count);
+    if (c.dtype == KDA_U8)
+        return launch_overlapped(copy_pages_scalar<uint8_t>, grid, dim3(kCopyThreads), 0, st, static_cast<uint8_t *>(c.data), c.n_rows,
                                  c.row_stride, units, src, dst, itype, count);
     return launch_overlapped(copy_pages_scalar<uint16_t>, grid, dim3(kCopyThreads), 0, st, static_cast<uint16_t *>(c.data), c.n_rows,
                              c.row_stride, units, src, dst, itype, count);
