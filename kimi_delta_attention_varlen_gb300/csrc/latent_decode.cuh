@@ -98,12 +98,13 @@ __device__ __forceinline__ void ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16])
                  : "r"(taddr));
 }
 
+template <int Threads = kSoftThreads>
 __device__ __forceinline__ bool soft_any(bool v)  // the softmax warps (named barrier 1)
 {
     uint32_t r;
     asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
                  : "=r"(r)
-                 : "r"(v ? 1u : 0u), "n"(kSoftThreads)
+                 : "r"(v ? 1u : 0u), "n"(Threads)
                  : "memory");
     return r != 0;
 }

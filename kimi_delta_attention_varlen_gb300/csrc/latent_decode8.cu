@@ -19,8 +19,8 @@
 // the rest takes no digits from more than 16,384 others.
 //
 // Shares, walk and join are those of the bf16 form (latent_decode.cuh); a tile (codes in panels of T tokens x 128 dimensions,
-// rope keys, units) is one stage of a ring.  Warps: 0 and 3 copy, 1 and 2 issue one product each, 4 to 7 do the softmax and the
-// epilogue, 8 to 11 split the next segment's queries into their parts while this one's tiles run.
+// rope keys, units) is one stage of a ring.  Warps: 0 and 3 copy, 1 and 2 issue one product each, 4 to 11 do the softmax and the
+// epilogue, 12 to 15 split the next segment's queries into their parts while this one's tiles run.
 //
 // Every wait is bounded; an expired one sets the workspace's status word (6) and ends the CTA.
 #include <cuda_fp16.h>
@@ -33,7 +33,7 @@ namespace {
 
 using namespace latent;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512, kSoft = 256;  // of the softmax: two warps for the same query rows, half of a tile's tokens each
 constexpr float kLazy = 4.f;   // log2 of the growth that forces a rescale
 constexpr int kLowest = -100;  // of a query row's exponent
 
@@ -86,6 +86,15 @@ __device__ __forceinline__ int exponent_for(uint32_t most, int p, uint32_t f)
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 __device__ __forceinline__ uint32_t bf16x2_finite_magnitude(uint32_t u) { return u & 0x7fff7fffu & ~bf16x2_not_finite(u); }
 
+__device__ __forceinline__ void ld1(uint32_t taddr, uint32_t &r)  // this thread's lane, one column
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n" : "=r"(r) : "r"(taddr));
+}
+__device__ __forceinline__ void st1(uint32_t taddr, uint32_t r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(r) : "memory");
+}
+
 template <int DL, int N>
 __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, const __grid_constant__ Maps maps)
 {
@@ -95,7 +104,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
     __shared__ __align__(8) Bars<C> bar;
     __shared__ uint32_t tmem_base;
     __shared__ int32_t not_finite;                    // segments (from 1) of the last value that was taken out
-    __shared__ float corr[2][N], fac[N], worth[N];    // corr: by parity of the tile, so that a late reader keeps its own
+    __shared__ float corr[N], fac[N], worth[N], top[2][N];
+    __shared__ float2 lm[2][N];                       // l and m of the halves of a tile's tokens
+    __shared__ uint32_t grown;                        // rows that are rescaled
     __shared__ float kept[2][N];                      // set aside: maximum that the sums are relative to, l
     __shared__ float q_unit[4][N];                    // 2^a of a segment's query rows, four segments deep: see the splitting warps
     __shared__ int64_t sums[kThreads / 32];
@@ -111,8 +122,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
     if (tid == 0) {
         for (int j = 0; j < C::RING; ++j) mbar_init(&bar.full[j], 2), mbar_init(&bar.empty[j], 1);
         mbar_init(&bar.q_full, 128), mbar_init(&bar.q_free, 1);
-        mbar_init(&bar.p, kSoftThreads), mbar_init(&bar.o, 1), mbar_init(&bar.rope, 1);
-        for (int j = 0; j < 2; ++j) mbar_init(&bar.s[j], 1), mbar_init(&bar.s_free[j], kSoftThreads), mbar_init(&bar.drain[j], 1);
+        mbar_init(&bar.p, kSoft), mbar_init(&bar.o, 1), mbar_init(&bar.rope, 1);
+        for (int j = 0; j < 2; ++j) mbar_init(&bar.s[j], 1), mbar_init(&bar.s_free[j], kSoft), mbar_init(&bar.drain[j], 1);
         not_finite = 0;
         fence_mbar_init();
     }
@@ -134,14 +145,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
         w.tile = edge[0].tile;
     }
     bool gave_up = false;
-    auto wait = [&](uint64_t *b, uint32_t parity) {
+    auto wait = [&](uint64_t *b, uint32_t parity) {  // by a whole warp, which goes on or gives up as one
         if (!gave_up && !mbar_wait(b, parity, kWaitLimit)) {
             gave_up = true;
             atomicExch(p.status, kStatusExpired);
         }
+        gave_up = __any_sync(0xffffffffu, gave_up) != 0;
         return !gave_up;
     };
-    auto all_wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
 
     if (warp == 0 || warp == 3) {
         // ---------------------------------------------------------------- copies
@@ -169,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
             const int32_t valid = w.n - w.tile * T < T ? w.n - w.tile * T : T;
             const int32_t chunks = (valid + br - 1) / br;
             const int s = i % C::RING;
-            if (!(ok = all_wait(&bar.empty[s], ((i / C::RING) & 1) ^ 1))) break;
+            if (!(ok = wait(&bar.empty[s], ((i / C::RING) & 1) ^ 1))) break;
             char *stage = smem + C::OFF_RING + s * C::STAGE;
             float *units = reinterpret_cast<float *>(smem + C::OFF_UNIT) + s * T;
             int32_t bytes = chunks * br * (C::MT / 2 * 128 + (part == 0 ? 0 : 128));
@@ -211,9 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
         bool ok = true;
         for (int32_t i = 0; i < total && ok; ++i) {
             const uint32_t d = tmem + C::COL_S + T * (i & 1);
-            if (i > 1) ok = all_wait(&bar.s_free[i & 1], ((i >> 1) & 1) ^ 1);
-            if (ok && __all_sync(0xffffffffu, i == 0 || w.first())) ok = all_wait(&bar.q_full, segs++ & 1);
-            if (!ok || !(ok = all_wait(&bar.full[slot], par))) break;
+            if (i > 1) ok = wait(&bar.s_free[i & 1], ((i >> 1) & 1) ^ 1);
+            if (ok && __all_sync(0xffffffffu, i == 0 || w.first())) ok = wait(&bar.q_full, segs++ & 1);
+            if (!ok || !(ok = wait(&bar.full[slot], par))) break;
             tc::fence_after_sync();
             const uint64_t x = x_desc + slot * (C::STAGE >> 4);
             if (elect_one()) {
@@ -224,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
             }
             __syncwarp();
             // products of another operand type join the sum only when these have: their order is promised within a type
-            if (!(ok = all_wait(&bar.rope, i & 1))) break;
+            if (!(ok = wait(&bar.rope, i & 1))) break;
             tc::fence_after_sync();
             const bool last = __all_sync(0xffffffffu, w.last()) != 0;
             if (elect_one()) {
@@ -253,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
         for (int32_t i = 0; i < total && ok; ++i) {
             if (w.first()) tile0 = 0;
             const uint32_t more = __all_sync(0xffffffffu, ((w.tile - tile0) & (kSumTiles - 1)) == 0) ? 0u : 1u;
-            if (!(ok = all_wait(&bar.p, i & 1))) break;
+            if (!(ok = wait(&bar.p, i & 1))) break;
             tc::fence_after_sync();
             if (elect_one()) {
 #pragma unroll
@@ -271,10 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
         }
         if (elect_one()) tc::commit(&bar.drain[1]);
         mbar_wait(&bar.drain[1], 0, kWaitLimit);
-    } else if (warp >= 8 && total > 0) {
+    } else if (warp >= 12 && total > 0) {
         // --------------------------------------------------- queries into their parts
         constexpr int TPR = 128 / N, UNITS = DL / 16 / TPR;  // threads a row; 16 values of the latent part a unit
-        const int qt = tid - 256, row = qt / TPR, j = qt % TPR;
+        const int qt = tid - 384, row = qt / TPR, j = qt % TPR;
         const int rho = 16 * (row >> 3) + (row & 7);  // of the first part; the second is 8 rows behind
         int32_t segs = 0;
         bool ok = true;
@@ -309,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
             const float down = power_of_two(-a);
             // the products of the segment before have read its parts (q_unit: the softmax has read the unit of the last
             // segment but two, since a tile's scores wait for the softmax of the last tile but one)
-            if (segs > 0 && !(ok = all_wait(&bar.q_free, (segs - 1) & 1))) break;
+            if (segs > 0 && !(ok = wait(&bar.q_free, (segs - 1) & 1))) break;
             if (j == 0) q_unit[segs & 3][row] = power_of_two(a);
 #pragma unroll
             for (int u = 0; u < UNITS; ++u) {
@@ -350,13 +361,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
             w.tile = w.tiles - 1;
             w.next(p);
         }
-    } else if (warp >= 4 && warp < 8 && total > 0) {
+    } else if (warp >= 4 && total > 0) {
         // --------------------------------------------------- softmax and epilogue
-        const int quad = warp & 3, g = lane >> 2, t = lane & 3;
+        const int quad = warp & 3, half = (warp - 4) >> 2, g = lane >> 2, t = lane & 3, st = tid - 128;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16);
         const bool active = 8 * quad < N;  // this warp holds the parts of query rows 8 quad ... + 7
         const int row = 8 * quad + g;
-        float m = -INFINITY, big = -INFINITY, l = 0.f, unit = 0.f;  // big: the maximum M of z + e
+        constexpr int HT = T / 2;  // a half's tokens
+        float m = -INFINITY, big = -INFINITY, l = 0.f, unit = 0.f;  // m, l: of this half; big: the maximum M of z + e
         int32_t seen = 0;
         int slot_out = 0;
         int32_t segments = 0, tile0 = 0;  // tile0: the segment's first
@@ -367,33 +379,38 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
                 float sum = l;
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if (t == 0) {
-                    float back = begun ? rebase(kept[0][row], m) : 0.f;
-                    if (begun) sum = fmaf(kept[1][row], back, sum);
-                    kept[0][row] = m, kept[1][row] = sum;
-                    // a weight's 16 parts, and from M to m: the sums come to be relative to m as l is
-                    float f = m == -INFINITY || big == -INFINITY ? 0.0625f : 0.0625f * exp2f(big - m);
-                    const int rr = w.group * N + row;
-                    if (whole) {
-                        const float inv = inverse(sum);
-                        f *= inv, back *= inv;
-                        if (p.a.lse != nullptr && rr < p.rows) p.a.lse[w.r * p.rows + rr] = log_sum(m, sum);
-                    } else if (end) {
-                        p.ml[part * N + row] = make_float4(m, sum, sum, 0.f);
-                    }
-                    fac[row] = f;
-                    worth[row] = back;
+                if (t == 0) lm[half][row] = make_float2(sum, m);
+            }
+            soft_any<kSoft>(false);
+            if (active && half == 0 && t == 0) {
+                const float2 a = lm[0][row], b = lm[1][row];
+                const float mm = fmaxf(a.y, b.y);
+                float sum = a.x * rebase(a.y, mm) + b.x * rebase(b.y, mm);
+                float back = begun ? rebase(kept[0][row], mm) : 0.f;
+                if (begun) sum = fmaf(kept[1][row], back, sum);
+                kept[0][row] = mm, kept[1][row] = sum;
+                // a weight's 16 parts, and from M to m: the sums come to be relative to m as l is
+                float f = mm == -INFINITY || big == -INFINITY ? 0.0625f : 0.0625f * exp2f(big - mm);
+                const int rr = w.group * N + row;
+                if (whole) {
+                    const float inv = inverse(sum);
+                    f *= inv, back *= inv;
+                    if (p.a.lse != nullptr && rr < p.rows) p.a.lse[w.r * p.rows + rr] = log_sum(mm, sum);
+                } else if (end) {
+                    p.ml[part * N + row] = make_float4(mm, sum, sum, 0.f);
                 }
+                fac[row] = f;
+                worth[row] = back;
             }
             l = 0.f, big = -INFINITY;
             wait(&bar.o, i & 1);
             tc::fence_after_sync();
-            soft_any(false);  // fac, worth are complete
+            soft_any<kSoft>(false);  // fac, worth are complete
             const int valid = p.rows - w.group * N < N ? p.rows - w.group * N : N;
             const int dim = 32 * quad + lane;
             const bool taken = end && not_finite == segments;
 #pragma unroll 1
-            for (int c0 = 0; c0 < C::MT * N; c0 += 16) {
+            for (int c0 = 16 * half; c0 < C::MT * N; c0 += 32) {
                 const int mt = c0 / N, row0 = c0 % N;
                 uint32_t o1[16], o2[16], o3[16];
                 tc::ld16(tl + mt * 3 * N + row0, o1);
@@ -436,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
                 }
             }
             tc::fence_before_sync();
-            soft_any(false);  // fac and worth may be written again
+            soft_any<kSoft>(false);  // fac and worth may be written again
         };
         // a thread that gave up goes on without waiting: all of them meet at every barrier
         for (int32_t i = 0; i < total; ++i) {
@@ -453,43 +470,39 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
                 finish(i - 1, w.tile - tile0 > kSumTiles, false, false);  // this tile's product does not add to it
             }
             const int stage = i % C::RING;
-            wait(&bar.s[i & 1], (i >> 1) & 1);
-            wait(&bar.full[stage], (i / C::RING) & 1);  // it was complete for S; the units are read here
+            wait(&bar.s[i & 1], (i >> 1) & 1);  // the tile's copies were complete for S
             tc::fence_after_sync();
-            const int32_t t0 = w.tile * T;
-            uint32_t h[T / 8];  // weights, 16 times, as fp16 pairs: tokens 8 j + 2 t, + 1
-            bool grew = false;
+            const int32_t t0 = w.tile * T, th = t0 + HT * half;
+            float u[HT / 4];  // z + e of tokens th + 8 j + 2 t, + 1
+            float mu = -INFINITY;
             if (active) {
                 if (fresh) unit = q_unit[(segments - 1) & 3][row] * p.scale_log2;
-                float z[T / 4], u[T / 4];
-                const float *units = reinterpret_cast<const float *>(smem + C::OFF_UNIT) + stage * T + 2 * t;
-#pragma unroll
-                for (int c0 = 0; c0 < T; c0 += 32) {
-                    uint32_t s[16];
-                    ld_16x256b_x4(tl + C::COL_S + T * (i & 1) + c0, s);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 un = *reinterpret_cast<const float2 *>(units + c0 + 8 * j);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float x = e ? un.y : un.x;
-                            const int k = c0 / 4 + 2 * j + e;
-                            z[k] = fmaf(__uint_as_float(s[4 * j + 2 + e]), 0.0625f, __uint_as_float(s[4 * j + e])) * x * unit;
-                            u[k] = z[k] + static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23 & 255u) - 127);
-                        }
-                    }
-                }
+                float z[HT / 4];
+                const float *units = reinterpret_cast<const float *>(smem + C::OFF_UNIT) + stage * T + HT * half + 2 * t;
+                uint32_t s[16];
+                ld_16x256b_x4(tl + C::COL_S + T * (i & 1) + HT * half, s);
+                tc::wait_ld();
                 tc::fence_before_sync();
                 mbar_arrive(&bar.s_free[i & 1]);
-                if (t0 + T > seen) {
 #pragma unroll
-                    for (int j = 0; j < T / 4; ++j)
-                        if (t0 + 8 * (j >> 1) + 2 * t + (j & 1) >= seen) z[j] = u[j] = -INFINITY;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 un = *reinterpret_cast<const float2 *>(units + 8 * j);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = e ? un.y : un.x;
+                        z[2 * j + e] = fmaf(__uint_as_float(s[4 * j + 2 + e]), 0.0625f, __uint_as_float(s[4 * j + e])) * x * unit;
+                        u[2 * j + e] = z[2 * j + e] + static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23 & 255u) - 127);
+                    }
                 }
-                float mx = z[0], mu = u[0];
+                if (th + HT > seen) {
 #pragma unroll
-                for (int j = 1; j < T / 4; ++j) mx = fmaxf(mx, z[j]), mu = fmaxf(mu, u[j]);
+                    for (int j = 0; j < HT / 4; ++j)
+                        if (th + 8 * (j >> 1) + 2 * t + (j & 1) >= seen) z[j] = u[j] = -INFINITY;
+                }
+                float mx = z[0];
+                mu = u[0];
+#pragma unroll
+                for (int j = 1; j < HT / 4; ++j) mx = fmaxf(mx, z[j]), mu = fmaxf(mu, u[j]);
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -498,48 +511,57 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
                     if (m != -INFINITY) l *= ex2_approx(m - mx);
                     m = mx;
                 }
-                float c = 1.f;
-                if (big == -INFINITY) {
-                    big = mu;  // nothing summed yet
-                } else if (mu > big + kLazy) {
-                    c = ex2_approx(big - mu);
-                    big = mu;
-                    grew = true;
-                }
-                if (t == 0) corr[i & 1][row] = c;
-                const float base = m == -INFINITY ? 0.f : m, above = (big == -INFINITY ? 0.f : big) - 4.f;  // 16 times
+                const float base = m == -INFINITY ? 0.f : m;
                 float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < T / 8; ++j) {
-                    sum += ex2_approx(z[2 * j] - base) + ex2_approx(z[2 * j + 1] - base);
-                    h[j] = half2_of(ex2_approx(u[2 * j] - above), ex2_approx(u[2 * j + 1] - above));
-                }
+                for (int j = 0; j < HT / 4; ++j) sum += ex2_approx(z[j] - base);
                 l += sum;
             } else {
                 mbar_arrive(&bar.s_free[i & 1]);
+            }
+            const bool first = big == -INFINITY;  // nothing summed yet
+            const bool grew = soft_any<kSoft>(active && (first ? mu != -INFINITY : mu > big + kLazy));
+            if (grew) {  // rarely: both halves take one M, the columns of the rows that grew are rescaled
+                if (st == 0) grown = 0;
+                if (active && t == 0) top[half][row] = mu;
+                soft_any<kSoft>(false);
+                if (active) {
+                    mu = fmaxf(top[0][row], top[1][row]);
+                    if (first) {
+                        big = mu;
+                    } else if (mu > big + kLazy) {
+                        if (half == 0 && t == 0) corr[row] = ex2_approx(big - mu), atomicOr(&grown, 1u << row);
+                        big = mu;
+                    }
+                }
+                soft_any<kSoft>(false);
             }
             // the second product of the tile before has read P and written O^T
             if (i > 0) wait(&bar.o, (i - 1) & 1);
             tc::fence_after_sync();
             if (active) {
+                const float above = (big == -INFINITY ? 0.f : big) - 4.f;  // weights 16 times, as fp16 pairs
                 char *pr = smem + C::OFF_P + row * 128 + 2 * t;
+                uint32_t h[HT / 8];
+#pragma unroll
+                for (int j = 0; j < HT / 8; ++j) h[j] = half2_of(ex2_approx(u[2 * j] - above), ex2_approx(u[2 * j + 1] - above));
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
 #pragma unroll
-                    for (int j = 0; j < T / 8; ++j)
-                        *reinterpret_cast<uint16_t *>(pr + k * N * 128 + ((((j >> 1) ^ (row & 7)) << 4) | ((j & 1) << 3))) =
+                    for (int j = 0; j < HT / 8; ++j)
+                        *reinterpret_cast<uint16_t *>(pr + k * N * 128 + (((2 * half + (j >> 1)) ^ (row & 7)) << 4 | (j & 1) << 3)) =
                             static_cast<uint16_t>(part_of(h[j]));
             }
             char *codes = smem + C::OFF_RING + stage * C::STAGE;
             if (w.n - t0 < T) {  // rows behind the last token: whatever they hold must not meet P = 0
                 const int from = w.n - t0;
-                for (int e = tid - 128; e < (T - from) * C::MT * 8; e += kSoftThreads)
+                for (int e = st; e < (T - from) * C::MT * 8; e += kSoft)
                     *reinterpret_cast<uint4 *>(codes + ((e >> 3) % C::MT) * C::PB + (from + (e >> 3) / C::MT) * 128 + (e & 7) * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
             }
             if (p.a.L > 1 && t0 + T > w.n - (p.a.L - 1)) {  // draft tokens: a NaN must not meet P = 0 either
                 const int from = max(w.n - (p.a.L - 1) - t0, 0), to = min(w.n - t0, T);
-                for (int e = tid - 128; e < (to - from) * C::MT * 8; e += kSoftThreads) {
+                for (int e = st; e < (to - from) * C::MT * 8; e += kSoft) {
                     uint4 *x = reinterpret_cast<uint4 *>(codes + ((e >> 3) % C::MT) * C::PB + (from + (e >> 3) / C::MT) * 128 + (e & 7) * 16);
                     const uint4 v = *x;
                     auto nan4 = [](uint32_t c) { return __vcmpeq4(c & 0x7f7f7f7fu, 0x7f7f7f7fu); };
@@ -550,25 +572,26 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
                     }
                 }
             }
-            fence_proxy_async_smem();
-            if (soft_any(grew) && !fresh) {
-#pragma unroll 1
-                for (int c0 = 0; c0 < C::MT * 3 * N; c0 += 16) {
-                    uint32_t o[16];
-                    tc::ld16(tl + c0, o);
+            if (grew) {
+                for (uint32_t rows = grown; rows != 0; rows &= rows - 1) {
+                    const int r2 = __ffs(rows) - 1;
+                    constexpr int COLS = 3 * C::MT / 2;  // this half's
+                    uint32_t o[COLS];
+#pragma unroll
+                    for (int c = 0; c < COLS; ++c) ld1(tl + (half * COLS + c) * N + r2, o[c]);
                     tc::wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr[i & 1][(c0 + e) % N]);
-                    tc::st16(tl + c0, o);
+                    for (int c = 0; c < COLS; ++c) st1(tl + (half * COLS + c) * N + r2, __float_as_uint(__uint_as_float(o[c]) * corr[r2]));
                 }
                 tc::wait_st();
             }
+            fence_proxy_async_smem();
             tc::fence_before_sync();
             mbar_arrive(&bar.p);
             const bool last = w.last();
             if (last || i + 1 == total) {  // the segment ends here
                 const bool whole = last && slot_out == 1;
-                if (!whole && tid == 128) (slot_out ? p.item1 : p.item0)[cta] = static_cast<int32_t>(w.r * p.groups + w.group);
+                if (!whole && st == 0) (slot_out ? p.item1 : p.item0)[cta] = static_cast<int32_t>(w.r * p.groups + w.group);
                 finish(i, w.tile - tile0 >= kSumTiles, true, whole);
             }
             w.next(p);
