@@ -318,10 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
             const uint32_t top = max(most << 16, most & 0xffff0000u), top_r = max(most_r << 16, most_r & 0xffff0000u);
             const int a = max(max(exponent_for(top, 8, 0x600000u), exponent_for(top_r, 64, 0u)), kLowest);
             const float down = power_of_two(-a);
-            // the products of the segment before have read its parts (q_unit: the softmax has read the unit of the last
-            // segment but two, since a tile's scores wait for the softmax of the last tile but one)
-            if (segs > 0 && !(ok = wait(&bar.q_free, (segs - 1) & 1))) break;
-            if (j == 0) q_unit[segs & 3][row] = power_of_two(a);
+            // x: of each 16 values the 16 codes of the first parts and those of the second
 #pragma unroll
             for (int u = 0; u < UNITS; ++u) {
                 uint32_t c1[4], c2[4];
@@ -340,19 +337,30 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
                     c1[e] = p1[0] | p1[1] << 16;
                     c2[e] = p2[0] | p2[1] << 16;
                 }
-                const int unit = u * TPR + j;
-                char *to = smem + (unit >> 3) * C::QB + rho * 128 + (((unit & 7) ^ (rho & 7)) << 4);
-                *reinterpret_cast<uint4 *>(to) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
-                *reinterpret_cast<uint4 *>(to + 8 * 128) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
+                x[u][0] = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+                x[u][1] = make_uint4(c2[0], c2[1], c2[2], c2[3]);
             }
 #pragma unroll
             for (int e = 0; e < 8 / TPR; ++e) {
-                const uint32_t v[4] = {rp[e].x, rp[e].y, rp[e].z, rp[e].w};
-                uint32_t y[4];
+                const uint4 v = rp[e];
+                rp[e] = make_uint4(pack_bf16x2(bf16_lo(v.x) * down, bf16_hi(v.x) * down), pack_bf16x2(bf16_lo(v.y) * down, bf16_hi(v.y) * down),
+                                   pack_bf16x2(bf16_lo(v.z) * down, bf16_hi(v.z) * down), pack_bf16x2(bf16_lo(v.w) * down, bf16_hi(v.w) * down));
+            }
+            // the products of the segment before have read its parts (q_unit: the softmax has read the unit of the last
+            // segment but two, since a tile's scores wait for the softmax of the last tile but one)
+            if (segs > 0 && !(ok = wait(&bar.q_free, (segs - 1) & 1))) break;
+            if (j == 0) q_unit[segs & 3][row] = power_of_two(a);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = pack_bf16x2(bf16_lo(v[k]) * down, bf16_hi(v[k]) * down);
+            for (int u = 0; u < UNITS; ++u) {
+                const int unit = u * TPR + j;
+                char *to = smem + (unit >> 3) * C::QB + rho * 128 + (((unit & 7) ^ (rho & 7)) << 4);
+                *reinterpret_cast<uint4 *>(to) = x[u][0];
+                *reinterpret_cast<uint4 *>(to + 8 * 128) = x[u][1];
+            }
+#pragma unroll
+            for (int e = 0; e < 8 / TPR; ++e) {
                 char *to = smem + C::MT * C::QB + rho * 128 + (((e * TPR + j) ^ (rho & 7)) << 4);
-                *reinterpret_cast<uint4 *>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4 *>(to) = rp[e];
                 *reinterpret_cast<uint4 *>(to + 8 * 128) = zero;
             }
             fence_proxy_async_smem();
@@ -487,12 +495,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 un = *reinterpret_cast<const float2 *>(units + 8 * j);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float x = e ? un.y : un.x;
-                        z[2 * j + e] = fmaf(__uint_as_float(s[4 * j + 2 + e]), 0.0625f, __uint_as_float(s[4 * j + e])) * x * unit;
-                        u[2 * j + e] = z[2 * j + e] + static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23 & 255u) - 127);
-                    }
+                    const float2 zz = mul2(mul2(fma2(make_float2(__uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3])),
+                                                     make_float2(0.0625f, 0.0625f),
+                                                     make_float2(__uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]))),
+                                                un), make_float2(unit, unit));
+                    // 2^23 + (e + 127), the exponent's bits behind those of 2^23
+                    const float2 e = make_float2(__uint_as_float(__float_as_uint(un.x) >> 23 | 0x4b000000u),
+                                                 __uint_as_float(__float_as_uint(un.y) >> 23 | 0x4b000000u));
+                    const float2 uu = add2(add2(e, make_float2(-8388735.f, -8388735.f)), zz);
+                    z[2 * j] = zz.x, z[2 * j + 1] = zz.y, u[2 * j] = uu.x, u[2 * j + 1] = uu.y;
                 }
                 if (th + HT > seen) {
 #pragma unroll
