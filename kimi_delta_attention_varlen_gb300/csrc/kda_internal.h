@@ -139,6 +139,9 @@ struct SharedGroups {
     const int32_t *cu, *shared;  // [groups + 1], [groups]
     int64_t groups;
 };
+// The tokens of each entry from base[r] on, joined with what `pre` holds of those before: per row its sum relative to m
+// (fp32 [dl]), and m, l, l of the rounded probabilities (float4).  Workspace as launch_latent_decode.
+cudaError_t launch_latent_decode_own(const LatentDecodeArgs &a, const int32_t *base, void *pre_ml, float *pre, cudaStream_t st);
 size_t latent_shared_workspace(int64_t batch, int64_t groups, int32_t L, int32_t h, int32_t dl);
 cudaError_t launch_latent_decode_shared(const LatentDecodeArgs &a, const SharedGroups &g, cudaStream_t st);
 

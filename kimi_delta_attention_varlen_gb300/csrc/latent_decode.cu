@@ -139,7 +139,8 @@ __device__ __noinline__ float4 set_aside(uint32_t tl, float *sums, float (*kept)
     return l;
 }
 
-template <int DL, int N>
+// Shared: the tokens behind a prefix (whose part, computed before, joins in at the end).
+template <int DL, int N, bool Shared>
 __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, const __grid_constant__ Maps maps)
 {
     using C = Cfg<DL, N>;
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
     __shared__ int32_t not_finite;          // segments (from 1) of the last value that was taken out
     __shared__ float corr[2][N], linv[N];  // corr: by parity of the tile, so that a late reader keeps its own
     __shared__ float kept[3][N];           // set aside: maximum that it is relative to, l, lr
+    float *const pinv = kept[2];           // of the prefix's part, when nothing is aside any more
     __shared__ int64_t sums[kThreads / 32];
     __shared__ Edge edge[2];
     const int tid = threadIdx.x, lane = tid & 31;
@@ -172,18 +174,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
     before_next();
     after_previous();
     if (tid == 0) {
-        if (cta == 0) *p.status = 0;
+        if (!Shared && cta == 0) *p.status = 0;
         p.item0[cta] = p.item1[cta] = -1;
     }
-    find_share<kThreads>(p, sums, edge);
+    find_share<kThreads, Shared>(p, sums, edge);
     const uint32_t tmem = tmem_base;
     constexpr uint32_t kColS = 256;
 
     const int32_t total = static_cast<int32_t>(edge[1].tiles_before - edge[0].tiles_before);
-    Walk w{};
+    WalkOf<Shared> w{};
     if (total > 0) {
         w.r = edge[0].r;
-        w.load(p.a);
+        w.load(p);
         w.group = edge[0].group;
         w.tile = edge[0].tile;
     }
@@ -203,10 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
         const int part = warp == 0 ? 0 : 1, u0 = part * (C::PAIRS / 2), u1 = u0 + C::PAIRS / 2;
         const int32_t br = p.box_rows, page = static_cast<int32_t>(p.a.page);
         // page (an out-of-range coordinate, read as zeros, where the number is invalid) and row of chunk `lane`
-        auto lookup = [&](const Walk &x, int32_t *pg, int32_t *row) {
-            const int32_t t = x.tile * T + lane * br;
+        auto lookup = [&](const WalkOf<Shared> &x, int32_t *pg, int32_t *row) {
+            const int32_t t = x.token(x.tile) + lane * br;
             *pg = 0, *row = 0;
-            if (lane * br < T && t < x.n) {
+            if (lane * br < T && lane * br < x.n - x.token(x.tile)) {
                 const int32_t e = p.a.block_table[x.slot * p.a.table_stride + t / page];
                 *pg = e >= 0 && e < p.a.cache.n_rows ? e : static_cast<int32_t>(p.a.cache.n_rows);
                 *row = t % page;
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
         if (total > 0) lookup(w, &pg, &row);
         bool ok = true;  // the same in every lane
         for (; i < total && ok; ++i) {
-            Walk nx = w;
+            WalkOf<Shared> nx = w;
             nx.next(p);
             int32_t pg_next = 0, row_next = 0;
             if (i + 1 < total) lookup(nx, &pg_next, &row_next);
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                 __syncwarp();
                 ++segs;
             }
-            const int32_t valid = w.n - w.tile * T < T ? w.n - w.tile * T : T;
+            const int32_t left = w.n - w.token(w.tile), valid = left < T ? left : T;
             const int32_t chunks = (valid + br - 1) / br;
             for (int u = u0; u < u1 && ok; ++u) {
                 const int k = i * C::PAIRS + u, s = k % C::RING;
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
             }
             wait(&bar.s[i & 1], (i >> 1) & 1);
             tc::fence_after_sync();
-            const int32_t t0 = w.tile * T;
+            const int32_t t0 = w.token(w.tile);
             uint32_t pk[2][T / 8];
             float z[2][T / 4];  // rows g and g + 8 of this warp; columns 8 j + 2 t, + 1
             bool grew = false;
@@ -537,14 +539,25 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                         sum_r += __shfl_xor_sync(0xffffffffu, sum_r, 2);
                         const int row = 16 * quad + 8 * e + g, rr = w.group * N + row;
                         if (t == 0) {
-                            linv[row] = inverse(sum_r);
+                            if (Shared && whole) {
+                                float f = 1.f, fy = 0.f, top = m[e];
+                                if (w.base > 0 && rr < p.rows) {
+                                    const float4 ml = p.pre_ml[w.r * p.rows + rr];
+                                    top = fmaxf(m[e], ml.x);
+                                    f = rebase(m[e], top), fy = rebase(ml.x, top);
+                                    sum = sum * f + ml.y * fy, sum_r = sum_r * f + ml.z * fy, m[e] = top;
+                                }
+                                linv[row] = f * inverse(sum_r), pinv[row] = fy * inverse(sum_r);
+                            } else {
+                                linv[row] = inverse(sum_r);
+                            }
                             if (!whole) p.ml[part * N + row] = make_float4(m[e], sum, sum_r, 0.f);
                             else if (p.a.lse != nullptr && rr < p.rows)
                                 p.a.lse[w.r * p.rows + rr] = log_sum(m[e], sum);
                         }
                     }
                 }
-                if (!whole && tid == 128) (slot_out ? p.item1 : p.item0)[cta] = static_cast<int32_t>(w.r * p.groups + w.group);
+                if (!whole && tid == 128) (slot_out ? p.item1 : p.item0)[cta] = static_cast<int32_t>(w.r * p.rows + w.group * N);
                 wait(&bar.o, (passes - 1) & 1);
                 tc::fence_after_sync();
                 soft_any(false);  // linv is complete
@@ -558,8 +571,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                     tc::wait_ld();
                     const int mt = c0 / N, row0 = c0 % N;
                     if (taken) {  // draft tokens' values that were taken out, to the rows that see them
-                        const int32_t last = min(w.n, (w.tile + 1) * T);
-                        for (int32_t tok = max(w.n - (p.a.L - 1), tile0 * T); tok < last; ++tok) {
+                        const int32_t last = min(w.n, w.token(w.tile + 1));
+                        for (int32_t tok = max(w.n - (p.a.L - 1), w.token(tile0)); tok < last; ++tok) {
                             const int32_t e = p.a.block_table[w.slot * p.a.table_stride + tok / p.a.page];
                             if (e < 0 || e >= p.a.cache.n_rows) continue;
                             const float x = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.a.cache.data)[
@@ -577,7 +590,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                                              (w.r * p.rows + w.group * N + row0) * DL + mt * 128 + dim;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            if (row0 + e < valid) out[e * DL] = __float2bfloat16_rn(__uint_as_float(o[e]) * linv[row0 + e]);
+                            if (row0 + e < valid) {
+                                float y = __uint_as_float(o[e]) * linv[row0 + e];
+                                if (Shared && w.base > 0)
+                                    y = fmaf(p.pre[(w.r * p.rows + w.group * N + row0 + e) * DL + mt * 128 + dim], pinv[row0 + e], y);
+                                out[e * DL] = __float2bfloat16_rn(y);
+                            }
                     } else {
                         float *out = p.part + (part * N + row0) * DL + mt * 128 + dim;
 #pragma unroll
@@ -599,20 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
 
 int rows_per_group(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-// Box of 64 columns x `rows` rows of a bf16 matrix [n2][n1][n0], strides in elements, 128-byte swizzle.
-bool encode(CUtensorMap *m, const void *base, int64_t n0, int64_t n1, int64_t n2, int64_t s1, int64_t s2, int rows)
-{
-    const PFN_cuTensorMapEncodeTiled_v12000 fn = prefill::tensor_map_encoder();
-    if (fn == nullptr) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(n0), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1}, elem[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, elem,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int DL, int N> cudaError_t launch(Params p, cudaStream_t st)
+template <int DL, int N, bool Shared> cudaError_t launch(Params p, cudaStream_t st)
 {
     using C = Cfg<DL, N>;
     const int grid = static_cast<int>(sm_count());
@@ -628,12 +633,12 @@ template <int DL, int N> cudaError_t launch(Params p, cudaStream_t st)
     if (!encode(&maps.q, p.a.q, C::D, q_rows, 1, C::D, q_rows * C::D, N) ||
         !encode(&maps.cache, p.a.cache.data, C::D, p.a.page, p.a.cache.n_rows, C::D, pitch, p.box_rows))
         return cudaErrorInvalidValue;
-    auto kern = latent_decode_kernel<DL, N>;
+    auto kern = latent_decode_kernel<DL, N, Shared>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     // the join keeps the main kernel's split between shared memory and L1 cache: changing it between kernels that
     // follow each other costs microseconds
-    auto join = latent_join_kernel<DL, N>;
+    auto join = latent_join_kernel<DL, N, Shared ? kOwn : kPlain>;
     if ((e = cudaFuncSetAttribute(join, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
         return e;
     if ((e = launch_overlapped(kern, dim3(grid), dim3(kThreads), C::SMEM, st, p, maps)) != cudaSuccess) return e;
@@ -649,18 +654,35 @@ size_t latent_decode_workspace(int64_t batch, int32_t L, int32_t h, int32_t dl)
     return up256(256 + 8 * grid) + 2 * grid * n * (16 + static_cast<size_t>(dl) * 4);
 }
 
+namespace {
+template <bool Shared> cudaError_t dispatch(Params p, cudaStream_t st)
+{
+    p.rows = p.a.L * p.a.h;
+    p.scale_log2 = p.a.scale * kLog2e;
+    const int n = rows_per_group(p.rows);
+    p.box_rows = T;  // the largest power of two that divides the page, at most a tile
+    while (p.a.page % p.box_rows != 0) p.box_rows >>= 1;
+    if (p.a.dl == 512)
+        return n == 16 ? launch<512, 16, Shared>(p, st) : n == 32 ? launch<512, 32, Shared>(p, st) : launch<512, 64, Shared>(p, st);
+    return n == 16 ? launch<256, 16, Shared>(p, st) : n == 32 ? launch<256, 32, Shared>(p, st) : launch<256, 64, Shared>(p, st);
+}
+}  // namespace
+
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t st)
 {
     Params p{};
     p.a = a;
-    p.rows = a.L * a.h;
-    p.scale_log2 = a.scale * kLog2e;
-    const int n = rows_per_group(p.rows);
-    p.box_rows = T;  // the largest power of two that divides the page, at most a tile
-    while (a.page % p.box_rows != 0) p.box_rows >>= 1;
-    if (a.dl == 512)
-        return n == 16 ? launch<512, 16>(p, st) : n == 32 ? launch<512, 32>(p, st) : launch<512, 64>(p, st);
-    return n == 16 ? launch<256, 16>(p, st) : n == 32 ? launch<256, 32>(p, st) : launch<256, 64>(p, st);
+    return dispatch<false>(p, st);
+}
+
+cudaError_t launch_latent_decode_own(const LatentDecodeArgs &a, const int32_t *base, void *pre_ml, float *pre, cudaStream_t st)
+{
+    Params p{};
+    p.a = a;
+    p.base = base;
+    p.pre_ml = static_cast<float4 *>(pre_ml);
+    p.pre = pre;
+    return dispatch<true>(p, st);
 }
 
 }  // namespace kda

@@ -29,9 +29,15 @@ struct Params {
     LatentDecodeArgs a;
     int32_t rows, groups, box_rows;  // L * h; row groups; rows of a TMA box (divides the page size)
     float scale_log2;
-    int32_t *status, *item0, *item1;  // [grid]: item whose part is in slot 0 / 1 of the CTA, or -1
+    int32_t *status, *item0, *item1;  // [grid]: first row (of all entries' rows) of the item whose part is in slot 0 / 1 of the CTA, or -1
     float4 *ml;                       // [grid][2][N]: m, l, l of the rounded probabilities
     float *part;                      // [grid][2][N][dl]; also what a segment sets aside, in its slot
+    // Prefixes that groups share: what was computed for them, of all entries' rows, and the token that each entry's own
+    // part begins with.
+    const int32_t *base;              // [batch]
+    float4 *pre_ml;                   // [rows of all entries]: m, l, l of the rounded probabilities
+    float *pre;                       // [rows of all entries][dl], relative to m
+    int32_t *item_rows;               // [grid]: rows of the item in slot 1 (of the prefixes' items)
 };
 
 __device__ __forceinline__ int64_t slot_of(const LatentDecodeArgs &a, int64_t r)
@@ -61,17 +67,32 @@ struct Edge {
     int32_t group, tile;
 };
 
-// Position on the line of tiles.
-struct Walk {
-    int64_t r, slot;
-    int32_t group, tile, n, tiles;
+// Token that entry r's line begins with, and the end of its tokens.
+template <bool Shared> __device__ __forceinline__ int32_t base_of(const Params &p, int64_t r)
+{
+    if (!Shared) return 0;
+    const int32_t b = p.base[r];  // anything where the groups' offsets break their contract
+    return b < 0 || b > p.a.width * p.a.page ? 0 : b;
+}
+template <bool Shared> __device__ __forceinline__ int32_t end_of(const Params &p, int64_t slot, int32_t base)
+{
+    const int32_t n = length_of(p.a, slot);
+    return Shared && n < base ? base : n;
+}
 
-    __device__ void load(const LatentDecodeArgs &a)
+// Position on the line of tiles (Shared: of the tokens behind a shared prefix).
+template <bool Shared> struct WalkOf {
+    int64_t r, slot;
+    int32_t group, tile, base, n, tiles;
+
+    __device__ void load(const Params &p)
     {
-        slot = slot_of(a, r);
-        n = length_of(a, slot);
-        tiles = tiles_of(n);
+        slot = slot_of(p.a, r);
+        base = base_of<Shared>(p, r);
+        n = end_of<Shared>(p, slot, base);
+        tiles = tiles_of(n - base);
     }
+    __device__ int32_t token(int32_t t) const { return Shared ? base + t * T : t * T; }  // a tile's first
     __device__ bool first() const { return tile == 0; }
     __device__ bool last() const { return tile + 1 == tiles; }
     // the first query token of the request sees this tile alone
@@ -82,9 +103,10 @@ struct Walk {
         tile = 0;
         if (++group < p.groups) return;
         group = 0;
-        if (++r < p.a.batch) load(p.a);
+        if (++r < p.a.batch) load(p);
     }
 };
+using Walk = WalkOf<false>;
 
 // 32 columns of 16 lanes: registers 4 j + {0, 1} are row lane / 4, columns 8 j + 2 (lane % 4) + {0, 1}, and
 // 4 j + {2, 3} the same columns of row lane / 4 + 8.
@@ -122,16 +144,20 @@ __device__ __forceinline__ bool elect_one()
 
 // The ends edge[0], edge[1] of this CTA's share of the line.  By all threads (Threads of them); `sums` holds a word a warp.
 // Synchronises the CTA.
-template <int Threads>
+template <int Threads, bool Shared = false>
 __device__ __forceinline__ void find_share(const Params &p, int64_t *sums, Edge *edge)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+    auto tiles_at = [&](int64_t r) {
+        const int32_t base = base_of<Shared>(p, r);
+        return tiles_of(end_of<Shared>(p, slot_of(p.a, r), base) - base);
+    };
     // A share is [w0, w1) of the line, on which a (request, group) takes its tiles and kItemUnits more: the
     // work that comes with it whatever its length (queries, first tile's latency, epilogue).
     const int64_t per = (p.a.batch + Threads - 1) / Threads, r_lo = per * tid;
     const int64_t r_hi = r_lo + per < p.a.batch ? r_lo + per : p.a.batch;
     int64_t mine = 0;  // units of this thread's slice of the requests, of one group
-    for (int64_t r = r_lo; r < r_hi; ++r) mine += tiles_of(length_of(p.a, slot_of(p.a, r))) + kItemUnits;
+    for (int64_t r = r_lo; r < r_hi; ++r) mine += tiles_at(r) + kItemUnits;
     int64_t scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -160,7 +186,7 @@ __device__ __forceinline__ void find_share(const Params &p, int64_t *sums, Edge 
             int64_t left = at - before, r = r_lo;
             int32_t tiles;
             for (;; ++r) {
-                tiles = tiles_of(length_of(p.a, slot_of(p.a, r)));
+                tiles = tiles_at(r);
                 const int64_t u = static_cast<int64_t>(tiles + kItemUnits) * p.groups;
                 if (left < u) break;
                 left -= u;
@@ -180,7 +206,12 @@ __device__ __forceinline__ void find_share(const Params &p, int64_t *sums, Edge 
 // whole CTA (one long request: 32 rows of 152 parts).
 constexpr int kFewParts = 8;
 
-template <int DL, int N>
+//
+// kOwn: the items are entries' own tokens behind a prefix, what was computed for that joins in; kPrefix: the items are
+// blocks of rows of the prefixes, and what comes out is not normalised.
+enum JoinForm { kPlain, kOwn, kPrefix };
+
+template <int DL, int N, JoinForm Form = kPlain>
 __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shares)
 {
     constexpr int kLanes = DL / 4, kSubs = 256 / kLanes, kAhead = 8;  // a row's float4s; parts at once; in flight per thread
@@ -190,7 +221,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
     __shared__ float sum[2], top;
     __shared__ int32_t listed, units;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int32_t per = p.rows < N ? p.rows : N;
+    const int32_t per = Form != kPrefix && p.rows < N ? p.rows : N;
     before_next();
     after_previous();
     int32_t *const head_of = before, *const more_of = reinterpret_cast<int32_t *>(weight);  // until they are needed
@@ -235,16 +266,36 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
             else hi = mid;
         }
         const int32_t c = first[lo], parts = parts_of[lo], item = p.item1[c];
-        const int64_t r = item / p.groups;
-        const int32_t row0 = item % p.groups * N;  // the group's first row
+        const int32_t left = Form == kPrefix ? p.item_rows[c] : p.rows - item % p.rows;  // rows from the item's first on
         auto at = [&](int32_t j, int32_t row) { return (static_cast<int64_t>(2) * (c + j) + (j == 0 ? 1 : 0)) * N + row; };
-        auto store = [&](int32_t row, int32_t d, float4 o, float inv) {
-            reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.a.out) + (r * p.rows + row0 + row) * DL)[d] =
-                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        // a row's sum o relative to m, with the sums l and lr
+        auto store = [&](int32_t row, int32_t d, float4 o, float m, float l, float lr) {
+            const int64_t at = item + row;
+            if (Form == kPrefix) {
+                if (lr == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);  // 0 times what is not finite
+                reinterpret_cast<float4 *>(p.pre + at * DL)[d] = o;
+                if (d == 0) p.pre_ml[at] = make_float4(m, l, lr, 0.f);
+                return;
+            }
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            float f = 1.f, fy = 0.f;
+            if (Form == kOwn && p.base[at / p.rows] > 0) {
+                const float4 ml = p.pre_ml[at];
+                const float top = fmaxf(m, ml.x);
+                f = rebase(m, top), fy = rebase(ml.x, top);
+                l = l * f + ml.y * fy, lr = lr * f + ml.z * fy, m = top;
+                y = reinterpret_cast<const float4 *>(p.pre + at * DL)[d];
+            }
+            const float inv = inverse(lr);
+            f *= inv, fy *= inv;
+            reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.a.out) + at * DL)[d] =
+                Form == kOwn ? make_uint2(pack_bf16x2(o.x * f + y.x * fy, o.y * f + y.y * fy), pack_bf16x2(o.z * f + y.z * fy, o.w * f + y.w * fy))
+                             : make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+            if (d == 0 && p.a.lse != nullptr) p.a.lse[at] = log_sum(m, l);
         };
         if (parts <= kFewParts) {
             const int32_t row = (unit - before[lo]) * 8 + warp;
-            if (row >= per || row0 + row >= p.rows) continue;
+            if (row >= per || row >= left) continue;
             float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
             if (lane < parts) ml = p.ml[at(lane, row)];
             float m = ml.x;
@@ -259,7 +310,6 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
                 lr += __shfl_xor_sync(0xffffffffu, lr, o);
             }
             l = __shfl_sync(0xffffffffu, l, 0), lr = __shfl_sync(0xffffffffu, lr, 0);
-            const float inv = inverse(lr);
             float4 o[kLanes / 32];
 #pragma unroll
             for (int q = 0; q < kLanes / 32; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -274,12 +324,11 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
                 }
             }
 #pragma unroll
-            for (int q = 0; q < kLanes / 32; ++q) store(row, lane + 32 * q, o[q], inv);
-            if (lane == 0 && p.a.lse != nullptr) p.a.lse[r * p.rows + row0 + row] = log_sum(m, l);
+            for (int q = 0; q < kLanes / 32; ++q) store(row, lane + 32 * q, o[q], m, l, lr);
             continue;
         }
         const int32_t row = unit - before[lo], sub = tid / kLanes, d = tid % kLanes;
-        if (row0 + row >= p.rows) continue;
+        if (row >= left) continue;
         if (warp == 0) {
             float m = -INFINITY, l = 0.f, lr = 0.f;
             for (int32_t j = lane; j < parts; j += 32) m = fmaxf(m, p.ml[at(j, row)].x);
@@ -322,12 +371,23 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
                 const float4 y = acc[q][d];
                 o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
             }
-            store(row, d, o, inverse(sum[1]));
-            if (d == 0 && p.a.lse != nullptr)
-                p.a.lse[r * p.rows + row0 + row] = log_sum(top, sum[0]);
+            store(row, d, o, top, sum[0], sum[1]);
         }
         __syncthreads();  // weight, sum and acc may be written again
     }
+}
+
+// Box of 64 columns x `rows` rows of a bf16 matrix [n2][n1][n0], strides in elements, 128-byte swizzle.
+inline bool encode(CUtensorMap *m, const void *base, int64_t n0, int64_t n1, int64_t n2, int64_t s1, int64_t s2, int rows)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = prefill::tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(n0), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1}, elem[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
     Walk w{};
     if (total > 0) {
         w.r = edge[0].r;
-        w.load(p.a);
+        w.load(p);
         w.group = edge[0].group;
         w.tile = edge[0].tile;
     }
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
             const bool last = w.last();
             if (last || i + 1 == total) {  // the segment ends here
                 const bool whole = last && slot_out == 1;
-                if (!whole && st == 0) (slot_out ? p.item1 : p.item0)[cta] = static_cast<int32_t>(w.r * p.groups + w.group);
+                if (!whole && st == 0) (slot_out ? p.item1 : p.item0)[cta] = static_cast<int32_t>(w.r * p.rows + w.group * N);
                 finish(i, w.tile - tile0 >= kSumTiles, true, whole);
             }
             w.next(p);
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
 int rows_per_group(int64_t rows) { return rows <= 16 ? 16 : 32; }
 
 // Box of 128 bytes x `rows` rows of [n_pages][page][n0] elements, strides in bytes, 128-byte swizzle.
-bool encode(CUtensorMap *map, CUtensorMapDataType type, int cols, const char *base, int64_t n0, int64_t n1, int64_t n2, int64_t s1,
+bool encode8(CUtensorMap *map, CUtensorMapDataType type, int cols, const char *base, int64_t n0, int64_t n1, int64_t n2, int64_t s1,
             int64_t s2, int rows)
 {
     const PFN_cuTensorMapEncodeTiled_v12000 fn = prefill::tensor_map_encoder();
@@ -643,8 +643,8 @@ template <int DL, int N> cudaError_t launch(Params p, cudaStream_t st)
     Maps maps;
     const char *data = static_cast<const char *>(p.a.cache.data);
     const int64_t P = p.a.page, pages = p.a.cache.n_rows, pitch = p.a.cache.row_stride;
-    if (!encode(&maps.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 128, data, DL, P, pages, DL, pitch, p.box_rows) ||
-        !encode(&maps.rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, data + P * DL, 64, P, pages, 128, pitch, p.box_rows))
+    if (!encode8(&maps.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 128, data, DL, P, pages, DL, pitch, p.box_rows) ||
+        !encode8(&maps.rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, data + P * DL, 64, P, pages, 128, pitch, p.box_rows))
         return cudaErrorInvalidValue;
     auto kern = latent_decode8_kernel<DL, N>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
