@@ -568,8 +568,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                 for (int c0 = 0; c0 < C::PAIRS * N; c0 += 16) {
                     uint32_t o[16];
                     tc::ld16(tl + c0, o);
-                    tc::wait_ld();
                     const int mt = c0 / N, row0 = c0 % N;
+                    float y[Shared ? 16 : 1];  // the prefix's part: all loads before the first store
+                    const bool prefixed = Shared && whole && w.base > 0;
+                    if constexpr (Shared) {
+                        const float *pre = p.pre + (w.r * p.rows + w.group * N + row0) * DL + mt * 128 + dim;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) y[e] = prefixed && row0 + e < valid ? pre[e * DL] * pinv[row0 + e] : 0.f;
+                    }
+                    tc::wait_ld();
                     if (taken) {  // draft tokens' values that were taken out, to the rows that see them
                         const int32_t last = min(w.n, w.token(w.tile + 1));
                         for (int32_t tok = max(w.n - (p.a.L - 1), w.token(tile0)); tok < last; ++tok) {
@@ -590,12 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                                              (w.r * p.rows + w.group * N + row0) * DL + mt * 128 + dim;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            if (row0 + e < valid) {
-                                float y = __uint_as_float(o[e]) * linv[row0 + e];
-                                if (Shared && w.base > 0)
-                                    y = fmaf(p.pre[(w.r * p.rows + w.group * N + row0 + e) * DL + mt * 128 + dim], pinv[row0 + e], y);
-                                out[e * DL] = __float2bfloat16_rn(y);
-                            }
+                            if (row0 + e < valid)
+                                out[e * DL] = __float2bfloat16_rn(__uint_as_float(o[e]) * linv[row0 + e] + (Shared ? y[Shared ? e : 0] : 0.f));
                     } else {
                         float *out = p.part + (part * N + row0) * DL + mt * 128 + dim;
 #pragma unroll
