@@ -572,9 +572,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                     float y[Shared ? 16 : 1];  // the prefix's part: all loads before the first store
                     const bool prefixed = Shared && whole && w.base > 0;
                     if constexpr (Shared) {
-                        const float *pre = p.pre + (w.r * p.rows + w.group * N + row0) * DL + mt * 128 + dim;
+                        if (prefixed) {  // (of the last row in place of those behind it: loads that wait for nothing)
+                            const float *pre = p.pre + (w.r * p.rows + w.group * N) * DL + mt * 128 + dim;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) y[e] = prefixed && row0 + e < valid ? pre[e * DL] * pinv[row0 + e] : 0.f;
+                            for (int e = 0; e < 16; ++e) y[e] = pre[min(row0 + e, valid - 1) * DL];
+                        }
                     }
                     tc::wait_ld();
                     if (taken) {  // draft tokens' values that were taken out, to the rows that see them
@@ -597,8 +599,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                                              (w.r * p.rows + w.group * N + row0) * DL + mt * 128 + dim;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            if (row0 + e < valid)
-                                out[e * DL] = __float2bfloat16_rn(__uint_as_float(o[e]) * linv[row0 + e] + (Shared ? y[Shared ? e : 0] : 0.f));
+                            if (row0 + e < valid) {
+                                float x = __uint_as_float(o[e]) * linv[row0 + e];
+                                if (prefixed) x = fmaf(y[Shared ? e : 0], pinv[row0 + e], x);
+                                out[e * DL] = __float2bfloat16_rn(x);
+                            }
                     } else {
                         float *out = p.part + (part * N + row0) * DL + mt * 128 + dim;
 #pragma unroll

@@ -14,7 +14,7 @@
 namespace kda {
 namespace {
 
-constexpr int kWarps = 8, kRope = 64;
+constexpr int kWarps = 4, kRope = 64;
 constexpr int kLowest = -64;  // of a token's exponent
 
 // Where token `pos` of a page lies, in bytes from the page's start.
@@ -41,11 +41,7 @@ __device__ __forceinline__ uint32_t finite_magnitude(float x)
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 
-__device__ __forceinline__ uint32_t codes2(float a, float b)  // infinities as NaN: e4m3 has none
-{
-    const float2 v = make_float2(fabsf(a) < INFINITY ? a : NAN, fabsf(b) < INFINITY ? b : NAN);
-    return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-}
+__device__ __forceinline__ uint32_t codes2(float a, float b) { return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3); }
 
 // Eight consecutive values of a row of x.
 template <typename X> __device__ __forceinline__ void load8(const X *p, float (&v)[8]);
@@ -64,48 +60,103 @@ template <> __device__ __forceinline__ void load8<float>(const float *p, float (
     for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
 }
 
-template <typename X, int DL>
+// Of a CTA's rows: where each one's token is. By warp 0: the entry of the CTA's first row is looked for by the whole warp, the
+// others follow from it (rows of one entry lie together), a row a lane.
+struct Spot {
+    int32_t page, slot;  // page: -1 where there is no such token, -2 where the row is no entry's
+};
+
+template <int Rows, bool Read>
+__device__ __forceinline__ void find_spots(const LatentRowsArgs &a, int64_t row0, Spot *spots)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t begin = a.cu[0], behind = a.cu[a.count];
+    const int64_t row = row0 + lane;
+    const int64_t from = row0 < begin ? begin : row0;
+    Spot x{-2, 0};
+    if (from < behind && from < row0 + Rows) {
+        int64_t i = entry_of(a.cu, a.count, from);
+        if (lane < Rows && row >= begin && row < behind && row < a.total) {
+            int64_t end = a.cu[i + 1];
+            while (row >= end && i + 1 < a.count) end = a.cu[++i + 1];
+            if (row < end) {
+                x.page = -1;
+                const int64_t req = load_index(a.req, a.idx_type, i);
+                if (req >= 0 && req < a.table.requests) {
+                    const int64_t n = length_of(a.table, req);
+                    const int64_t pos = Read ? row - a.cu[i] + (a.first != nullptr ? a.first[i] : 0) : n - end + row;
+                    if (pos >= 0 && pos < n) {
+                        const int32_t e = a.table.block_table[req * a.table.table_stride + pos / a.table.page_size];
+                        if (e >= 0 && e < a.table.n_pages) x = Spot{e, static_cast<int32_t>(pos % a.table.page_size)};
+                    }
+                }
+            }
+        }
+    }
+    if (lane < Rows) spots[lane] = x;
+}
+
+template <typename X, int DL, int Per>
 __global__ void __launch_bounds__(32 * kWarps) append8_kernel(const X *x, LatentRowsArgs a)
 {
+    __shared__ Spot spots[kWarps * Per];
     before_next();
     after_previous();
-    const int lane = threadIdx.x & 31;
-    const int64_t tok = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (tok >= a.total || tok < a.cu[0] || tok >= a.cu[a.count]) return;
-    const X *from = x + tok * a.stride;
-    float c[DL / 256][8], r[2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kWarps * Per;
+    float c[Per][DL / 256][8], r[Per][2];
+    auto load = [&](int k) {
+        if (row0 + warp + kWarps * k >= a.total) return;
+        const X *from = x + (row0 + warp + kWarps * k) * a.stride;
 #pragma unroll
-    for (int e = 0; e < DL / 256; ++e) load8(from + 256 * e + 8 * lane, c[e]);
-    r[0] = load_as_f32(from + DL + 2 * lane), r[1] = load_as_f32(from + DL + 2 * lane + 1);
-    const int64_t i = entry_of(a.cu, a.count, tok), req = load_index(a.req, a.idx_type, i);
-    if (req < 0 || req >= a.table.requests || tok >= a.cu[i + 1]) return;
-    const int64_t pos = length_of(a.table, req) - a.cu[i + 1] + tok;
-    if (pos < 0) return;
-    const int32_t page = a.table.block_table[req * a.table.table_stride + pos / a.table.page_size];
-    if (page < 0 || page >= a.table.n_pages) return;
+        for (int e = 0; e < DL / 256; ++e) load8(from + 256 * e + 8 * lane, c[k][e]);
+        r[k][0] = load_as_f32(from + DL + 2 * lane), r[k][1] = load_as_f32(from + DL + 2 * lane + 1);
+    };
+#pragma unroll
+    for (int k = 0; k < Per; ++k) load(k);
+    if (warp == 0) find_spots<kWarps * Per, false>(a, row0, spots);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < Per; ++k) {
+        const Spot spot = spots[warp + kWarps * k];
+        if (spot.page < 0) continue;
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < DL / 256; ++e)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(c[k][e][j]) & 0x7fffffffu);
+        most = warp_max(most);
+        const bool finite = most < 0x7f800000u;  // of the latent, in every lane alike: then no value needs a look of its own
+        if (!finite) {
+            most = 0;
+#pragma unroll
+            for (int e = 0; e < DL / 256; ++e)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    most = max(most, finite_magnitude(c[k][e][j]));
+                    if (!(fabsf(c[k][e][j]) < INFINITY)) c[k][e][j] = NAN;  // e4m3 has no infinities
+                }
+            most = warp_max(most);
+        }
+        const int kc = exponent_for(most, 8, 0x600000u);  // 448 = 2^8 * 1.75
+        const int kr = exponent_for(warp_max(max(finite_magnitude(r[k][0]), finite_magnitude(r[k][1]))), 64, 0u);
+        const int exponent = max(max(kc, kr), kLowest);             // at most 120
+        const float unit = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
 
-    uint32_t most = 0;
+        const Place8 place = place8(a.table.page_size, spot.slot, DL);
+        char *to = static_cast<char *>(a.cache.data) + spot.page * a.cache.row_stride;
 #pragma unroll
-    for (int e = 0; e < DL / 256; ++e)
+        for (int e = 0; e < DL / 256; ++e) {
+            const float *v = c[k][e];
+            uint32_t w[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) most = max(most, finite_magnitude(c[e][j]));
-    const int k = exponent_for(warp_max(most), 8, 0x600000u);  // 448 = 2^8 * 1.75
-    const int kr = exponent_for(warp_max(max(finite_magnitude(r[0]), finite_magnitude(r[1]))), 64, 0u);
-    const int exponent = max(max(k, kr), kLowest);             // at most 120
-    const float unit = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
-
-    const Place8 at = place8(a.table.page_size, pos % a.table.page_size, DL);
-    char *to = static_cast<char *>(a.cache.data) + page * a.cache.row_stride;
-#pragma unroll
-    for (int e = 0; e < DL / 256; ++e) {
-        uint32_t w[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            w[j] = codes2(c[e][4 * j] * unit, c[e][4 * j + 1] * unit) | codes2(c[e][4 * j + 2] * unit, c[e][4 * j + 3] * unit) << 16;
-        *reinterpret_cast<uint2 *>(to + at.codes + 256 * e + 8 * lane) = make_uint2(w[0], w[1]);
+            for (int j = 0; j < 2; ++j)
+                w[j] = codes2(v[4 * j] * unit, v[4 * j + 1] * unit) | codes2(v[4 * j + 2] * unit, v[4 * j + 3] * unit) << 16;
+            *reinterpret_cast<uint2 *>(to + place.codes + 256 * e + 8 * lane) = make_uint2(w[0], w[1]);
+        }
+        *reinterpret_cast<uint32_t *>(to + place.rope + 4 * lane) = pack_bf16x2(r[k][0] * unit, r[k][1] * unit);
+        if (lane == 0) *reinterpret_cast<float *>(to + place.scale) = __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23);
     }
-    *reinterpret_cast<uint32_t *>(to + at.rope + 4 * lane) = pack_bf16x2(r[0] * unit, r[1] * unit);
-    if (lane == 0) *reinterpret_cast<float *>(to + at.scale) = __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23);
 }
 
 __device__ __forceinline__ uint32_t values2(uint32_t codes, float scale)  // two codes (low halfword) as bf16 values
@@ -115,71 +166,84 @@ __device__ __forceinline__ uint32_t values2(uint32_t codes, float scale)  // two
     return pack_bf16x2(v.x * scale, v.y * scale);
 }
 
-template <int DL, bool Eight>
+template <int DL, bool Eight, int Per>
 __global__ void __launch_bounds__(32 * kWarps) read_kernel(LatentRowsArgs a)
 {
+    __shared__ Spot spots[kWarps * Per];
     before_next();
     after_previous();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (row >= a.total || row < a.cu[0] || row >= a.cu[a.count]) return;
-    const int64_t i = entry_of(a.cu, a.count, row), req = load_index(a.req, a.idx_type, i);
-    if (row >= a.cu[i + 1]) return;
-    const int64_t pos = row - a.cu[i] + (a.first != nullptr ? a.first[i] : 0);
-    int32_t page = -1;
-    if (req >= 0 && req < a.table.requests && pos >= 0 && pos < length_of(a.table, req))
-        page = a.table.block_table[req * a.table.table_stride + pos / a.table.page_size];
-    const bool valid = page >= 0 && page < a.table.n_pages;
-    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.rows) + row * a.stride;
-    const int64_t slot = pos % a.table.page_size;
-    uint4 v[DL / 256];
-    uint32_t rope = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kWarps * Per;
+    if (warp == 0) find_spots<kWarps * Per, true>(a, row0, spots);
+    __syncthreads();
+    uint4 v[Per][DL / 256];  // Eight: the codes in the first half
+    uint32_t rope[Per];
+    float scale[Per];
 #pragma unroll
-    for (int e = 0; e < DL / 256; ++e) v[e] = make_uint4(0u, 0u, 0u, 0u);
-    if (valid && Eight) {
-        const char *from = static_cast<const char *>(a.cache.data) + page * a.cache.row_stride;
-        const Place8 at = place8(a.table.page_size, slot, DL);
-        uint2 w[DL / 256];
+    for (int k = 0; k < Per; ++k) {  // all loads before the first store
+        const Spot spot = spots[warp + kWarps * k];
+        rope[k] = 0, scale[k] = 0.f;
 #pragma unroll
-        for (int e = 0; e < DL / 256; ++e) w[e] = *reinterpret_cast<const uint2 *>(from + at.codes + 256 * e + 8 * lane);
-        const uint32_t r = *reinterpret_cast<const uint32_t *>(from + at.rope + 4 * lane);
-        const float scale = *reinterpret_cast<const float *>(from + at.scale);
+        for (int e = 0; e < DL / 256; ++e) v[k][e] = make_uint4(0u, 0u, 0u, 0u);
+        if (spot.page < 0) continue;
+        if (Eight) {
+            const char *from = static_cast<const char *>(a.cache.data) + spot.page * a.cache.row_stride;
+            const Place8 place = place8(a.table.page_size, spot.slot, DL);
 #pragma unroll
-        for (int e = 0; e < DL / 256; ++e)
-            v[e] = make_uint4(values2(w[e].x, scale), values2(w[e].x >> 16, scale), values2(w[e].y, scale), values2(w[e].y >> 16, scale));
-        rope = pack_bf16x2(bf16_lo(r) * scale, bf16_hi(r) * scale);
-    } else if (valid) {
-        const __nv_bfloat16 *from = static_cast<const __nv_bfloat16 *>(a.cache.data) + page * a.cache.row_stride + slot * (DL + kRope);
+            for (int e = 0; e < DL / 256; ++e) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(from + place.codes + 256 * e + 8 * lane);
+                v[k][e].x = w.x, v[k][e].y = w.y;
+            }
+            rope[k] = *reinterpret_cast<const uint32_t *>(from + place.rope + 4 * lane);
+            scale[k] = *reinterpret_cast<const float *>(from + place.scale);
+        } else {
+            const __nv_bfloat16 *from = static_cast<const __nv_bfloat16 *>(a.cache.data) + spot.page * a.cache.row_stride +
+                                        static_cast<int64_t>(spot.slot) * (DL + kRope);
 #pragma unroll
-        for (int e = 0; e < DL / 256; ++e) v[e] = ld_v4(from + 256 * e + 8 * lane);
-        rope = *reinterpret_cast<const uint32_t *>(from + DL + 2 * lane);
+            for (int e = 0; e < DL / 256; ++e) v[k][e] = ld_v4(from + 256 * e + 8 * lane);
+            rope[k] = *reinterpret_cast<const uint32_t *>(from + DL + 2 * lane);
+        }
     }
 #pragma unroll
-    for (int e = 0; e < DL / 256; ++e) *reinterpret_cast<uint4 *>(to + 256 * e + 8 * lane) = v[e];
-    *reinterpret_cast<uint32_t *>(to + DL + 2 * lane) = rope;
+    for (int k = 0; k < Per; ++k) {
+        if (spots[warp + kWarps * k].page == -2) continue;
+        __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.rows) + (row0 + warp + kWarps * k) * a.stride;
+#pragma unroll
+        for (int e = 0; e < DL / 256; ++e) {
+            const uint4 w = v[k][e];
+            *reinterpret_cast<uint4 *>(to + 256 * e + 8 * lane) =
+                Eight ? make_uint4(values2(w.x, scale[k]), values2(w.x >> 16, scale[k]), values2(w.y, scale[k]), values2(w.y >> 16, scale[k])) : w;
+        }
+        *reinterpret_cast<uint32_t *>(to + DL + 2 * lane) = Eight ? pack_bf16x2(bf16_lo(rope[k]) * scale[k], bf16_hi(rope[k]) * scale[k]) : rope[k];
+    }
 }
 
-dim3 grid_of(int64_t total) { return dim3(static_cast<unsigned>((total + kWarps - 1) / kWarps)); }
+// Rows a warp (kWarps times that many are at most 32): 73,364 tokens written in 34.8 us with 2, 38.8 with 4 and 35.4 with 1, read
+// in 24.1 with 8, 24.4 with 4 and 26.6 with 1.
+constexpr int kPerAppend = 2, kPerRead = 4;
+
+dim3 grid_of(int64_t total, int per) { return dim3(static_cast<unsigned>((total + kWarps * per - 1) / (kWarps * per))); }
 
 }  // namespace
 
 cudaError_t launch_latent_append8(const LatentRowsArgs &a, cudaStream_t st)
 {
-    const dim3 grid = grid_of(a.total), block(32 * kWarps);
+    const dim3 grid = grid_of(a.total, kPerAppend), block(32 * kWarps);
     if (a.dtype == KDA_F32) {
         const float *x = static_cast<const float *>(a.rows);
-        return launch_overlapped(a.dl == 512 ? append8_kernel<float, 512> : append8_kernel<float, 256>, grid, block, 0, st, x, a);
+        return launch_overlapped(a.dl == 512 ? append8_kernel<float, 512, kPerAppend> : append8_kernel<float, 256, kPerAppend>, grid, block, 0, st, x, a);
     }
     const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.rows);
-    return launch_overlapped(a.dl == 512 ? append8_kernel<__nv_bfloat16, 512> : append8_kernel<__nv_bfloat16, 256>, grid, block, 0, st, x, a);
+    return launch_overlapped(a.dl == 512 ? append8_kernel<__nv_bfloat16, 512, kPerAppend> : append8_kernel<__nv_bfloat16, 256, kPerAppend>, grid,
+                             block, 0, st, x, a);
 }
 
 cudaError_t launch_latent_read(const LatentRowsArgs &a, cudaStream_t st)
 {
-    const dim3 grid = grid_of(a.total), block(32 * kWarps);
+    const dim3 grid = grid_of(a.total, kPerRead), block(32 * kWarps);
     if (a.cache.dtype == KDA_U8)
-        return launch_overlapped(a.dl == 512 ? read_kernel<512, true> : read_kernel<256, true>, grid, block, 0, st, a);
-    return launch_overlapped(a.dl == 512 ? read_kernel<512, false> : read_kernel<256, false>, grid, block, 0, st, a);
+        return launch_overlapped(a.dl == 512 ? read_kernel<512, true, kPerRead> : read_kernel<256, true, kPerRead>, grid, block, 0, st, a);
+    return launch_overlapped(a.dl == 512 ? read_kernel<512, false, kPerRead> : read_kernel<256, false, kPerRead>, grid, block, 0, st, a);
 }
 
 }  // namespace kda

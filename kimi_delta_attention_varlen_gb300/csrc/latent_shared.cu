@@ -72,44 +72,63 @@ __device__ __forceinline__ void entries_of(const SharedParams &s, int64_t g, int
     if (*to < *from) *to = *from;
 }
 
-// One CTA a group (in turn).  The entries outside all groups are the first CTA's.
-__global__ void __launch_bounds__(128) plan_kernel(SharedParams s)
+// What a tile of 64 tokens takes a CTA, in cycles: with an entry's own rows (in groups of 16, 32 or 64), and with 64 rows of a
+// prefix; and what the prefixes' launches and the joins take the GPU besides.
+constexpr int64_t kOwnTile = 3100, kPrefixTile = 3000, kExtra = 24000;
+
+// By one CTA, a group a warp.  Sharing pays where the prefixes' tiles cost less than the entries' own would by more than the
+// launches: with 32 heads two requests or more to a block of rows, from some 10 us of own tiles on.  Where it does not (few tokens,
+// or entries that have 64 rows already, which the tensor cores bound in either form), nothing is shared.
+__global__ void __launch_bounds__(1024) plan_kernel(SharedParams s, int32_t ctas)
 {
-    __shared__ uint64_t best;
+    __shared__ int64_t saved[32];
     before_next();
     after_previous();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const LatentDecodeArgs &a = s.p.a;
-    if (blockIdx.x == 0) {
-        if (tid == 0) *s.p.status = 0;  // of all the kernels of the call
-        const int64_t first = bound(s.g.cu[0], a.batch), last = bound(s.g.cu[s.g.groups], a.batch);
-        for (int64_t r = tid; r < a.batch; r += blockDim.x)
-            if (r < first || r >= last) s.plan.base[r] = 0;
-    }
-    for (int64_t g = blockIdx.x; g < s.g.groups; g += gridDim.x) {
+    if (tid == 0) *s.p.status = 0;  // of all the kernels of the call
+    const int64_t own = s.p.rows <= 16 ? 16 : s.p.rows <= 32 ? 32 : 64;
+    int64_t mine = 0;
+    for (int64_t g = warp; g < s.g.groups; g += 32) {
         int64_t from, to;
         entries_of(s, g, &from, &to);
-        __syncthreads();
-        if (tid == 0) best = 0;
-        __syncthreads();
-        uint64_t mine = 0;  // the longest member, of these the first
-        for (int64_t r = from + tid; r < to; r += blockDim.x) {
-            const uint64_t n = static_cast<uint64_t>(length_of(a, slot_of(a, r)));
-            const uint64_t key = n << 32 | static_cast<uint32_t>(0x7fffffff - (r - from));
-            mine = key > mine ? key : mine;
+        int64_t best = -1;  // the longest member, of these the first
+        for (int64_t r = from + lane; r < to; r += 32) {
+            const int64_t key = static_cast<int64_t>(length_of(a, slot_of(a, r))) << 31 | (0x7fffffff - (r - from));
+            best = key > best ? key : best;
         }
-        atomicMax(reinterpret_cast<unsigned long long *>(&best), static_cast<unsigned long long>(mine));
-        __syncthreads();
-        const int64_t n = static_cast<int64_t>(best >> 32);
-        const int64_t told = s.g.shared[g];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const int64_t x = __shfl_xor_sync(0xffffffffu, best, o);
+            best = x > best ? x : best;
+        }
         // whole pages; alone, a member shares nothing
-        const int64_t b = to - from < 2 ? 0 : bound(told, n) / a.page * a.page;
-        if (tid == 0) {
+        const int64_t b = to - from < 2 ? 0 : bound(s.g.shared[g], best >> 31) / a.page * a.page;
+        if (lane == 0) {
             s.plan.tokens[g] = static_cast<int32_t>(b);
-            s.plan.slot[g] = b > 0 ? static_cast<int32_t>(slot_of(a, from + (0x7fffffff - static_cast<int64_t>(best & 0xffffffffu)))) : 0;
+            s.plan.slot[g] = b > 0 ? static_cast<int32_t>(slot_of(a, from + (0x7fffffff - (best & 0x7fffffff)))) : 0;
+            const int64_t rows = (to - from) * s.p.rows;
+            mine += (b + T - 1) / T * ((to - from) * ((s.p.rows + own - 1) / own) * kOwnTile - (rows + N - 1) / N * kPrefixTile);
         }
-        for (int64_t r = from + tid; r < to; r += blockDim.x) s.plan.base[r] = static_cast<int32_t>(b);
     }
+    if (lane == 0) saved[warp] = mine;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) all += saved[w];
+    const bool pays = all > kExtra * ctas;
+    for (int64_t g = warp; g < s.g.groups; g += 32) {
+        int64_t from, to;
+        entries_of(s, g, &from, &to);
+        __syncwarp();
+        const int32_t b = pays ? s.plan.tokens[g] : 0;
+        __syncwarp();
+        if (lane == 0) s.plan.tokens[g] = b;
+        for (int64_t r = from + lane; r < to; r += 32) s.plan.base[r] = b;
+    }
+    const int64_t first = bound(s.g.cu[0], a.batch), last = bound(s.g.cu[s.g.groups], a.batch);  // of all groups' entries
+    for (int64_t r = tid; r < a.batch; r += blockDim.x)
+        if (r < first || r >= last) s.plan.base[r] = 0;
 }
 
 // Position on the line of the prefixes' tiles.
@@ -753,7 +772,7 @@ template <int DL> cudaError_t launch(const LatentDecodeArgs &a, const SharedGrou
     if (!encode(&maps.q, a.q, C::D, q_rows, 1, C::D, q_rows * C::D, N) ||
         !encode(&maps.cache, a.cache.data, C::D, a.page, a.cache.n_rows, C::D, a.cache.row_stride, p.box_rows))
         return cudaErrorInvalidValue;
-    cudaError_t e = launch_overlapped(plan_kernel, dim3(static_cast<unsigned>(g.groups < 1024 ? g.groups : 1024)), dim3(128), 0, st, s);
+    cudaError_t e = launch_overlapped(plan_kernel, dim3(1), dim3(1024), 0, st, s, grid);
     if (e != cudaSuccess) return e;
     auto kern = prefix_kernel<DL>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
@@ -773,6 +792,9 @@ size_t latent_shared_workspace(int64_t batch, int64_t groups, int32_t L, int32_t
 
 cudaError_t launch_latent_decode_shared(const LatentDecodeArgs &a, const SharedGroups &g, cudaStream_t st)
 {
+    // Entries of 64 rows and more are bound by the tensor cores in either form: there is nothing to save (4 draft tokens x 128
+    // heads of 18 entries on 9,001 tokens: 221 us, with the prefixes' kernel 309 us).
+    if (static_cast<int64_t>(a.L) * a.h >= N) return launch_latent_decode(a, st);
     return a.dl == 512 ? launch<512>(a, g, st) : launch<256>(a, g, st);
 }
 
