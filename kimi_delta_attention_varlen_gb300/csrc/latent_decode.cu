@@ -558,26 +558,30 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                     }
                 }
                 if (!whole && tid == 128) (slot_out ? p.item1 : p.item0)[cta] = static_cast<int32_t>(w.r * p.rows + w.group * N);
+                const int valid = p.rows - w.group * N < N ? p.rows - w.group * N : N;
+                const int dim = 32 * quad + lane;
+                // the prefix's part of 16 columns, loaded while those before them are worked on
+                const bool prefixed = Shared && whole && w.base > 0;
+                float y[Shared ? 16 : 1];
+                auto load_prefix = [&](int c0) {
+                    if constexpr (Shared) {
+                        if (prefixed) {  // (of the last row in place of those behind it: loads that wait for nothing)
+                            const float *pre = p.pre + (w.r * p.rows + w.group * N) * DL + c0 / N * 128 + dim;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) y[e] = pre[min(c0 % N + e, valid - 1) * DL];
+                        }
+                    }
+                };
+                load_prefix(0);
                 wait(&bar.o, (passes - 1) & 1);
                 tc::fence_after_sync();
                 soft_any(false);  // linv is complete
-                const int valid = p.rows - w.group * N < N ? p.rows - w.group * N : N;
-                const int dim = 32 * quad + lane;
                 const bool taken = not_finite == segments;
 #pragma unroll 1
                 for (int c0 = 0; c0 < C::PAIRS * N; c0 += 16) {
                     uint32_t o[16];
                     tc::ld16(tl + c0, o);
                     const int mt = c0 / N, row0 = c0 % N;
-                    float y[Shared ? 16 : 1];  // the prefix's part: all loads before the first store
-                    const bool prefixed = Shared && whole && w.base > 0;
-                    if constexpr (Shared) {
-                        if (prefixed) {  // (of the last row in place of those behind it: loads that wait for nothing)
-                            const float *pre = p.pre + (w.r * p.rows + w.group * N) * DL + mt * 128 + dim;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) y[e] = pre[min(row0 + e, valid - 1) * DL];
-                        }
-                    }
                     tc::wait_ld();
                     if (taken) {  // draft tokens' values that were taken out, to the rows that see them
                         const int32_t last = min(w.n, w.token(w.tile + 1));
@@ -598,12 +602,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
                                              (w.r * p.rows + w.group * N + row0) * DL + mt * 128 + dim;
 #pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float x = __uint_as_float(o[e]) * linv[row0 + e];
+                            if (prefixed) x = fmaf(y[Shared ? e : 0], pinv[row0 + e], x);
+                            o[e] = __float_as_uint(x);
+                        }
+                        if (c0 + 16 < C::PAIRS * N) load_prefix(c0 + 16);
+#pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            if (row0 + e < valid) {
-                                float x = __uint_as_float(o[e]) * linv[row0 + e];
-                                if (prefixed) x = fmaf(y[Shared ? e : 0], pinv[row0 + e], x);
-                                out[e * DL] = __float2bfloat16_rn(x);
-                            }
+                            if (row0 + e < valid) out[e * DL] = __float2bfloat16_rn(__uint_as_float(o[e]));
                     } else {
                         float *out = p.part + (part * N + row0) * DL + mt * 128 + dim;
 #pragma unroll
