@@ -474,8 +474,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
                 l = 0.f;
                 const int rr = w.group * N + row;
                 seen = active && rr < p.rows ? w.n - (p.a.L - 1 - rr / p.a.h) : 0;
-            } else if (((w.tile - tile0) & (kSumTiles - 1)) == 0) {
-                finish(i - 1, w.tile - tile0 > kSumTiles, false, false);  // this tile's product does not add to it
             }
             const int stage = i % C::RING;
             wait(&bar.s[i & 1], (i >> 1) & 1);  // the tile's copies were complete for S
@@ -548,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
                 soft_any<kSoft>(false);
             }
             // the second product of the tile before has read P and written O^T
-            if (i > 0) wait(&bar.o, (i - 1) & 1);
+            if (i > 0 && !__all_sync(0xffffffffu, mbar_test(&bar.o, (i - 1) & 1))) wait(&bar.o, (i - 1) & 1);
             tc::fence_after_sync();
             if (active) {
                 const float above = (big == -INFINITY ? 0.f : big) - 4.f;  // weights 16 times, as fp16 pairs
@@ -599,11 +597,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
             fence_proxy_async_smem();
             tc::fence_before_sync();
             mbar_arrive(&bar.p);
-            const bool last = w.last();
-            if (last || i + 1 == total) {  // the segment ends here
+            // the segment ends here, or the next tile's product does not add to what the accumulator holds
+            const bool last = w.last(), over = last || i + 1 == total;
+            if (over || ((w.tile + 1 - tile0) & (kSumTiles - 1)) == 0) {
                 const bool whole = last && slot_out == 1;
-                if (!whole && st == 0) (slot_out ? p.item1 : p.item0)[cta] = static_cast<int32_t>(w.r * p.rows + w.group * N);
-                finish(i, w.tile - tile0 >= kSumTiles, true, whole);
+                if (over && !whole && st == 0) (slot_out ? p.item1 : p.item0)[cta] = static_cast<int32_t>(w.r * p.rows + w.group * N);
+                finish(i, w.tile - tile0 >= kSumTiles, over, whole);
             }
             w.next(p);
         }
