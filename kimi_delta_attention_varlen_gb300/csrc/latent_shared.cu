@@ -72,13 +72,13 @@ __device__ __forceinline__ void entries_of(const SharedParams &s, int64_t g, int
     if (*to < *from) *to = *from;
 }
 
-// What a tile of 64 tokens takes a CTA, in cycles: with an entry's own rows (in groups of 16, 32 or 64), and with 64 rows of a
-// prefix; and what the prefixes' launches and the joins take the GPU besides.
-constexpr int64_t kOwnTile = 3100, kPrefixTile = 3000, kExtra = 24000;
+// What a tile of 64 tokens takes a CTA, in cycles: with up to 32 rows of an entry, and with 64 rows (of an entry or of a
+// prefix).  What joining the prefix's part takes an entry's group of rows, and what the launches take the GPU, a CTA.
+constexpr int64_t kTile32 = 3100, kTile64 = 3430, kEntry = 20000, kLaunches = 24000;
 
-// By one CTA, a group a warp.  Sharing pays where the prefixes' tiles cost less than the entries' own would by more than the
-// launches: with 32 heads two requests or more to a block of rows, from some 10 us of own tiles on.  Where it does not (few tokens,
-// or entries that have 64 rows already, which the tensor cores bound in either form), nothing is shared.
+// By one CTA, a group a warp.  Sharing pays where it saves more tiles' time than the joins and launches take.  Where it does not,
+// nothing is shared and each entry takes all of its tokens (measured both ways: 64 entries of 32 heads on 32,768 tokens 227 us
+// against 344 us apart; 8 on 4,133 tokens 44 us against 31 us with nothing shared).
 __global__ void __launch_bounds__(1024) plan_kernel(SharedParams s, int32_t ctas)
 {
     __shared__ int64_t saved[32];
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(SharedParams s, int32_t ctas
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const LatentDecodeArgs &a = s.p.a;
     if (tid == 0) *s.p.status = 0;  // of all the kernels of the call
-    const int64_t own = s.p.rows <= 16 ? 16 : s.p.rows <= 32 ? 32 : 64;
+    const int64_t own = s.p.rows <= 32 ? 32 : 64;  // (one group of rows: entries of 64 rows do not come here)
     int64_t mine = 0;
     for (int64_t g = warp; g < s.g.groups; g += 32) {
         int64_t from, to;
@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(SharedParams s, int32_t ctas
             s.plan.tokens[g] = static_cast<int32_t>(b);
             s.plan.slot[g] = b > 0 ? static_cast<int32_t>(slot_of(a, from + (0x7fffffff - (best & 0x7fffffff)))) : 0;
             const int64_t rows = (to - from) * s.p.rows;
-            mine += (b + T - 1) / T * ((to - from) * ((s.p.rows + own - 1) / own) * kOwnTile - (rows + N - 1) / N * kPrefixTile);
+            if (b > 0)
+                mine += (b + T - 1) / T * ((to - from) * (own == N ? kTile64 : kTile32) - (rows + N - 1) / N * kTile64) - (to - from) * kEntry;
         }
     }
     if (lane == 0) saved[warp] = mine;
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(SharedParams s, int32_t ctas
     int64_t all = 0;
 #pragma unroll
     for (int w = 0; w < 32; ++w) all += saved[w];
-    const bool pays = all > kExtra * ctas;
+    const bool pays = all > kLaunches * ctas;
     for (int64_t g = warp; g < s.g.groups; g += 32) {
         int64_t from, to;
         entries_of(s, g, &from, &to);

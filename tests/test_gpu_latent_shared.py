@@ -38,6 +38,27 @@ def grouped(groups, page, dl, seed, gap=0, spare=3, width_extra=0):
     return cache, table, sl, rows, torch.tensor(cu, **i32), torch.tensor([p for p, _ in groups], **i32)
 
 
+def with_ballast(cache, table, sl, cu, shared, q):
+    """The same batch with one more group behind it, 300 entries that share 4,096 tokens: enough for sharing to pay, so that the groups
+    in front of it are computed together however small they are (alone the call leaves them to the plain kernel).
+    (cache, table, sl, cu, shared, q) with those entries; entries are picked by row, so req is not used with it."""
+    M, page, D = 300, cache.shape[2], cache.shape[3]
+    need = 4096 // page + 1
+    N = cache.shape[0]
+    g = wl.generator(N, DEV)
+    more = torch.empty(N + need, 1, page, D, dtype=BF, device=DEV)
+    more[:N] = cache
+    more[N:] = torch.randn(need, 1, page, D, generator=g, device=DEV).to(BF)
+    W = max(table.shape[1], need)
+    wide = torch.full((table.shape[0] + M, W), -1, dtype=torch.int32, device=DEV)
+    wide[:table.shape[0], :table.shape[1]] = table
+    wide[wide == N] = N + need  # a number behind the pool stays one
+    wide[table.shape[0]:, :need] = torch.arange(N, N + need, dtype=torch.int32, device=DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    return (more, wide, torch.cat([sl, torch.full((M,), 4096, **i32)]), torch.cat([cu, cu[-1:] + M]), torch.cat([shared, torch.tensor([4096], **i32)]),
+            torch.cat([q, torch.randn(M, *q.shape[1:], generator=g, device=DEV).to(BF)]))
+
+
 def run_shared(q, cache, table, lens, cu, shared, dl, scale=SCALE, req=None, stream=None, lse=True):
     R, L, H, D = q.shape
     out = poisoned(R, L, H, dl)
@@ -51,12 +72,25 @@ def run_shared(q, cache, table, lens, cu, shared, dl, scale=SCALE, req=None, str
     return out, ls
 
 
+def run_both(q, cache, table, sl, cu, shared, dl, scale=SCALE):
+    """The batch alone, and its entries out of the batch with ballast."""
+    R = q.shape[0]
+    yield run_shared(q, cache, table, sl, cu, shared, dl, scale)
+    cache, table, sl, cu, shared, q = with_ballast(cache, table, sl, cu, shared, q)
+    out, lse = run_shared(q, cache, table, sl, cu, shared, dl, scale)
+    # of the ballast, whose entries all see the same tokens, two
+    rows = cache[table[R, :4096 // cache.shape[2] + 1].long()].reshape(-1, cache.shape[3])[:4096]
+    assert_attention(out[[R, -1]], lse[[R, -1]], decode_reference(q[[R, -1]], lambda r, n: rows[:n], [4096, 4096], scale, dl), "ballast")
+    yield out[:R], lse[:R]
+
+
 def check_shared(groups, page, dl, heads, L=1, seed=0, scale=SCALE, **kw):
     cache, table, sl, rows, cu, shared = grouped(groups, page, dl, seed, **kw)
     q = queries(sl.numel(), L, heads, dl + 64, seed=seed)
-    out, lse = run_shared(q, cache, table, sl, cu, shared, dl, scale)
     lens = sl.tolist()
-    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, scale, dl), f"page {page} dl {dl} heads {heads} L {L}")
+    ref = decode_reference(q, lambda r, n: rows[r][:n], lens, scale, dl)
+    for k, (out, lse) in enumerate(run_both(q, cache, table, sl, cu, shared, dl, scale)):
+        assert_attention(out, lse, ref, f"page {page} dl {dl} heads {heads} L {L} {'with ballast' if k else 'alone'}")
 
 
 @pytest.mark.parametrize("dl", [512, 256])
@@ -86,7 +120,7 @@ def test_draft_tokens_are_causal(L, heads):
     check_shared([(200, [L, L + 1, 64 + L]), (130, [L + 3, 2 * L])], 16, 512, heads, L=L, seed=L, width_extra=3)
 
 
-@pytest.mark.parametrize("L", [1, 3, 70])
+@pytest.mark.parametrize("L", [1, 3, 7, 70])
 def test_prefix_that_is_not_behind_all_query_tokens(L):
     """Requests that end inside the prefix or just behind it: the drafts' mask falls into the shared pages, members are shorter
     than what is called shared."""
@@ -102,8 +136,9 @@ def test_prefix_that_is_not_behind_all_query_tokens(L):
             for r in range(4):
                 rows[r] = rows[3]
             rows[5] = rows[4]
-        out, lse = run_shared(q, cache, table, sl, cu, torch.tensor(told, dtype=torch.int32, device=DEV), dl)
-        assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, dl), f"L {L} told {told}")
+        ref = decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, dl)
+        for out, lse in run_both(q, cache, table, sl, cu, torch.tensor(told, dtype=torch.int32, device=DEV), dl):
+            assert_attention(out, lse, ref, f"L {L} told {told}")
 
 
 def test_nothing_shared_is_plain_decode():
@@ -113,8 +148,9 @@ def test_nothing_shared_is_plain_decode():
     ref = decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, 512)
     i32 = dict(dtype=torch.int32, device=DEV)
     for cu, shared in (([0, 4], [0]), ([0, 4], [63]), ([0, 4], [-5]), ([0, 1, 2, 3, 4], [100, 0, 3000, 64]), ([0, 0, 4, 4], [9, 0, 9]), ([2, 3], [640])):
-        out, lse = run_shared(q, cache, table, sl, torch.tensor(cu, **i32), torch.tensor(shared, **i32), 512)
-        assert_attention(out, lse, ref, f"{cu} {shared}")
+        for out, lse in run_both(q, cache, table, sl, torch.tensor(cu, **i32), torch.tensor(shared, **i32), 512) if cu[-1] == 4 else \
+                [run_shared(q, cache, table, sl, torch.tensor(cu, **i32), torch.tensor(shared, **i32), 512)]:
+            assert_attention(out, lse, ref, f"{cu} {shared}")
 
 
 @pytest.mark.parametrize("itype", [torch.int32, torch.int64])
@@ -161,11 +197,11 @@ def test_values_that_are_not_finite_reach_only_requests_that_see_them(where, bad
     ref = decode_reference(q, lambda r, n: rows[r][:n], sl.tolist(), SCALE, dl)
     tok = 100 if where == "prefix" else 250
     cache[table[1, tok // page].long(), 0, tok % page, dims] = bad  # 0 * bad is no number: the score is one neither
-    out, lse = run_shared(q, cache, table, sl, cu, shared, dl)
     hit = [0, 1, 2] if where == "prefix" else [1]
     clean = [r for r in range(5) if r not in hit]
-    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
-    assert_attention(out[clean], lse[clean], [x[clean] for x in ref], where)
+    for out, lse in run_both(q, cache, table, sl, cu, shared, dl):
+        assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+        assert_attention(out[clean], lse[clean], [x[clean] for x in ref], where)
 
 
 @pytest.mark.parametrize("bad", [math.inf, math.nan])
@@ -180,12 +216,12 @@ def test_values_of_the_prefix_that_some_query_tokens_do_not_see(bad, tok):
     q[..., 9] = 0
     ref = decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, dl)
     cache[table[0, tok // page].long(), 0, tok % page, 9] = bad
-    out, lse = run_shared(q, cache, table, sl, cu, shared, dl)
     sees = torch.tensor([[tok < n - (L - 1 - t) for t in range(L)] for n in lens])
-    assert torch.isnan(out.cpu()[sees]).all() and torch.isnan(lse.cpu()[sees]).all()
     clean = ~sees
-    if clean.any():
-        assert_attention(out.cpu()[clean], lse.cpu()[clean], [x[clean] for x in ref], f"token {tok}")
+    for out, lse in run_both(q, cache, table, sl, cu, shared, dl):
+        assert torch.isnan(out.cpu()[sees]).all() and torch.isnan(lse.cpu()[sees]).all()
+        if clean.any():
+            assert_attention(out.cpu()[clean], lse.cpu()[clean], [x[clean] for x in ref], f"token {tok}")
 
 
 def test_queries_that_are_not_finite_stay_in_their_rows():
@@ -193,11 +229,11 @@ def test_queries_that_are_not_finite_stay_in_their_rows():
     q = queries(3, 1, 32, 576, seed=9)
     ref = decode_reference(q, lambda r, n: rows[r][:n], sl.tolist(), SCALE, 512)
     q[0, 0, 3, 17], q[1, 0, 9, 540], q[2, 0, 30, 0] = math.nan, math.inf, -math.inf
-    out, lse = run_shared(q, cache, table, sl, cu, shared, 512)
     bad = torch.zeros(3, 1, 32, dtype=torch.bool)
     bad[0, 0, 3] = bad[1, 0, 9] = bad[2, 0, 30] = True
-    assert torch.isnan(out.cpu()[bad]).all() and torch.isnan(lse.cpu()[bad]).all()
-    assert_attention(out.cpu()[~bad], lse.cpu()[~bad], [x[~bad] for x in ref])
+    for out, lse in run_both(q, cache, table, sl, cu, shared, 512):
+        assert torch.isnan(out.cpu()[bad]).all() and torch.isnan(lse.cpu()[bad]).all()
+        assert_attention(out.cpu()[~bad], lse.cpu()[~bad], [x[~bad] for x in ref])
 
 
 def test_scores_that_differ_widely_between_prefix_and_suffix():
@@ -216,8 +252,9 @@ def test_scores_that_differ_widely_between_prefix_and_suffix():
         rows[r][:160] = rows[0][:160]
     q = queries(2, 1, 4, dl + 64, seed=10)
     q[..., 0] = torch.tensor([20.0, -20.0, 200.0, -200.0], device=DEV)
-    out, lse = run_shared(q, cache, table, sl, cu, shared, dl, scale=1.0)
-    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], sl.tolist(), 1.0, dl))
+    ref = decode_reference(q, lambda r, n: rows[r][:n], sl.tolist(), 1.0, dl)
+    for out, lse in run_both(q, cache, table, sl, cu, shared, dl, scale=1.0):
+        assert_attention(out, lse, ref)
 
 
 def test_invalid_pages_read_as_zero_rows():
@@ -227,8 +264,9 @@ def test_invalid_pages_read_as_zero_rows():
         rows[r][32:64] = 0
     rows[1][128:160] = 0
     q = queries(2, 1, 32, 576, seed=11)
-    out, lse = run_shared(q, cache, table, sl, cu, shared, 512)
-    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], sl.tolist(), SCALE, 512))
+    ref = decode_reference(q, lambda r, n: rows[r][:n], sl.tolist(), SCALE, 512)
+    for out, lse in run_both(q, cache, table, sl, cu, shared, 512):
+        assert_attention(out, lse, ref)
 
 
 def test_forked_requests_share_what_the_fork_left_them():
@@ -301,6 +339,72 @@ def test_captured_in_a_graph_and_replayed_with_other_groups():
         graph.replay()
         torch.cuda.synchronize()
         assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, 512), f"{told_cu} {told}")
+
+
+@pytest.mark.parametrize("itype", [torch.int32, torch.int64])
+def test_a_shared_batch_with_padding(itype):
+    """400 entries on one prefix, every fifth of them invalid or empty, in a batch that sharing pays for; twice, bit for bit."""
+    page, dl, R = 64, 512, 400
+    cache, table, sl, rows, _, _ = grouped([(4096, [0, 40, 700])], page, dl, seed=21)
+    pick = [(0, 1, 2, 1, -1)[i % 5] for i in range(R - 2)] + [7, 1]
+    q = queries(R, 1, 16, 576, seed=21)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    args = (q, cache, table, sl, torch.tensor([0, R], **i32), torch.tensor([4110], **i32), dl)
+    req = torch.tensor(pick, dtype=itype, device=DEV)
+    out, lse = run_shared(*args, req=req)
+    again, _ = run_shared(*args, req=req)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+    bad = [i for i, p in enumerate(pick) if p not in (0, 1, 2)]
+    assert (out[bad] == 0).all() and (lse[bad] == -math.inf).all()
+    some = [0, 1, 2, 3, 200, 201, 202, 396, 397, 399]
+    some = [i for i in some if pick[i] in (0, 1, 2)]
+    ref = decode_reference(q[some], lambda i, n: rows[pick[some[i]]][:n], [int(sl[pick[i]]) for i in some], SCALE, dl)
+    assert_attention(out[some], lse[some], ref)
+
+
+def test_a_shared_batch_captured_and_replayed():
+    cache, table, sl, rows, cu, shared = grouped([(320, [17, 90, 1]), (128, [64, 5])], 64, 512, seed=14)
+    cache, table, sl, cu, shared, q = with_ballast(cache, table, sl, cu, shared, queries(5, 1, 32, 576, seed=14))
+    R = q.shape[0]
+    out, lse = torch.empty(R, 1, 32, 512, dtype=BF, device=DEV), torch.empty(R, 1, 32, device=DEV)
+    ws = torch.empty(kda.kda_latent_decode_shared_workspace_size(R, 3, 1, 32, 512, 64), dtype=torch.uint8, device=DEV)
+
+    def call():
+        kda.kda_latent_decode_shared(q, cache, table, sl, cu, shared, out, ws, latent_dim=512, scale=SCALE, lse=lse)
+
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            call()
+    for told, lens in (([320, 128, 4096], [337, 410, 321, 192, 133]), ([64, 0, 4096], [337, 410, 321, 192, 133]), ([320, 128, 0], [337, 410, 321, 192, 133]),
+                       ([256, 128, 4000], [330, 340, 320, 10, 0])):
+        shared.copy_(torch.tensor(told))
+        sl[:5] = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        out.fill_(math.nan)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert kda.kda_prefill_workspace_status(ws) == 0
+        assert_attention(out[:5], lse[:5], decode_reference(q[:5], lambda r, n: rows[r][:n], lens, SCALE, 512), f"{told}")
+
+
+def test_which_batches_share():
+    """Alone, a small batch is the plain call's, bit for bit; in a batch that sharing pays for it is summed in another order; entries of
+    64 rows are the plain call's in any batch."""
+    for heads, same_in_ballast in ((32, False), (64, True)):
+        cache, table, sl, rows, cu, shared = grouped([(1280, [17, 90, 1]), (640, [64, 5])], 64, 512, seed=30)
+        q = queries(5, 1, heads, 576, seed=30)
+        plain = torch.empty(5, 1, heads, 512, dtype=BF, device=DEV)
+        ws = torch.empty(kda.kda_latent_decode_workspace_size(5, 1, heads, 512, 64), dtype=torch.uint8, device=DEV)
+        kda.kda_latent_decode(q, cache, table, sl, plain, ws, latent_dim=512, scale=SCALE)
+        (alone, _), (among, _) = run_both(q, cache, table, sl, cu, shared, 512)
+        assert torch.equal(alone.view(torch.int16), plain.view(torch.int16))
+        # (the same kernel may cut its items elsewhere in a larger batch: equality of bits says the most about the smaller difference)
+        far = (among.float() - plain.float()).abs().max() / plain.float().abs().max()
+        assert far <= 2.0 ** -6 and (same_in_ballast or not torch.equal(among.view(torch.int16), plain.view(torch.int16)))
 
 
 def test_two_calls_queued_on_two_workspaces():
