@@ -665,9 +665,12 @@ int kda_latent_append(const void *x, int64_t x_stride, int64_t total, const int3
  *
  * kda_latent_decode for a batch whose entries come in groups that begin with
  * the same tokens in the same pages (parallel samples of a prompt, a common
- * system prompt): the attention to those tokens is computed once for all query
- * rows of a group together, so their pages are read once and not once a
- * request, and joined with each entry's own rest.
+ * system prompt): the attention to those tokens is computed for all query rows
+ * of a group together and joined with each entry's own rest, so their pages
+ * are read once for 64 rows and not once a request.  Where that saves less
+ * than it costs (decided on the device from the lengths: few tokens, few
+ * members; entries of L * h >= 64 rows, which the tensor cores bound in either
+ * form) each entry takes all of its tokens, as kda_latent_decode does.
  *   cu_groups [groups + 1] device int32, from 0, non-decreasing, ending at
  *             batch (precondition; entries outside all groups share nothing):
  *             entries cu_groups[g] .. cu_groups[g + 1] - 1 are group g
@@ -680,8 +683,9 @@ int kda_latent_append(const void *x, int64_t x_stride, int64_t total, const int3
  * are not finite, empty and invalid requests, sizes built and errors - is as for
  * kda_latent_decode; results differ from its by the order of summation.
  *   workspace kda_latent_decode_shared_workspace_size(...) bytes, 256-byte
- *             aligned.  Errors beside those: KDA_ERR_SHAPE (groups < 1),
- *             _RANGE (groups >= 2^24).
+ *             aligned (dl * 4 + 16 bytes for every query row among them).
+ *             Errors beside those: KDA_ERR_SHAPE (groups < 1), _RANGE (groups
+ *             >= 2^24).
  * ---------------------------------------------------------------------- */
 size_t kda_latent_decode_shared_workspace_size(int64_t batch, int64_t groups, int32_t L, int32_t h,
                                                int32_t dl, int32_t dr);

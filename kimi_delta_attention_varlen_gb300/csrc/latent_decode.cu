@@ -48,6 +48,8 @@
 // later).  64-token tiles because of the same ring: 512 requests took 617 us with 96 and 572 with 128 where they took
 // 439 with 64.  Four copying warps instead of two: 425 / 420 us, drafts alike.
 //
+// With a prefix that groups share (latent_shared.cu) the same kernels take the tokens behind it and add its part at the end.
+//
 // Every wait is bounded; an expired one sets the workspace's status word (6) and ends the CTA.
 #include "latent_decode.cuh"
 

@@ -22,6 +22,15 @@
 // rope keys, units) is one stage of a ring.  Warps: 0 and 3 copy, 1 and 2 issue one product each, 4 to 11 do the softmax and the
 // epilogue, 12 to 15 split the next segment's queries into their parts while this one's tiles run.
 //
+// What bounds it: the chain of a tile through the softmax warps (scores, maximum, exponentials, parts, hand-over: about 2,200
+// cycles, where the bytes of a tile, 41 KB, take 1,800) and the end of a segment (6,800 cycles).  512 requests of 512..8,192 tokens,
+// 32 heads: 286..290 us = 4.9 TB/s (bf16 pages: 426 us); two of 131,072: 56 us (66); one of 1,009: 16 us (13).  33 requests x 4 draft
+// tokens x 128 heads: 280 us (bf16 pages: 222 us): 32 rows to a group where that form has 64, so the pages come twice as
+// often, from L2.  Instructions count here as code: the kernel's roles share an instruction cache, and the epilogue in two places
+// cost the 512 requests 23 us, unrolled once more 30 us.  Tried and not kept: four softmax warps (341 us at that time, eight
+// with half of the tokens each 317), two groups of four that take the tiles in turn (399), weights in two places so that the next
+// are written while these are read (316), the rope products of a tile ahead (313), queries read twice instead of held (318).
+//
 // Every wait is bounded; an expired one sets the workspace's status word (6) and ends the CTA.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

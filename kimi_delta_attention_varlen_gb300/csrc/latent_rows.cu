@@ -1,9 +1,14 @@
 // Rows of latents into 8-bit pages (kda_latent_append8) and out of pages (kda_latent_read).
 //
-// A token is one warp's: append8 has the row in registers (dl / 32 + 2 values a lane), takes the largest magnitudes of
-// its latent and of its rope key by shuffles and from them the token's unit 2^e, scales (exact: a power of two) and
-// rounds once.  Reading back multiplies by 2^e, exact in bf16 for every code.  Loads and stores are whole 16- or 8-byte
-// vectors, consecutive across the warp.
+// Writing: a token is one warp's, which has the row in registers, takes the largest magnitudes of its latent and of its rope
+// key across the warp and from them the token's unit 2^e, scales (exact: a power of two) and rounds once.  One power of two for a
+// token and not an fp32 maximum / 448: e4m3's relative step is the same in every binade, so nothing is lost, and code * 2^e and
+// rope * 2^-e are exact in bf16, whatever reads them.  Reading back multiplies by 2^e.
+//
+// What bounds it: bytes (644 + 1,152 a token), and before them the look-ups, five loads that wait for one another (offsets, request,
+// length, page, row).  A CTA's rows are looked up together, a row a lane; reading keeps four rows a warp in flight behind them.
+// 73,364 tokens: written in 29.6 us = 4.5 TB/s, read in 24.3 us = 5.5 TB/s (one look-up a warp: 37.5 and 27.6 us); 24 new tokens 3.1 us.
+// Loads and stores are whole 16- or 8-byte vectors, consecutive across the warp.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -43,22 +48,28 @@ __device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_s
 
 __device__ __forceinline__ uint32_t codes2(float a, float b) { return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3); }
 
-// Eight consecutive values of a row of x.
-template <typename X> __device__ __forceinline__ void load8(const X *p, float (&v)[8]);
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&v)[8])
-{
-    const uint4 u = ld_v4(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight consecutive values of a row of x, as they are (until they are needed they take half of the registers in bf16).
+template <typename X> struct Eight8 {
+    static constexpr int V = sizeof(X) / 2;
+    uint4 u[V];
+    __device__ void load(const X *p)
+    {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(w[e]), v[2 * e + 1] = bf16_hi(w[e]);
-}
-template <> __device__ __forceinline__ void load8<float>(const float *p, float (&v)[8])
-{
-    const uint4 a = ld_v4(p), b = ld_v4(p + 4);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        for (int e = 0; e < V; ++e) u[e] = ld_v4(p + e * 16 / sizeof(X));
+    }
+    __device__ void values(float (&v)[8]) const
+    {
+        if (V == 1) {
+            const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
-}
+            for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(w[e]), v[2 * e + 1] = bf16_hi(w[e]);
+        } else {
+            const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[V - 1].x, u[V - 1].y, u[V - 1].z, u[V - 1].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
+        }
+    }
+};
 
 // Of a CTA's rows: where each one's token is. By warp 0: the entry of the CTA's first row is looked for by the whole warp, the
 // others follow from it (rows of one entry lie together), a row a lane.
@@ -104,12 +115,13 @@ __global__ void __launch_bounds__(32 * kWarps) append8_kernel(const X *x, Latent
     after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kWarps * Per;
-    float c[Per][DL / 256][8], r[Per][2];
+    Eight8<X> x8[Per][DL / 256];
+    float r[Per][2];
     auto load = [&](int k) {
         if (row0 + warp + kWarps * k >= a.total) return;
         const X *from = x + (row0 + warp + kWarps * k) * a.stride;
 #pragma unroll
-        for (int e = 0; e < DL / 256; ++e) load8(from + 256 * e + 8 * lane, c[k][e]);
+        for (int e = 0; e < DL / 256; ++e) x8[k][e].load(from + 256 * e + 8 * lane);
         r[k][0] = load_as_f32(from + DL + 2 * lane), r[k][1] = load_as_f32(from + DL + 2 * lane + 1);
     };
 #pragma unroll
@@ -120,11 +132,14 @@ __global__ void __launch_bounds__(32 * kWarps) append8_kernel(const X *x, Latent
     for (int k = 0; k < Per; ++k) {
         const Spot spot = spots[warp + kWarps * k];
         if (spot.page < 0) continue;
+        float c[DL / 256][8];
         uint32_t most = 0;
 #pragma unroll
-        for (int e = 0; e < DL / 256; ++e)
+        for (int e = 0; e < DL / 256; ++e) {
+            x8[k][e].values(c[e]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(c[k][e][j]) & 0x7fffffffu);
+            for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(c[e][j]) & 0x7fffffffu);
+        }
         most = warp_max(most);
         const bool finite = most < 0x7f800000u;  // of the latent, in every lane alike: then no value needs a look of its own
         if (!finite) {
@@ -133,8 +148,8 @@ __global__ void __launch_bounds__(32 * kWarps) append8_kernel(const X *x, Latent
             for (int e = 0; e < DL / 256; ++e)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    most = max(most, finite_magnitude(c[k][e][j]));
-                    if (!(fabsf(c[k][e][j]) < INFINITY)) c[k][e][j] = NAN;  // e4m3 has no infinities
+                    most = max(most, finite_magnitude(c[e][j]));
+                    if (!(fabsf(c[e][j]) < INFINITY)) c[e][j] = NAN;  // e4m3 has no infinities
                 }
             most = warp_max(most);
         }
@@ -147,7 +162,7 @@ __global__ void __launch_bounds__(32 * kWarps) append8_kernel(const X *x, Latent
         char *to = static_cast<char *>(a.cache.data) + spot.page * a.cache.row_stride;
 #pragma unroll
         for (int e = 0; e < DL / 256; ++e) {
-            const float *v = c[k][e];
+            const float *v = c[e];
             uint32_t w[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -218,9 +233,9 @@ __global__ void __launch_bounds__(32 * kWarps) read_kernel(LatentRowsArgs a)
     }
 }
 
-// Rows a warp (kWarps times that many are at most 32): 73,364 tokens written in 34.8 us with 2, 38.8 with 4 and 35.4 with 1, read
-// in 24.1 with 8, 24.4 with 4 and 26.6 with 1.
-constexpr int kPerAppend = 2, kPerRead = 4;
+// Rows a warp (kWarps times that many are at most 32).  73,364 tokens of 512 + 64 values: written in 29.6 us with 1 or 2, 31.8 with
+// 4 (a step's 24 tokens 3.1, 3.8 and 5.2); read in 24.3 us with 4 or 8, 26.6 with 1.
+constexpr int kPerAppend = 1, kPerRead = 4;
 
 dim3 grid_of(int64_t total, int per) { return dim3(static_cast<unsigned>((total + kWarps * per - 1) / (kWarps * per))); }
 

@@ -16,6 +16,13 @@
 // that is less (a request that ends in the prefix).  Eight softmax warps, two for the same 16 rows with half of a tile's tokens
 // each, since the ring has room for two tiles and a tile keeps its place until its second product is done.
 //
+// What bounds it: shared memory.  A tile of 64 tokens x 64 rows moves 319 KB through it (operands of S 147, of O^T 98, the copy 74:
+// 2,500 cycles at 128 bytes each), and takes 3,430 cycles: the copies wait for the products' reads, and the ring has room for one
+// tile beside the one that is worked on.  64 requests of 32 heads on 32,768 tokens: 188 us of 232 us (apart: 344 us); 500 requests
+// on seven system prompts of 3,000..6,001 tokens 212 us of 389 us (447 us); the rest's kernel then adds the prefix's sums, 64 KB a
+// request, which it loads a step ahead.  Tried and not kept: panels copied once for two CTAs of a cluster (multicast, an item of
+// 128 rows: 237 and 450 us where it was 233 and 446 then).
+//
 // Every wait is bounded; an expired one sets the workspace's status word (6) and ends the CTA.
 #include "latent_decode.cuh"
 
