@@ -89,7 +89,19 @@ __device__ __forceinline__ void find_spots(const LatentRowsArgs &a, int64_t row0
         int64_t i = entry_of(a.cu, a.count, from);
         if (lane < Rows && row >= begin && row < behind && row < a.total) {
             int64_t end = a.cu[i + 1];
-            while (row >= end && i + 1 < a.count) end = a.cu[++i + 1];
+            for (int step = 0; row >= end && i + 1 < a.count; ++step) {
+                if (step == 3) {  // many entries without rows between: the last one that begins at or before this row
+                    int64_t hi = a.count;
+                    while (hi - i > 1) {
+                        const int64_t mid = (i + hi) >> 1;
+                        if (a.cu[mid] <= row) i = mid;
+                        else hi = mid;
+                    }
+                    end = a.cu[i + 1];
+                    break;
+                }
+                end = a.cu[++i + 1];
+            }
             if (row < end) {
                 x.page = -1;
                 const int64_t req = load_index(a.req, a.idx_type, i);

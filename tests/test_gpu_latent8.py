@@ -200,6 +200,28 @@ def test_written_rows_come_back_within_their_rounding():
     assert torch.equal(out[:, dl:], x[:, dl:])  # a power of two away: the same bf16 digits
 
 
+@pytest.mark.parametrize("rows", [1, 3, 40])
+def test_lists_of_which_most_entries_have_no_rows(rows):
+    """5,000 entries, of which a few have rows: a step of a server that lists all of its requests."""
+    dl, page, R = 256, 16, 5000
+    g = torch.Generator().manual_seed(rows)
+    has = sorted(torch.randperm(R, generator=g)[:60].tolist())
+    lens = [0] * R
+    for r in has:
+        lens[r] = rows
+    cache, table, sl, data = h8.paged8(lens, page, dl, seed=3)
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    out = read_back(cache, table, lens, page, dl, cu, list(range(R)), None, cu[-1])
+    assert torch.equal(out.double().cpu(), torch.cat([data[r] for r in has]))
+    x = torch.randn(cu[-1], dl + 64, generator=wl.generator(rows, DEV), device=DEV).to(BF)
+    run_append(x, cu, list(range(R)), table, lens, cache, dl, page)
+    c, rope, scale = h8.quantise(x, dl)
+    out = read_back(cache, table, lens, page, dl, cu, list(range(R)), None, cu[-1])
+    assert torch.equal(out.double().cpu(), torch.cat([c, rope], 1) * scale[:, None])
+
+
 # ----------------------------------------------------------------- decode --
 
 def run_decode8(q, cache, table, lens, dl, scale, req=None, stream=None, lse=True):
@@ -327,6 +349,65 @@ def test_decode_sink_and_a_long_flat_rest():
     q[..., dl] = 0.125
     out, lse = run_decode8(q, cache, table, sl, dl, 1.0)
     assert_attention(out, lse, decode_reference(q, lambda r, k: rows[:k], [n], 1.0, dl))
+
+
+@pytest.mark.parametrize("dl", [512, 256])
+def test_decode_millions_of_tokens(dl):
+    """One request of 3.2 million tokens, whose table lists the same 50 pages over and over: 20,000 tokens and more to a CTA, so that
+    the accumulator is set aside.  Each row's weight counts as often as it is listed."""
+    page, pages, times = 64, 50, 1000
+    cache, table, _, rows = h8.paged8([page * pages], page, dl, seed=51)
+    n = page * pages * times - 17
+    table = table[:, :pages].repeat(1, times).contiguous()
+    q = queries(1, 1, 32, dl + 64, seed=51)
+    out, lse = run_decode8(q, cache, table, torch.tensor([n], dtype=torch.int32, device=DEV), dl, SCALE)
+    x = rows[0]
+    count = torch.full((page * pages,), float(times), dtype=torch.float64)
+    count[-17:] -= 1
+    z = q[0, 0].double().cpu() @ x.T * SCALE + count.log()
+    want_lse = torch.logsumexp(z, -1)
+    p = torch.softmax(z, -1)
+    bound = (q[0, 0].double().cpu().abs() @ x.abs().T * SCALE).amax(-1)
+    assert_attention(out[0, 0], lse[0, 0], (p @ x[:, :dl], p @ x[:, :dl].abs(), want_lse, bound))
+
+
+@pytest.mark.parametrize("heads,fall", [(4, False), (32, False), (32, True)])
+def test_decode_scores_that_rise_or_fall_over_millions_of_tokens(heads, fall):
+    """Scores 40 apart over 4.2 million tokens of two units, 27,000 tokens to a CTA: both maxima move again and again, and what was set
+    aside is brought to the new ones."""
+    dl, page, N = 256, 64, 65536
+    n = N * page - 5
+    cache = torch.empty(N, 1, page, dl + 132, dtype=torch.uint8, device=DEV)
+    g = wl.generator(61, DEV)
+    codes, rope, scales = h8.parts(cache, dl)
+    one = torch.randn(97, dl, generator=g, device=DEV).clamp(-448, 448).to(torch.float8_e4m3fn)  # tokens' codes, in turn
+    t = torch.arange(N * page, device=DEV)
+    codes.copy_(one.view(torch.uint8)[t % 97].view(N, page, dl))
+    unit = torch.where(t % 3 == 0, 2.0 ** -7, 1.0)
+    rope.zero_()
+    level = 40.0 * t / n
+    rope[..., 0] = ((40 - level if fall else level) / unit).to(BF).view(N, page)  # (rounded: the score is what the page holds)
+    scales.copy_(unit.view(N, page))
+    table = torch.arange(N, dtype=torch.int32, device=DEV)[None]
+    q = torch.zeros(1, 1, heads, dl + 64, dtype=BF, device=DEV)
+    q[..., dl] = 1
+    q[0, 0, 1:, 3] = 0.25
+    out, lse = run_decode8(q, cache, table, torch.tensor([n], dtype=torch.int32, device=DEV), dl, 1.0)
+    u = unit[:n].double()
+    r0 = rope[..., 0].reshape(-1)[:n].double() * u
+    c3 = one[:, 3].double()[t[:n] % 97] * u
+    want, mag, want_lse, bound = [], [], [], []
+    for h in (0, 1):
+        z = r0 + (0.25 * c3 if h else 0)
+        p = torch.softmax(z, 0)
+        by = torch.zeros(97, dtype=torch.float64, device=DEV).index_add_(0, t[:n] % 97, p * u)
+        want.append(by @ one.double())
+        mag.append(by @ one.double().abs())
+        want_lse.append(torch.logsumexp(z, 0))
+        bound.append((r0.abs() + 0.25 * c3.abs()).max())
+    ref = [torch.stack(x).cpu() for x in (want, mag, want_lse, bound)]
+    assert_attention(out[0, 0, :2], lse[0, 0, :2], ref, f"heads {heads} fall {fall}")
+    assert torch.equal(out[0, 0, 1].expand(heads - 1, -1), out[0, 0, 1:]) and torch.equal(lse[0, 0, 1].expand(heads - 1), lse[0, 0, 1:])
 
 
 def test_decode_queries_that_are_not_finite_stay_in_their_rows():

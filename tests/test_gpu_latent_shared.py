@@ -173,6 +173,30 @@ def test_long_prefixes(groups, heads):
     check_shared(groups, 64, 512, heads, seed=heads)
 
 
+@pytest.mark.parametrize("dl", [512, 256])
+def test_a_prefix_of_millions_of_tokens(dl):
+    """Four entries on 3.2 million tokens, the same 50 pages over and over: the accumulator of the prefix is set aside."""
+    page, pages, times, H = 64, 50, 1000, 32
+    cache, table, _, rows = paged_latents([page * pages] + [page + 5 + r for r in range(4)], page, dl, seed=52)
+    listed = table[0, :pages].repeat(times)
+    tables = torch.full((4, pages * times + 2), -1, dtype=torch.int32, device=DEV)
+    tables[:, :pages * times] = listed
+    tables[:, pages * times:] = table[1:, :2]
+    n = [page * pages * times + page + 5 + r for r in range(4)]
+    i32 = dict(dtype=torch.int32, device=DEV)
+    q = queries(4, 1, H, dl + 64, seed=52)
+    out, lse = run_shared(q, cache, tables, torch.tensor(n, **i32), torch.tensor([0, 4], **i32), torch.tensor([page * pages * times], **i32), dl)
+    for r in range(4):
+        x = torch.cat([rows[0], rows[1 + r]]).double().cpu()
+        count = torch.ones(x.shape[0], dtype=torch.float64)
+        count[:page * pages] = times
+        qq = q[r, 0].double().cpu()
+        z = qq @ x.T * SCALE + count.log()
+        p = torch.softmax(z, -1)
+        bound = (qq.abs() @ x.abs().T * SCALE).amax(-1)
+        assert_attention(out[r, 0], lse[r, 0], (p @ x[:, :dl], p @ x[:, :dl].abs(), torch.logsumexp(z, -1), bound))
+
+
 def test_many_groups():
     g = torch.Generator().manual_seed(8)
     groups = [(int(torch.randint(0, 400, (1,), generator=g)), torch.randint(0, 90, (int(torch.randint(0, 6, (1,), generator=g)),), generator=g).tolist())
