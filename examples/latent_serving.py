@@ -9,8 +9,13 @@ ends another, and packs the pages, with the calls of the library only:
     kda_latent_prefill                       the prompts' attention (expanded form)
     kda_prefill_varlen_cached                the prompts through the recurrent layer
     kda_pages_fork, kda_pages_copy           parallel samples share pages; recurrent states are copied
-    kda_latent_decode, kda_decode_step       one token a request (absorbed form; recurrent step)
+    kda_latent_decode_shared, kda_decode_step
+                                             one token a request (absorbed form, what the samples have in
+                                             common once for all of them; recurrent step)
     kda_pages_release, kda_pages_compact     requests end, pages are packed
+
+With the latents in 8 bits, kda_latent_append8 and kda_latent_decode8 take the place of the bf16
+calls, and kda_latent_read brings rows back out of the pages.
 
     python examples/latent_serving.py
 """
@@ -52,18 +57,21 @@ class Layer:
 
 
 class Server:
-    """Page tables, a latent cache and recurrent states for a fixed number of requests."""
+    """Page tables, a latent cache (eight: in 8 bits) and recurrent states for a fixed number of requests."""
 
-    def __init__(self, layer, requests=16, pages=64, page=16, width=16, dev="cuda"):
+    def __init__(self, layer, requests=16, pages=64, page=16, width=16, dev="cuda", eight=False):
         i32 = dict(dtype=torch.int32, device=dev)
-        self.layer, self.dev = layer, dev
+        self.layer, self.dev, self.eight = layer, dev, eight
         self.table, self.lens, self.ref = torch.full((requests, width), -1, **i32), torch.zeros(requests, **i32), torch.zeros(pages, **i32)
         self.pt = kda.page_table_descriptor(self.table, self.lens, self.ref, page)
-        self.latents = torch.zeros(pages, 1, page, LATENT + ROPE, dtype=BF, device=dev)
+        self.latents = torch.zeros(pages, 1, page, LATENT + 2 * ROPE + 4, dtype=torch.uint8, device=dev) if eight else \
+            torch.zeros(pages, 1, page, LATENT + ROPE, dtype=BF, device=dev)
         self.states = torch.zeros(requests, H, DIM, DIM, device=dev)
         self.info = torch.zeros(4, **i32)
         self.page_ws = torch.empty(kda.kda_pages_workspace_size(pages, requests), dtype=torch.uint8, device=dev)
-        self.decode_ws = torch.empty(kda.kda_latent_decode_workspace_size(requests, 1, H, LATENT, ROPE), dtype=torch.uint8, device=dev)
+        size = kda.kda_latent_decode8_workspace_size(requests, 1, H, LATENT, ROPE) if eight else \
+            kda.kda_latent_decode_shared_workspace_size(requests, requests, 1, H, LATENT, ROPE)
+        self.decode_ws = torch.empty(size, dtype=torch.uint8, device=dev)
 
     def ints(self, x):
         return torch.tensor(x, dtype=torch.int32, device=self.dev)
@@ -74,7 +82,16 @@ class Server:
         src, dst = torch.empty_like(req), torch.empty_like(req)
         kda.kda_pages_reserve(self.pt, req, self.ints(counts), src, dst, self.info, self.page_ws)
         kda.kda_pages_copy(self.latents, src, dst)  # unfinished pages that were shared
-        kda.kda_latent_append(rows, cu, req, self.pt, self.latents)
+        if self.eight:
+            kda.kda_latent_append8(rows, cu, req, self.pt, self.latents, latent_dim=LATENT)
+        else:
+            kda.kda_latent_append(rows, cu, req, self.pt, self.latents)
+
+    def read(self, r, first, n):
+        """Latent rows first .. first + n - 1 of a request, as the cache holds them."""
+        out = torch.empty(n, LATENT + ROPE, dtype=BF, device=self.dev)
+        kda.kda_latent_read(self.latents, self.ints([0, n]), self.ints([r]), self.pt, out, latent_dim=LATENT, first=self.ints([first]))
+        return out
 
     def prompts(self, req, lengths, rows, q, gates):
         """Prompts of new requests: attention outputs [T, H, DIM] and recurrent outputs of all their tokens."""
@@ -95,12 +112,18 @@ class Server:
         kda.kda_pages_fork(self.pt, self.ints(src), self.ints(dst))
         kda.kda_pages_copy(self.states, self.ints(src), self.ints(dst))
 
-    def step(self, req, rows, q, gates):
-        """One token of each request: attention values and recurrent outputs [R, H, DIM]."""
+    def step(self, req, groups, rows, q, gates):
+        """One token of each request: attention values and recurrent outputs [R, H, DIM].  groups: (requests, tokens that they
+        have in common), in the order of req."""
         self.grow(req, [1] * len(req), rows)
         out = torch.empty(len(req), 1, H, LATENT, dtype=BF, device=self.dev)
-        kda.kda_latent_decode(self.layer.absorb(q), self.latents, self.table, self.lens, out, self.decode_ws, latent_dim=LATENT,
-                              scale=self.layer.scale, req=self.ints(req))
+        args = dict(latent_dim=LATENT, scale=self.layer.scale, req=self.ints(req))
+        if self.eight:
+            kda.kda_latent_decode8(self.layer.absorb(q), self.latents, self.table, self.lens, out, self.decode_ws, **args)
+        else:
+            cu = self.ints([0] + [n for n, _ in groups]).cumsum(0, dtype=torch.int32)
+            kda.kda_latent_decode_shared(self.layer.absorb(q), self.latents, self.table, self.lens, cu, self.ints([t for _, t in groups]), out,
+                                         self.decode_ws, **args)
         mixed = torch.empty(len(req), H, DIM, dtype=BF, device=self.dev)
         kda.kda_decode_step(gates["q"], gates["k"], gates["v"], gates["g"], gates["beta"], self.states, self.ints(req), mixed)
         return self.layer.values(out), mixed
@@ -123,12 +146,12 @@ def attention(layer, rows, q):
     return torch.einsum("ht,the->he", torch.softmax(z, -1), v)
 
 
-def main(seed=0, dev="cuda"):
+def main(seed=0, dev="cuda", eight=False):
     """Serves and checks every attention output against the 64-bit form on the request's own tokens; the largest error."""
     gen = torch.Generator(device=dev)
     gen.manual_seed(seed)
     layer = Layer(gen, dev)
-    server = Server(layer, dev=dev)
+    server = Server(layer, dev=dev, eight=eight)
     history, worst = {}, 0.0
 
     def draw(n):
@@ -153,15 +176,18 @@ def main(seed=0, dev="cuda"):
         for t in (0, n // 2, n - 1):
             check(out[at + t], attention(layer, rows[at:at + t + 1], q[at + t]))
         at += n
+        if eight:  # from here on attention sees what the cache holds
+            history[r] = server.read(r, 0, n)
     # request 1 samples twice in parallel
     server.fork([1, 1], [5, 6])
     history[5] = history[6] = history[1]
-    live = [0, 1, 2, 5, 6]
+    live = [0, 1, 5, 6, 2]
     for token in range(6):
         rows, q, gates = draw(len(live))
-        out, _ = server.step(live, rows, q, gates)
+        out, _ = server.step(live, [(1, 0), (3, lengths[1])] + [(1, 0)] * (len(live) - 4), rows, q, gates)
         for i, r in enumerate(live):
-            history[r] = torch.cat([history[r], rows[i:i + 1]])
+            row = server.read(r, history[r].shape[0], 1) if eight else rows[i:i + 1]
+            history[r] = torch.cat([history[r], row])
             check(out[i], attention(layer, history[r], q[i]))
         if token == 1:  # request 5 takes its last token back
             server.release([5], [history[5].shape[0] - 1])
@@ -176,4 +202,4 @@ def main(seed=0, dev="cuda"):
 
 
 if __name__ == "__main__":
-    print(f"largest error against the 64-bit form, over the outputs' size: {main():.2e}")
+    print(f"largest error against the 64-bit form, over the outputs' size: {main():.2e}, with latents in 8 bits {main(eight=True):.2e}")
