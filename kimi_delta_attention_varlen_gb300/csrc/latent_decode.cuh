@@ -38,6 +38,7 @@ struct Params {
     float4 *pre_ml;                   // [rows of all entries]: m, l, l of the rounded probabilities
     float *pre;                       // [rows of all entries][dl], relative to m
     int32_t *item_rows;               // [grid]: rows of the item in slot 1 (of the prefixes' items)
+    const int32_t *shares_any;        // 0: no group has a prefix that is shared
 };
 
 __device__ __forceinline__ int64_t slot_of(const LatentDecodeArgs &a, int64_t r)
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
     const int32_t per = Form != kPrefix && p.rows < N ? p.rows : N;
     before_next();
     after_previous();
+    if (Form == kPrefix && *p.shares_any == 0) return;
     int32_t *const head_of = before, *const more_of = reinterpret_cast<int32_t *>(weight);  // until they are needed
     for (int32_t j = tid; j < shares; j += 256) {
         parts_of[j] = 1;

@@ -38,6 +38,7 @@ constexpr float kLazy = 8.f;   // log2 of the growth that forces a rescale
 struct Plan {  // in the workspace
     int32_t *tokens, *slot;  // [groups]: tokens of the prefix, block table row
     int32_t *base;           // [batch]: tokens before the entry's own
+    int32_t *any;            // whether a group has a prefix
 };
 
 struct SharedParams {
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(SharedParams s, int32_t ctas
 #pragma unroll
     for (int w = 0; w < 32; ++w) all += saved[w];
     const bool pays = all > kLaunches * ctas;
+    if (tid == 0) *s.plan.any = pays;
     for (int64_t g = warp; g < s.g.groups; g += 32) {
         int64_t from, to;
         entries_of(s, g, &from, &to);
@@ -214,6 +216,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
     const int cta = blockIdx.x;
 
+    before_next();
+    after_previous();
+    if (*sp.plan.any == 0) return;
     if (warp == 3) {
         tc::tmem_alloc(&tmem_base, 512);
         tc::tmem_relinquish();
@@ -226,10 +231,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         not_finite = 0;
         lowest[0] = lowest[1] = 0x7fffffff;
         fence_mbar_init();
-    }
-    before_next();
-    after_previous();
-    if (tid == 0) {
         p.item0[cta] = p.item1[cta] = -1;
     }
     // This CTA's share of the line, as in find_share(): items are the blocks of groups with a prefix.
@@ -744,7 +745,7 @@ Layout layout(int64_t batch, int64_t groups, int32_t L, int32_t h, int32_t dl)
     y.ml = y.lists + up256(12 * grid);
     y.part = y.ml + 2 * grid * N * 16;
     y.plan = y.part + 2 * grid * N * static_cast<size_t>(dl) * 4;
-    y.pre_ml = y.plan + up256(static_cast<size_t>(2 * groups + batch) * 4);
+    y.pre_ml = y.plan + up256(static_cast<size_t>(2 * groups + batch + 1) * 4);
     y.pre = y.pre_ml + up256(rows * 16);
     y.total = y.pre + rows * static_cast<size_t>(dl) * 4;
     return y;
@@ -775,6 +776,8 @@ template <int DL> cudaError_t launch(const LatentDecodeArgs &a, const SharedGrou
     s.plan.tokens = reinterpret_cast<int32_t *>(ws + y.plan);
     s.plan.slot = s.plan.tokens + g.groups;
     s.plan.base = s.plan.slot + g.groups;
+    s.plan.any = s.plan.base + a.batch;
+    p.shares_any = s.plan.any;
     Maps maps;
     const int64_t q_rows = a.batch * p.rows;
     if (!encode(&maps.q, a.q, C::D, q_rows, 1, C::D, q_rows * C::D, N) ||
