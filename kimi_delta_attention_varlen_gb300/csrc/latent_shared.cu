@@ -18,7 +18,7 @@
 //
 // What bounds it: shared memory.  A tile of 64 tokens x 64 rows moves 319 KB through it (operands of S 147, of O^T 98, the copy 74:
 // 2,500 cycles at 128 bytes each), and takes 3,430 cycles: the copies wait for the products' reads, and the ring has room for one
-// tile beside the one that is worked on.  64 requests of 32 heads on 32,768 tokens: 188 us of 232 us (apart: 344 us); 500 requests
+// tile beside the one that is worked on.  64 requests of 32 heads on 32,768 tokens: 188 us of 229 us (apart: 344 us); 500 requests
 // on seven system prompts of 3,000..6,001 tokens 212 us of 389 us (447 us); the rest's kernel then adds the prefix's sums, 64 KB a
 // request, which it loads a step ahead.  Tried and not kept: panels copied once for two CTAs of a cluster (multicast, an item of
 // 128 rows: 237 and 450 us where it was 233 and 446 then).
@@ -86,7 +86,7 @@ constexpr int64_t kTile32 = 3100, kTile64 = 3430, kEntry = 20000, kLaunches = 24
 
 // By one CTA, a group a warp.  Sharing pays where it saves more tiles' time than the joins and launches take.  Where it does not,
 // nothing is shared and each entry takes all of its tokens (measured both ways: 64 entries of 32 heads on 32,768 tokens 227 us
-// against 344 us apart; 8 on 4,133 tokens 44 us against 31 us with nothing shared).
+// against 344 us apart; 8 on 4,133 tokens 43 us against 29 us with nothing shared).
 __global__ void __launch_bounds__(1024) plan_kernel(SharedParams s, int32_t ctas)
 {
     __shared__ int64_t saved[32];

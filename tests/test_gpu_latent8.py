@@ -509,6 +509,52 @@ def test_write_read_and_attend_captured_in_a_graph():
             at += n[r]
 
 
+def strided(table):
+    """The same block table as a slice of a wider one, rows 5 entries further apart, whose other entries are no pages."""
+    wide = torch.full((table.shape[0], table.shape[1] + 5), 1 << 30, dtype=torch.int32, device=table.device)
+    wide[:, 2:2 + table.shape[1]] = table
+    return wide[:, 2:2 + table.shape[1]]
+
+
+def test_strided_block_tables():
+    dl, page, lens = 256, 16, [40, 0, 333]
+    cache, table, sl, rows = h8.paged8(lens, page, dl, seed=71)
+    q = queries(3, 2, 16, dl + 64, seed=71)
+    out, lse = run_decode8(q, cache, strided(table), sl, dl, SCALE)
+    assert_attention(out, lse, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, dl))
+    got = read_back(cache, strided(table), lens, page, dl, [0, 40, 373], [0, 2], None, 373)
+    assert torch.equal(got.double().cpu(), torch.cat([rows[0], rows[2]]))
+    x = torch.randn(7, dl + 64, generator=wl.generator(72, DEV), device=DEV).to(BF)
+    run_append(x, [0, 7], [2], strided(table), lens, cache, dl, page)
+    c, rope, scale = h8.quantise(x, dl)
+    got = read_back(cache, table, lens, page, dl, [0, 333], [2], None, 333)
+    assert torch.equal(got.double().cpu(), torch.cat([rows[2][:326], torch.cat([c, rope], 1) * scale[:, None]]))
+
+
+def test_calls_on_two_streams_at_once():
+    """Two decodes, each on a stream and a workspace of its own, again and again; and writes and reads of other requests between them."""
+    dl, sets = 512, []
+    for k in range(2):
+        lens = [3000 + 500 * k, 17, 900, 64]
+        cache, table, sl, rows = h8.paged8(lens, 64, dl, seed=80 + k)
+        q = queries(4, 1, 32, 576, seed=80 + k)
+        ws = torch.empty(kda.kda_latent_decode8_workspace_size(4, 1, 32, dl, 64), dtype=torch.uint8, device=DEV)
+        pt = kda.page_table_descriptor(table, sl, torch.ones(cache.shape[0], dtype=torch.int32, device=DEV), 64)
+        sets.append((lens, cache, table, sl, rows, q, ws, pt, torch.empty(4, 1, 32, dl, dtype=BF, device=DEV),
+                     torch.empty(900, 576, dtype=BF, device=DEV), torch.cuda.Stream()))
+    cu, req = torch.tensor([0, 900], dtype=torch.int32, device=DEV), torch.tensor([2], dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for lens, cache, table, sl, rows, q, ws, pt, out, back, st in sets:
+            kda.kda_latent_decode8(q, cache, table, sl, out, ws, latent_dim=dl, scale=SCALE, stream=st)
+            kda.kda_latent_read(cache, cu, req, pt, back, latent_dim=dl, stream=st)
+    torch.cuda.synchronize()
+    for lens, cache, table, sl, rows, q, ws, pt, out, back, st in sets:
+        assert kda.kda_prefill_workspace_status(ws) == 0
+        assert_attention(out, None, decode_reference(q, lambda r, n: rows[r][:n], lens, SCALE, dl))
+        assert torch.equal(back.double().cpu(), rows[2])
+
+
 def test_pages_of_bytes_are_copied():
     for page, gap in ((16, 0), (8, 32), (8, 5)):  # the last: pages that are not 16-byte aligned
         size = page * 644

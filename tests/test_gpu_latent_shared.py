@@ -431,6 +431,26 @@ def test_which_batches_share():
         assert far <= 2.0 ** -6 and (same_in_ballast or not torch.equal(among.view(torch.int16), plain.view(torch.int16)))
 
 
+def test_strided_block_tables_and_two_streams():
+    sets = []
+    for k in range(2):
+        cache, table, sl, rows, cu, shared = grouped([(600, [17, 90, 1]), (128 + 64 * k, [64, 5])], 64, 512, seed=90 + k, gap=64)
+        q = queries(5, 1, 32, 576, seed=90 + k)
+        cache, table, sl, cu, shared, q = with_ballast(cache, table, sl, cu, shared, q)
+        wide = torch.full((table.shape[0], table.shape[1] + 3), 1 << 30, dtype=torch.int32, device=DEV)
+        wide[:, 1:-2] = table
+        ws = torch.empty(kda.kda_latent_decode_shared_workspace_size(q.shape[0], 3, 1, 32, 512, 64), dtype=torch.uint8, device=DEV)
+        sets.append((cache, wide[:, 1:-2], sl, rows, cu, shared, q, ws, torch.empty(*q.shape[:3], 512, dtype=BF, device=DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for cache, table, sl, rows, cu, shared, q, ws, out, st in sets:
+            kda.kda_latent_decode_shared(q, cache, table, sl, cu, shared, out, ws, latent_dim=512, scale=SCALE, stream=st)
+    torch.cuda.synchronize()
+    for cache, table, sl, rows, cu, shared, q, ws, out, st in sets:
+        assert kda.kda_prefill_workspace_status(ws) == 0
+        assert_attention(out[:5], None, decode_reference(q[:5], lambda r, n: rows[r][:n], sl[:5].tolist(), SCALE, 512))
+
+
 def test_two_calls_queued_on_two_workspaces():
     sets = [grouped([(600, [17, 90, 1]), (128, [64, 5])], 64, 512, seed=s) for s in (15, 16)]
     qs = [queries(5, 1, 32, 576, seed=s) for s in (15, 16)]
