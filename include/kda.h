@@ -685,7 +685,7 @@ int kda_latent_append(const void *x, int64_t x_stride, int64_t total, const int3
  *   workspace kda_latent_decode_shared_workspace_size(...) bytes, 256-byte
  *             aligned (dl * 4 + 16 bytes for every query row among them).
  *             Errors beside those: KDA_ERR_SHAPE (groups < 1), _RANGE (groups
- *             >= 2^24).
+ *             >= 2^24, requests >= 2^31).
  * ---------------------------------------------------------------------- */
 size_t kda_latent_decode_shared_workspace_size(int64_t batch, int64_t groups, int32_t L, int32_t h,
                                                int32_t dl, int32_t dr);

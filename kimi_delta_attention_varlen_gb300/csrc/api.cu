@@ -511,7 +511,7 @@ int kda_latent_decode_shared(const void *q, int32_t io_dtype, int64_t batch, int
                                  requests, width, table_stride, seq_lens, req, idx_type, out, lse, workspace, &a);
     if (rc != KDA_OK) return rc;
     if (groups < 1) return KDA_ERR_SHAPE;
-    if (groups >= (1 << 24)) return KDA_ERR_RANGE;
+    if (groups >= (1 << 24) || requests >= (INT64_C(1) << 31)) return KDA_ERR_RANGE;  // the plan's rows are 32-bit
     if (batch == 0) return KDA_OK;
     if (cu_groups == nullptr || shared == nullptr) return KDA_ERR_NULL;
     if (!aligned(cu_groups, 4) || !aligned(shared, 4)) return KDA_ERR_ALIGN;

@@ -70,7 +70,7 @@ def test_decode_refusals(L, name):
     assert need > 0 and call(ws_bytes=need - 1) == WORKSPACE and call(ws=A + 128) == WORKSPACE
     assert call(batch=0, q=None, out=None, ws=None, cu=None, shared=None) == OK
     if not eight:
-        assert call(groups=0) == SHAPE and call(groups=-1) == SHAPE and call(groups=1 << 24) == RANGE
+        assert call(groups=0) == SHAPE and call(groups=-1) == SHAPE and call(groups=1 << 24) == RANGE and call(requests=1 << 31) == RANGE
 
 
 def test_workspace_sizes(L):
