@@ -270,34 +270,50 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
         const int32_t c = first[lo], parts = parts_of[lo], item = p.item1[c];
         const int32_t left = Form == kPrefix ? p.item_rows[c] : p.rows - item % p.rows;  // rows from the item's first on
         auto at = [&](int32_t j, int32_t row) { return (static_cast<int64_t>(2) * (c + j) + (j == 0 ? 1 : 0)) * N + row; };
-        // a row's sum o relative to m, with the sums l and lr
-        auto store = [&](int32_t row, int32_t d, float4 o, float m, float l, float lr) {
-            const int64_t at = item + row;
+        // A row's sum o relative to m, with the sums l and lr, to where it goes; (kOwn) y and ml: the prefix's part.
+        const bool joined = Form == kOwn && p.base[item / p.rows] > 0;
+        struct Weights {
+            float own, prefix;
+        };
+        auto prefix_sums = [&](int32_t row) { return joined ? p.pre_ml[item + row] : make_float4(-INFINITY, 0.f, 0.f, 0.f); };
+        auto prefix_part = [&](int32_t row, int32_t d) {
+            return joined ? reinterpret_cast<const float4 *>(p.pre + (static_cast<int64_t>(item) + row) * DL)[d] : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        auto weigh = [&](int32_t row, bool first, float m, float l, float lr, float4 ml) {
+            Weights w{1.f, 0.f};
             if (Form == kPrefix) {
-                if (lr == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);  // 0 times what is not finite
-                reinterpret_cast<float4 *>(p.pre + at * DL)[d] = o;
-                if (d == 0) p.pre_ml[at] = make_float4(m, l, lr, 0.f);
-                return;
+                if (first) p.pre_ml[item + row] = make_float4(m, l, lr, 0.f);
+                w.own = lr == 0.f ? 0.f : 1.f;
+                return w;
             }
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            float f = 1.f, fy = 0.f;
-            if (Form == kOwn && p.base[at / p.rows] > 0) {
-                const float4 ml = p.pre_ml[at];
+            if (joined) {
                 const float top = fmaxf(m, ml.x);
-                f = rebase(m, top), fy = rebase(ml.x, top);
-                l = l * f + ml.y * fy, lr = lr * f + ml.z * fy, m = top;
-                y = reinterpret_cast<const float4 *>(p.pre + at * DL)[d];
+                w.own = rebase(m, top), w.prefix = rebase(ml.x, top);
+                l = l * w.own + ml.y * w.prefix, lr = lr * w.own + ml.z * w.prefix, m = top;
             }
             const float inv = inverse(lr);
-            f *= inv, fy *= inv;
-            reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.a.out) + at * DL)[d] =
-                Form == kOwn ? make_uint2(pack_bf16x2(o.x * f + y.x * fy, o.y * f + y.y * fy), pack_bf16x2(o.z * f + y.z * fy, o.w * f + y.w * fy))
-                             : make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
-            if (d == 0 && p.a.lse != nullptr) p.a.lse[at] = log_sum(m, l);
+            w.own *= inv, w.prefix *= inv;
+            if (first && p.a.lse != nullptr) p.a.lse[item + row] = log_sum(m, l);
+            return w;
+        };
+        auto store = [&](int32_t row, int32_t d, float4 o, Weights w, float4 y) {
+            const int64_t at = static_cast<int64_t>(item) + row;
+            if (Form == kPrefix) {
+                if (w.own == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);  // nothing is seen: 0 times what is not finite
+                reinterpret_cast<float4 *>(p.pre + at * DL)[d] = o;
+                return;
+            }
+            o.x *= w.own, o.y *= w.own, o.z *= w.own, o.w *= w.own;
+            if (joined) o.x = fmaf(y.x, w.prefix, o.x), o.y = fmaf(y.y, w.prefix, o.y), o.z = fmaf(y.z, w.prefix, o.z), o.w = fmaf(y.w, w.prefix, o.w);
+            reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.a.out) + at * DL)[d] = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
         };
         if (parts <= kFewParts) {
             const int32_t row = (unit - before[lo]) * 8 + warp;
             if (row >= per || row >= left) continue;
+            const float4 prefix = prefix_sums(row);
+            float4 y[kLanes / 32];
+#pragma unroll
+            for (int q = 0; q < kLanes / 32; ++q) y[q] = prefix_part(row, lane + 32 * q);
             float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
             if (lane < parts) ml = p.ml[at(lane, row)];
             float m = ml.x;
@@ -325,8 +341,9 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
                     o[q].x += fj * y.x, o[q].y += fj * y.y, o[q].z += fj * y.z, o[q].w += fj * y.w;
                 }
             }
+            const Weights w = weigh(row, lane == 0, m, l, lr, prefix);
 #pragma unroll
-            for (int q = 0; q < kLanes / 32; ++q) store(row, lane + 32 * q, o[q], m, l, lr);
+            for (int q = 0; q < kLanes / 32; ++q) store(row, lane + 32 * q, o[q], w, y[q]);
             continue;
         }
         const int32_t row = unit - before[lo], sub = tid / kLanes, d = tid % kLanes;
@@ -373,7 +390,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(Params p, int32_t shar
                 const float4 y = acc[q][d];
                 o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
             }
-            store(row, d, o, top, sum[0], sum[1]);
+            store(row, d, o, weigh(row, d == 0, top, sum[0], sum[1], prefix_sums(row)), prefix_part(row, d));
         }
         __syncthreads();  // weight, sum and acc may be written again
     }
