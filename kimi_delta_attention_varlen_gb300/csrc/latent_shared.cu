@@ -13,8 +13,9 @@
 //
 // The prefixes' kernel has the products, panels and rings of latent_decode.cu at 64 rows (S = Q X^T, O^T = C^T P^T, tiles of 64
 // tokens).  Its rows are consecutive rows of q, its mask a limit of each row's own: b, or what the row's query token sees where
-// that is less (a request that ends in the prefix).  Eight softmax warps, two for the same 16 rows with half of a tile's tokens
-// each, since the ring has room for two tiles and a tile keeps its place until its second product is done.
+// that is less (a request that ends in the prefix).  An item of which a row sees at most a tile of tokens takes what the rounding of
+// its first tile's weights leaves off in a second pass, as latent_decode.cu does.  Eight softmax warps, two for the same 16 rows with
+// half of a tile's tokens each, since the ring has room for two tiles and a tile keeps its place until its second product is done.
 //
 // What bounds it: shared memory.  A tile of 64 tokens x 64 rows moves 319 KB through it (operands of S 147, of O^T 98, the copy 74:
 // 2,500 cycles at 128 bytes each), and takes 3,430 cycles: the copies wait for the products' reads, and the ring has room for one
@@ -161,7 +162,6 @@ struct PrefixWalk {
     __device__ int32_t valid() const { const int64_t v = rows - static_cast<int64_t>(block) * N; return v < N ? static_cast<int32_t>(v) : N; }
     __device__ bool first() const { return tile == 0; }
     __device__ bool last() const { return tile + 1 == tiles; }
-    __device__ bool twice() const { return n <= T; }  // all rows may see few tokens only
     __device__ void next(const SharedParams &s)
     {
         if (++tile < tiles) return;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     float *const worth = corr;
     __shared__ float2 top[N];              // by the second half: its maximum; at the end its l and lr
     __shared__ uint32_t grown[2];          // rows that are rescaled
-    __shared__ int32_t lowest[2];          // fewest tokens that a row of the segment sees, by parity of the segment
+    __shared__ int32_t lowest[2];          // fewest tokens that a row of the segment sees (of those that see any), by parity of the segment
     int64_t *const sums = reinterpret_cast<int64_t *>(kept), *const counts = sums + kThreads / 32;  // at the start
     __shared__ PrefixEdge edge[2];
     const int tid = threadIdx.x, lane = tid & 31;
@@ -425,17 +425,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         const uint32_t base = smem_u32(smem);
         const uint64_t p_desc = tc::sdesc_sw128(base + C::OFF_P, 16, 1024),
                        val_desc = tc::sdesc_sw128(base + C::OFF_RING, C::PB, 1024);
-        int slot = 0;
+        int slot = 0, segs = 0;
         uint32_t passes = 0;
         int32_t tile0 = w.tile;  // the segment's first
         bool ok = true;
         for (int32_t i = 0; i < total && ok; ++i) {
+            if (i == 0 || w.first()) ++segs;
             if (w.first()) tile0 = 0;
             const uint32_t more = __all_sync(0xffffffffu, ((w.tile - tile0) & (kSumTiles - 1)) == 0) ? 0u : 1u;
-            const bool two = __all_sync(0xffffffffu, w.twice()) != 0;
-            for (int pass = two ? 0 : 1; pass < 2; ++pass, ++passes) {
-                if (!(ok = wait(&bar.p, passes & 1))) break;
-                tc::fence_after_sync();
+            const bool begins = __all_sync(0xffffffffu, w.first()) != 0;
+            if (!(ok = wait(&bar.p, passes++ & 1))) break;
+            tc::fence_after_sync();
+            // (written before the softmax arrived, and again only after this product has arrived there)
+            bool again = begins && __all_sync(0xffffffffu, lowest[segs & 1] <= T) != 0;
+            for (uint32_t add = more;; add = 1u) {
                 if (elect_one()) {
                     int sl = slot;
 #pragma unroll
@@ -443,14 +446,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                         const uint64_t v = val_desc + sl * (2 * C::PB >> 4);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            tc::mma_bf16(tmem + mt * N, v + ks * 128, p_desc + ks * 2, kId, ks > 0 || (two && pass == 1) ? 1u : more);
-                        if (pass == 1) tc::commit(&bar.empty[sl]);
+                            tc::mma_bf16(tmem + mt * N, v + ks * 128, p_desc + ks * 2, kId, ks > 0 ? 1u : add);
+                        if (!again) tc::commit(&bar.empty[sl]);
                         sl = sl + 1 == C::RING ? 0 : sl + 1;
                     }
                     tc::commit(&bar.o);
                 }
                 __syncwarp();
+                if (!again || !(ok = wait(&bar.p, passes++ & 1))) break;
+                tc::fence_after_sync();
+                again = false;
             }
+            if (!ok) break;
             slot = (slot + C::PAIRS) % C::RING;
             w.next(sp);
         }
@@ -697,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             tc::fence_before_sync();
             mbar_arrive(&bar.p);
             ++passes;
-            if (w.twice()) {  // the second pass: what the rounding left off
+            if (w.first() && low <= T) {  // the second pass: what the rounding left off
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float base = m[e] == -INFINITY ? 0.f : m[e];

@@ -1,0 +1,75 @@
+"""Rows of a shared batch whose own limit is not the prefix's (kda_latent_decode_shared): members that are shorter than what their group has
+in common, empty entries among them, and what the decision to share makes of those."""
+import math
+
+import pytest
+import torch
+
+import kimi_delta_attention_varlen_gb300 as kda
+from tests.latent_helpers import assert_attention, decode_reference
+from tests.test_gpu_latent import paged_latents, poisoned, queries
+from tests.test_gpu_latent_shared import run_both, run_shared, with_ballast
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+SCALE = 192 ** -0.5
+I32 = dict(dtype=torch.int32, device=DEV)
+
+
+def run_plain(q, cache, table, sl, dl, scale=SCALE, req=None):
+    R, L, H, D = q.shape
+    out, lse = poisoned(R, L, H, dl), torch.full((R, L, H), math.nan, device=DEV)
+    ws = torch.empty(kda.kda_latent_decode_workspace_size(R, L, H, dl, D - dl), dtype=torch.uint8, device=DEV)
+    kda.kda_latent_decode(q, cache, table, sl, out, ws, latent_dim=dl, scale=scale, req=req, lse=lse)
+    torch.cuda.synchronize()
+    assert kda.kda_prefill_workspace_status(ws) == 0
+    return out, lse
+
+
+def same_bits(a, b):
+    return torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+def three_bf16(x):
+    """A number as a sum of three bf16 values (its 24 leading bits)."""
+    parts = []
+    for _ in range(3):
+        parts.append(float(torch.tensor(x).to(BF)))
+        x -= parts[-1]
+    return parts
+
+
+# Rows that see at most 64 tokens take what the rounding of their weights leaves off, in whichever kernel.  Two tokens hold the weight: z = 0 and
+# ln w with w next to (1 + 2^-8) / 2, halfway between two bf16 values, and latents a and -2 a, so that the output is about 2^-8.6 of a.  The
+# output's rounding is then 2^-8 of that.  Weights in two parts are off by 2^-16 of themselves, the scores (fp32, below 1) and the approximate
+# exponential by less: 2^-13 sum p |x| covers them eightfold.  A weight rounded once is off by 2^-8, the output by 2^-9 sum p |x|.
+@pytest.mark.parametrize("dl", [512, 256])
+@pytest.mark.parametrize("L,heads,lens", [(1, 16, [645, 2, 640, 3, 61, 64, 2, 1]), (31, 1, [94, 80, 33, 65]), (2, 16, [300, 65, 66, 3])])
+def test_rows_that_see_few_tokens_of_a_long_prefix(L, heads, lens, dl):
+    page, longest = 16, max(lens)
+    cache, table, _, rows = paged_latents([longest], page, dl, seed=L)
+    x = rows[0].clone()
+    x[:, dl:] = 0
+    x[2:, dl + 63] = -20.0
+    x[1, :dl] = -2 * x[0, :dl]
+    for h in range(heads):
+        w = (1 + 2.0 ** -8) / 2 * (1 + (-1) ** h * (h + 1) * 2.0 ** -13)
+        x[1, dl + 3 * h:dl + 3 * h + 3] = torch.tensor(three_bf16(math.log(w)), device=DEV)
+    for j in range(-(-longest // page)):
+        part = x[j * page:(j + 1) * page]
+        cache[table[0, j].long(), 0, :part.shape[0]] = part
+    q = torch.zeros(len(lens), L, heads, dl + 64, dtype=BF, device=DEV)
+    q[..., dl + 63] = 1
+    for h in range(heads):
+        q[:, :, h, dl + 3 * h:dl + 3 * h + 3] = 1
+    tables = table.expand(len(lens), -1).contiguous()
+    ref = decode_reference(q, lambda r, n: x[:n], lens, 1.0, dl)
+    few = torch.tensor([[1 < n - (L - 1 - t) <= 64 for t in range(L)] for n in lens])
+    assert few.sum() >= 3
+    for k, (out, lse) in enumerate(run_both(q, cache, tables, torch.tensor(lens, **I32), torch.tensor([0, len(lens)], **I32),
+                                            torch.tensor([10 ** 6], **I32), dl, scale=1.0)):
+        assert_attention(out, lse, ref, f"L {L} {'with ballast' if k else 'alone'}")
+        want, mag = ref[0][few], ref[1][few]
+        over = (out.double().cpu()[few] - want).abs() - (2.0 ** -8 * want.abs() + 2.0 ** -13 * mag)
+        assert over.max() <= 0, f"{'with ballast' if k else 'alone'}: {float(over.max()):.3e} over its tolerance"
