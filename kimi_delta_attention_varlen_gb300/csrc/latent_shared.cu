@@ -84,26 +84,34 @@ __device__ __forceinline__ void entries_of(const SharedParams &s, int64_t g, int
 // What a tile of 64 tokens takes a CTA, in cycles: with up to 32 rows of an entry, and with 64 rows (of an entry or of a
 // prefix).  What joining the prefix's part takes an entry's group of rows, and what the launches take the GPU, a CTA.
 constexpr int64_t kTile32 = 3100, kTile64 = 3430, kEntry = 20000, kLaunches = 24000;
+constexpr int kPlanThreads = 512;
+constexpr int kLengths = 8192;  // entries whose lengths the plan loads at once; of those behind them each when it is needed
 
-// By one CTA, a group a warp.  Sharing pays where it saves more tiles' time than the joins and launches take.  Where it does not,
+// By one CTA, a group a warp.  Sharing pays where it saves more tiles' time than the joins and launches take; an entry saves the tiles
+// that it would take apart, so one that is shorter than the prefix saves few and an empty one none.  Where it does not pay,
 // nothing is shared and each entry takes all of its tokens (measured both ways: 64 entries of 32 heads on 32,768 tokens 227 us
 // against 344 us apart; 8 on 4,133 tokens 43 us against 29 us with nothing shared).
-__global__ void __launch_bounds__(1024) plan_kernel(SharedParams s, int32_t ctas)
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(SharedParams s, int32_t ctas)
 {
-    __shared__ int64_t saved[32];
+    constexpr int kWarps = kPlanThreads / 32;
+    __shared__ int64_t saved[kWarps];
+    __shared__ int32_t lengths[kLengths];
     before_next();
     after_previous();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const LatentDecodeArgs &a = s.p.a;
     if (tid == 0) *s.p.status = 0;  // of all the kernels of the call
+    for (int64_t r = tid; r < a.batch && r < kLengths; r += blockDim.x) lengths[r] = length_of(a, slot_of(a, r));
+    __syncthreads();
+    auto length = [&](int64_t r) { return r < kLengths ? lengths[r] : length_of(a, slot_of(a, r)); };
     const int64_t own = s.p.rows <= 32 ? 32 : 64;  // (one group of rows: entries of 64 rows do not come here)
     int64_t mine = 0;
-    for (int64_t g = warp; g < s.g.groups; g += 32) {
+    for (int64_t g = warp; g < s.g.groups; g += kWarps) {
         int64_t from, to;
         entries_of(s, g, &from, &to);
         int64_t best = -1;  // the longest member, of these the first
         for (int64_t r = from + lane; r < to; r += 32) {
-            const int64_t key = static_cast<int64_t>(length_of(a, slot_of(a, r))) << 31 | (0x7fffffff - (r - from));
+            const int64_t key = static_cast<int64_t>(length(r)) << 31 | (0x7fffffff - (r - from));
             best = key > best ? key : best;
         }
 #pragma unroll
@@ -116,19 +124,26 @@ __global__ void __launch_bounds__(1024) plan_kernel(SharedParams s, int32_t ctas
         if (lane == 0) {
             s.plan.tokens[g] = static_cast<int32_t>(b);
             s.plan.slot[g] = b > 0 ? static_cast<int32_t>(slot_of(a, from + (0x7fffffff - (best & 0x7fffffff)))) : 0;
-            const int64_t rows = (to - from) * s.p.rows;
-            if (b > 0)
-                mine += (b + T - 1) / T * ((to - from) * (own == N ? kTile64 : kTile32) - (rows + N - 1) / N * kTile64) - (to - from) * kEntry;
         }
+        if (b == 0) continue;
+        int64_t tiles = 0;  // that the entries do not take themselves
+        for (int64_t r = from + lane; r < to; r += 32) {
+            const int32_t n = length(r), before = static_cast<int32_t>(b);
+            tiles += tiles_of(n) - tiles_of(n > before ? n - before : 0);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        const int64_t rows = (to - from) * s.p.rows;
+        mine += tiles * (own == N ? kTile64 : kTile32) - (b + T - 1) / T * ((rows + N - 1) / N) * kTile64 - (to - from) * kEntry;
     }
     if (lane == 0) saved[warp] = mine;
     __syncthreads();
     int64_t all = 0;
 #pragma unroll
-    for (int w = 0; w < 32; ++w) all += saved[w];
+    for (int w = 0; w < kWarps; ++w) all += saved[w];
     const bool pays = all > kLaunches * ctas;
     if (tid == 0) *s.plan.any = pays;
-    for (int64_t g = warp; g < s.g.groups; g += 32) {
+    for (int64_t g = warp; g < s.g.groups; g += kWarps) {
         int64_t from, to;
         entries_of(s, g, &from, &to);
         __syncwarp();
@@ -790,7 +805,7 @@ template <int DL> cudaError_t launch(const LatentDecodeArgs &a, const SharedGrou
     if (!encode(&maps.q, a.q, C::D, q_rows, 1, C::D, q_rows * C::D, N) ||
         !encode(&maps.cache, a.cache.data, C::D, a.page, a.cache.n_rows, C::D, a.cache.row_stride, p.box_rows))
         return cudaErrorInvalidValue;
-    cudaError_t e = launch_overlapped(plan_kernel, dim3(1), dim3(1024), 0, st, s, grid);
+    cudaError_t e = launch_overlapped(plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, s, grid);
     if (e != cudaSuccess) return e;
     auto kern = prefix_kernel<DL>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;

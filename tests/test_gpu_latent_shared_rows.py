@@ -73,3 +73,26 @@ def test_rows_that_see_few_tokens_of_a_long_prefix(L, heads, lens, dl):
         want, mag = ref[0][few], ref[1][few]
         over = (out.double().cpu()[few] - want).abs() - (2.0 ** -8 * want.abs() + 2.0 ** -13 * mag)
         assert over.max() <= 0, f"{'with ballast' if k else 'alone'}: {float(over.max()):.3e} over its tolerance"
+
+
+@pytest.mark.parametrize("dl", [512, 256])
+@pytest.mark.parametrize("others", ["invalid", "empty", "short"])
+def test_members_that_save_nothing_do_not_make_a_group_share(others, dl):
+    """One member on 32,768 tokens among 63 that see 64 tokens or none: there is nothing to compute together, and the call is the plain one's bit
+    for bit.  (With 64 such members it is not: the next test.)"""
+    R, n, page, H = 64, 32768, 64, 32
+    cache, table, _, rows = paged_latents([n], page, dl, seed=40)
+    tables = table.expand(R, -1).contiguous()
+    lens, pick = [n] + [64] * (R - 1), list(range(R))
+    if others == "empty":
+        lens[1:] = [0] * (R - 1)
+    elif others == "invalid":
+        pick[1:] = [-1] * (R - 1)
+    q = queries(R, 1, H, dl + 64, seed=40)
+    sl, req = torch.tensor(lens, **I32), torch.tensor(pick, **I32)
+    got = run_shared(q, cache, tables, sl, torch.tensor([0, R], **I32), torch.tensor([n], **I32), dl, req=req)
+    assert same_bits(got, run_plain(q, cache, tables, sl, dl, req=req))
+    seen = [m if p >= 0 else 0 for m, p in zip(lens, pick)]
+    some = [0, 1, 63]
+    ref = decode_reference(q[some], lambda i, m: rows[0][:m], [seen[i] for i in some], SCALE, dl)
+    assert_attention(got[0][some], got[1][some], ref, others)
