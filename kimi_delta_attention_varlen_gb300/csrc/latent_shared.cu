@@ -218,11 +218,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) Bars<C> bar;
     __shared__ uint32_t tmem_base;
-    __shared__ int32_t not_finite;         // segments (from 1) of the last value that was taken out
+    __shared__ uint32_t taken_out[kSumTiles / 32];  // tiles that values were taken out of, since the sums began (a bit a tile)
     __shared__ __align__(8) float kept[3][N];  // what was set aside: maximum that it is relative to, l, lr
     __shared__ float corr[N];              // of the rows that grew; at a segment's end: worth of what was set aside
     float *const worth = corr;
-    __shared__ float2 top[N];              // by the second half: its maximum; at the end its l and lr
+    __shared__ float2 top[N];              // the halves' maxima; at the end the second half's l and lr, then (x) what a row sees
     __shared__ uint32_t grown[2];          // rows that are rescaled
     __shared__ int32_t lowest[2];          // fewest tokens that a row of the segment sees (of those that see any), by parity of the segment
     int64_t *const sums = reinterpret_cast<int64_t *>(kept), *const counts = sums + kThreads / 32;  // at the start
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         for (int j = 0; j < C::ROPE; ++j) mbar_init(&bar.rope_full[j], 1), mbar_init(&bar.rope_empty[j], 1);
         mbar_init(&bar.q_full, 1), mbar_init(&bar.q_free, 1), mbar_init(&bar.p, kSoft), mbar_init(&bar.o, 1);
         for (int j = 0; j < 2; ++j) mbar_init(&bar.s[j], 1), mbar_init(&bar.s_free[j], kSoft), mbar_init(&bar.drain[j], 1);
-        not_finite = 0;
+        for (int j = 0; j < kSumTiles / 32; ++j) taken_out[j] = 0;
         lowest[0] = lowest[1] = 0x7fffffff;
         fence_mbar_init();
         p.item0[cta] = p.item1[cta] = -1;
@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     if (begun) sum = fmaf(kept[1][row], back, sum), sum_r = fmaf(kept[2][row], back, sum_r);
                     kept[0][row] = m[e], kept[1][row] = sum, kept[2][row] = sum_r;
                     worth[row] = back;
+                    top[row].x = __int_as_float(seen[e]);
                     if (end && row < w.valid()) {
                         if (whole) p.pre_ml[w.first_row() + row] = make_float4(m[e], sum, sum_r, 0.f);
                         else p.ml[part * N + row] = make_float4(m[e], sum, sum_r, 0.f);
@@ -518,7 +519,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             tc::fence_after_sync();
             soft_any<kSoft>(false);  // worth and kept are complete
             const int valid = w.valid(), dim = 32 * quad + lane;
-            const bool taken = end && not_finite == segments;
+            uint32_t taken = 0;
+#pragma unroll
+            for (int j = 0; j < kSumTiles / 32; ++j) taken |= taken_out[j];
+            const int32_t begin = end ? w.tile - ((w.tile - tile0) & (kSumTiles - 1)) : w.tile - kSumTiles;  // tile that the sums began with
             float *to = end && whole ? p.pre + w.first_row() * DL : p.part + part * N * DL;
             const float *aside = p.part + part * N * DL;
 #pragma unroll 1
@@ -532,25 +536,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     for (int e = 0; e < 16; ++e)
                         o[e] = __float_as_uint(fmaf(aside[(row0 + e) * DL + mt * 128 + dim], worth[row0 + e], __uint_as_float(o[e])));
                 }
-                if (taken) {  // values that were taken out, to the rows that see them
-                    const int32_t last = min(w.n, (w.tile + 1) * T);
-                    for (int32_t tok = max(low, tile0 * T); tok < last; ++tok) {
-                        const int32_t e = p.a.block_table[w.slot * p.a.table_stride + tok / p.a.page];
-                        if (e < 0 || e >= p.a.cache.n_rows) continue;
-                        const float x = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.a.cache.data)[
-                            e * p.a.cache.row_stride + tok % p.a.page * C::D + mt * 128 + dim]);
-                        if (isfinite(x)) continue;
-#pragma unroll 1
-                        for (int q = 0; q < 16; ++q) {
-                            const int64_t f = w.first_row() + row0 + q, r = f / p.rows;
-                            if (row0 + q < valid && tok < length_of(p.a, slot_of(p.a, r)) - (p.a.L - 1 - static_cast<int32_t>(f % p.rows) / p.a.h)) {
+                // Values that were taken out, to the rows that see them: of those tiles alone and eight loads at a time, since every
+                // other warp's waits run while this lasts (all of 256 tiles: some 20 ms of their second).
+                for (int j = 0; taken != 0 && j < kSumTiles / 32; ++j)
+                    for (uint32_t bits = taken_out[j]; bits != 0; bits &= bits - 1) {
+                        const int32_t t0 = (begin + 32 * j + __ffs(bits) - 1) * T, last = min(w.n, t0 + T);
+                        for (int32_t tok = t0; tok < last; tok += 8) {  // within a page
+                            const int32_t e = p.a.block_table[w.slot * p.a.table_stride + tok / p.a.page];
+                            if (tok + 8 <= low || e < 0 || e >= p.a.cache.n_rows) continue;
+                            const __nv_bfloat16 *from = static_cast<const __nv_bfloat16 *>(p.a.cache.data) + e * p.a.cache.row_stride +
+                                                        tok % p.a.page * C::D + mt * 128 + dim;
+                            float x[8];
 #pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    if (k == q) o[k] = __float_as_uint(__uint_as_float(o[k]) + x);
+                            for (int k = 0; k < 8; ++k) x[k] = __bfloat162float(from[k * C::D]);
+#pragma unroll 1
+                            for (int k = 0; k < 8; ++k) {
+                                float bad = x[0];
+#pragma unroll
+                                for (int u = 1; u < 8; ++u) bad = u == k ? x[u] : bad;
+                                if (isfinite(bad) || tok + k < low) continue;
+#pragma unroll
+                                for (int q = 0; q < 16; ++q)
+                                    if (tok + k < __float_as_int(top[row0 + q].x)) o[q] = __float_as_uint(__uint_as_float(o[q]) + bad);
                             }
                         }
                     }
-                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     if (!end || row0 + e < valid) {
@@ -560,7 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     }
             }
             tc::fence_before_sync();
-            soft_any<kSoft>(false);  // worth and kept may be written again
+            soft_any<kSoft>(false);  // worth, kept, top and taken_out may be written again
+            if (st < kSumTiles / 32) taken_out[st] = 0;
         };
         // a thread that gave up goes on without waiting: all of them meet at every barrier
         for (int32_t i = 0; i < total; ++i) {
@@ -695,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     if (behind) {
                         *x = make_uint4(0u, 0u, 0u, 0u);
                     } else if (bad.x | bad.y | bad.z | bad.w) {
-                        not_finite = segments;
+                        const int32_t k = (w.tile - tile0) & (kSumTiles - 1);
+                        atomicOr(&taken_out[k >> 5], 1u << (k & 31));
                         *x = make_uint4(u.x & ~bad.x, u.y & ~bad.y, u.z & ~bad.z, u.w & ~bad.w);
                     }
                 }

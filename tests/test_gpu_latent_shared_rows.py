@@ -96,3 +96,20 @@ def test_members_that_save_nothing_do_not_make_a_group_share(others, dl):
     some = [0, 1, 63]
     ref = decode_reference(q[some], lambda i, m: rows[0][:m], [seen[i] for i in some], SCALE, dl)
     assert_attention(got[0][some], got[1][some], ref, others)
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_values_of_a_long_prefix_that_a_short_member_does_not_see(bad):
+    """Sixty-three entries on 3.2 million tokens (the same 50 pages over and over) with a value that is not finite in every fiftieth page, and one of
+    40 tokens before the first of them: its output stays finite, and no wait runs out over the others'."""
+    page, pages, times, H, dl, R = 64, 50, 1000, 32, 512, 64
+    cache, table, _, rows = paged_latents([page * pages], page, dl, seed=53)
+    cache[table[0, 20].long(), 0, 5, [9, 300]] = bad
+    tables = table[:, :pages].repeat(R, times).contiguous()
+    n = [page * pages * times] * R
+    n[17] = 40
+    q = queries(R, 1, H, dl + 64, seed=53)
+    out, lse = run_shared(q, cache, tables, torch.tensor(n, **I32), torch.tensor([0, R], **I32), torch.tensor([n[0]], **I32), dl)
+    others = [r for r in range(R) if r != 17]
+    assert not torch.isfinite(out[others][..., [9, 300]]).any()
+    assert_attention(out[[17]], lse[[17]], decode_reference(q[[17]], lambda r, m: rows[0][:m], [40], SCALE, dl))
