@@ -82,15 +82,23 @@ __device__ __forceinline__ void entries_of(const SharedParams &s, int64_t g, int
 }
 
 // What a tile of 64 tokens takes a CTA, in cycles: with up to 32 rows of an entry, and with 64 rows (of an entry or of a
-// prefix).  What joining the prefix's part takes an entry's group of rows, and what the launches take the GPU, a CTA.
-constexpr int64_t kTile32 = 3100, kTile64 = 3430, kEntry = 20000, kLaunches = 24000;
+// prefix); alike for latents of 256 and of 512, whose tiles wait for the same softmax.  What comes with a block of 64 rows of a prefix
+// whatever its length, what joining the prefix's part takes an entry of 32 rows of 512 (in proportion to both), and what launches and
+// joins take the GPU, a CTA.
+constexpr int64_t kTile32 = 3100, kTile64 = 3430, kItem = 4 * kTile64, kEntry = 4000;
+__host__ __device__ constexpr int64_t launches(int32_t dl) { return dl == 512 ? 36000 : 20000; }
+// In a share of the prefixes' line an item takes its tiles and this many more (7 prompts of 427..27,485 tokens, 199 entries of 40 heads:
+// 186, 167, 171 and 174 us with 3, 6, 9 and 12; one long prefix alike within 2 %).
+constexpr int kPrefixUnits = 6;
 constexpr int kPlanThreads = 512;
 constexpr int kLengths = 8192;  // entries whose lengths the plan loads at once; of those behind them each when it is needed
 
 // By one CTA, a group a warp.  Sharing pays where it saves more tiles' time than the joins and launches take; an entry saves the tiles
 // that it would take apart, so one that is shorter than the prefix saves few and an empty one none.  Where it does not pay,
 // nothing is shared and each entry takes all of its tokens (measured both ways: 64 entries of 32 heads on 32,768 tokens 227 us
-// against 344 us apart; 8 on 4,133 tokens 43 us against 29 us with nothing shared).
+// against 344 us apart; 8 on 4,133 tokens 43 us against 29 us with nothing shared).  752 batches of 1 to 56 rows an entry, latents of 256
+// and 512, one to seven prefixes of 200 to 39,000 tokens under 2 to 256 entries, each timed both ways: but for five of them the rule
+// takes the faster side or loses less than 5 % (11 % at the most, 0.1 % on average).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(SharedParams s, int32_t ctas)
 {
     constexpr int kWarps = kPlanThreads / 32;
@@ -134,14 +142,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(SharedParams s, int3
 #pragma unroll
         for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
         const int64_t rows = (to - from) * s.p.rows;
-        mine += tiles * (own == N ? kTile64 : kTile32) - (b + T - 1) / T * ((rows + N - 1) / N) * kTile64 - (to - from) * kEntry;
+        mine += tiles * (own == N ? kTile64 : kTile32) - (rows + N - 1) / N * ((b + T - 1) / T * kTile64 + kItem) -
+                rows * a.dl * kEntry / (32 * 512);
     }
     if (lane == 0) saved[warp] = mine;
     __syncthreads();
     int64_t all = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) all += saved[w];
-    const bool pays = all > kLaunches * ctas;
+    const bool pays = all > launches(a.dl) * ctas;
     if (tid == 0) *s.plan.any = pays;
     for (int64_t g = warp; g < s.g.groups; g += kWarps) {
         int64_t from, to;
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         w.g = g;
         w.load(sp);
         *items = w.n > 0 ? w.blocks() : 0;
-        return w.tiles + kItemUnits;
+        return w.tiles + kPrefixUnits;
     };
     int64_t mine = 0, my_items = 0;
     for (int64_t g = g_lo; g < g_hi; ++g) {
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int64_t at = shares > 0 && cta + e <= shares ? all * (cta + e) / shares : all;
-        if (tid == 0 && at == all) edge[e] = PrefixEdge{0, all - kItemUnits * all_i, 0, 0};
+        if (tid == 0 && at == all) edge[e] = PrefixEdge{0, all - kPrefixUnits * all_i, 0, 0};
         if (at >= before && at < before + mine) {
             int64_t left = at - before, done = before_i, g = g_lo, items;
             int32_t u;
@@ -294,9 +303,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 left -= items * u, done += items;
             }
             const int32_t block = static_cast<int32_t>(left / u), x = static_cast<int32_t>(left % u);
-            const int32_t tile = x > kItemUnits ? x - kItemUnits : 0;
-            // tiles before: units before the item, less kItemUnits for each item before it
-            edge[e] = PrefixEdge{g, at - x + tile - kItemUnits * (done + block), block, tile};
+            const int32_t tile = x > kPrefixUnits ? x - kPrefixUnits : 0;
+            // tiles before: units before the item, less kPrefixUnits for each item before it
+            edge[e] = PrefixEdge{g, at - x + tile - kPrefixUnits * (done + block), block, tile};
         }
     }
     __syncthreads();

@@ -98,6 +98,21 @@ def test_members_that_save_nothing_do_not_make_a_group_share(others, dl):
     assert_attention(got[0][some], got[1][some], ref, others)
 
 
+@pytest.mark.parametrize("dl,heads,R,prefix,shares", [(512, 16, 4, 32768, False), (512, 8, 8, 16384, False), (512, 4, 4, 32768, False), (512, 16, 64, 8192, True),
+                                                      (256, 8, 256, 512, True), (256, 32, 256, 1024, True), (256, 16, 4, 4096, False), (256, 4, 64, 4096, True)])
+def test_sharing_follows_what_was_measured(dl, heads, R, prefix, shares):
+    """Entries of few rows and latents of 256, on the side of the decision where they were measured to be faster: the plain call bit for bit, or
+    summed in another order."""
+    page = 64
+    cache, table, _, rows = paged_latents([prefix + 37], page, dl, seed=42)
+    tables, sl = table.expand(R, -1).contiguous(), torch.full((R,), prefix + 37, **I32)
+    q = queries(R, 1, heads, dl + 64, seed=42)
+    got = run_shared(q, cache, tables, sl, torch.tensor([0, R], **I32), torch.tensor([prefix], **I32), dl)
+    assert same_bits(got, run_plain(q, cache, tables, sl, dl)) != shares
+    some = [0, R - 1]
+    assert_attention(got[0][some], got[1][some], decode_reference(q[some], lambda i, m: rows[0][:m], [prefix + 37] * 2, SCALE, dl))
+
+
 @pytest.mark.parametrize("bad", [math.inf, math.nan])
 def test_values_of_a_long_prefix_that_a_short_member_does_not_see(bad):
     """Sixty-three entries on 3.2 million tokens (the same 50 pages over and over) with a value that is not finite in every fiftieth page, and one of
