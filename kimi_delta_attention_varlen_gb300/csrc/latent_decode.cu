@@ -467,6 +467,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(Params p, co
                 }
             };
             if (active) put();
+            // What the copies wrote is read and written below.  They were complete for S; each one's own barrier, which turns again only
+            // behind this tile's second product, is looked at so that this is seen here too.
+            if (t0 + T > w.n - (p.a.L - 1)) {
+                const int k = i * C::PAIRS + lane % C::PAIRS;
+                mbar_test(&bar.full[k % C::RING], (k / C::RING) & 1);
+                __syncwarp();
+            }
             if (w.n - t0 < T) {  // rows behind the last token: whatever they hold must not meet P = 0
                 const int from = w.n - t0;
                 for (int e = tid - 128; e < (T - from) * 2 * C::PAIRS * 8; e += kSoftThreads) {

@@ -485,8 +485,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
                 seen = active && rr < p.rows ? w.n - (p.a.L - 1 - rr / p.a.h) : 0;
             }
             const int stage = i % C::RING;
-            wait(&bar.s[i & 1], (i >> 1) & 1);  // the tile's copies were complete for S
+            wait(&bar.s[i & 1], (i >> 1) & 1);
             tc::fence_after_sync();
+            // The copies were complete for S; their own barrier, which turns again only behind this tile's second product, is looked at
+            // so that this is seen here too (behind the scores' loads: 512 requests 294 us, drafts 286 us; without the look 291 and 285 us).
+            auto seen_here = [&]() {
+                if (lane == 0) mbar_test(&bar.full[stage], (i / C::RING) & 1);
+                __syncwarp();
+            };
             const int32_t t0 = w.tile * T, th = t0 + HT * half;
             float u[HT / 4];  // z + e of tokens th + 8 j + 2 t, + 1
             float mu = -INFINITY;
@@ -496,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
                 const float *units = reinterpret_cast<const float *>(smem + C::OFF_UNIT) + stage * T + HT * half + 2 * t;
                 uint32_t s[16];
                 ld_16x256b_x4(tl + C::COL_S + T * (i & 1) + HT * half, s);
+                seen_here();
                 tc::wait_ld();
                 tc::fence_before_sync();
                 mbar_arrive(&bar.s_free[i & 1]);
@@ -535,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, c
                 for (int j = 0; j < HT / 4; ++j) sum += ex2_approx(z[j] - base);
                 l += sum;
             } else {
+                seen_here();
                 mbar_arrive(&bar.s_free[i & 1]);
             }
             const bool first = big == -INFINITY;  // nothing summed yet

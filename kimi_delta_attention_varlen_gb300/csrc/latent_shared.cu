@@ -702,6 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             };
             put();
             if (w.n - t0 < T || low < min(w.n, t0 + T)) {
+                // The copies were complete for S; each one's own barrier, which turns again only behind this tile's second product, is
+                // looked at so that this is seen here too.
+                const int turn = i * C::PAIRS + lane % C::PAIRS;
+                mbar_test(&bar.full[turn % C::RING], (turn / C::RING) & 1);
+                __syncwarp();
                 // Rows behind the prefix: whatever they hold must not meet P = 0.  Tokens that some row does not see: nor must
                 // what is not finite.
                 const int from = max(min(low, w.n) - t0, 0);
