@@ -668,9 +668,12 @@ int kda_latent_append(const void *x, int64_t x_stride, int64_t total, const int3
  * system prompt): the attention to those tokens is computed for all query rows
  * of a group together and joined with each entry's own rest, so their pages
  * are read once for 64 rows and not once a request.  Where that saves less
- * than it costs (decided on the device from the lengths: few tokens, few
- * members; entries of L * h >= 64 rows, which the tensor cores bound in either
- * form) each entry takes all of its tokens, as kda_latent_decode does.
+ * than it costs (decided on the device from the entries' lengths: few tokens,
+ * few members, members that are much shorter than the others) each entry takes
+ * all of its tokens, as kda_latent_decode does; the decision and launches that
+ * find nothing to do then cost about 8 us beside that call.  Entries of L * h
+ * >= 64 rows, which fill the plain kernel by themselves, always go to
+ * kda_latent_decode's kernels directly.
  *   cu_groups [groups + 1] device int32, from 0, non-decreasing, ending at
  *             batch (precondition; entries outside all groups share nothing):
  *             entries cu_groups[g] .. cu_groups[g + 1] - 1 are group g
@@ -683,7 +686,8 @@ int kda_latent_append(const void *x, int64_t x_stride, int64_t total, const int3
  * are not finite, empty and invalid requests, sizes built and errors - is as for
  * kda_latent_decode; results differ from its by the order of summation.
  *   workspace kda_latent_decode_shared_workspace_size(...) bytes, 256-byte
- *             aligned (dl * 4 + 16 bytes for every query row among them).
+ *             aligned (dl * 4 + 16 bytes for every query row among them; for
+ *             L * h >= 64 as much as kda_latent_decode takes).
  *             Errors beside those: KDA_ERR_SHAPE (groups < 1), _RANGE (groups
  *             >= 2^24, requests >= 2^31).
  * ---------------------------------------------------------------------- */

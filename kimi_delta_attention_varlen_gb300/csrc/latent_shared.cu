@@ -781,6 +781,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     if (warp == 3) tc::tmem_dealloc(tmem, 512);
 }
 
+// Entries of 64 rows and more fill the plain kernel's groups of rows by themselves: the prefixes' kernel, which takes 64 rows as well, with
+// as little room in its ring, has nothing to save there (4 draft tokens x 128 heads of 18 entries on 9,001 tokens: 221 us, with it 309 us).
+bool takes_prefixes(int32_t L, int32_t h) { return static_cast<int64_t>(L) * h < N; }
+
 // The workspace: that of the rest's calls (its status word first), the prefixes' lists and parts, the plan, the prefixes' sums.
 struct Layout {
     size_t lists, ml, part, plan, pre_ml, pre, total;
@@ -847,13 +851,14 @@ template <int DL> cudaError_t launch(const LatentDecodeArgs &a, const SharedGrou
 
 }  // namespace
 
-size_t latent_shared_workspace(int64_t batch, int64_t groups, int32_t L, int32_t h, int32_t dl) { return layout(batch, groups, L, h, dl).total; }
+size_t latent_shared_workspace(int64_t batch, int64_t groups, int32_t L, int32_t h, int32_t dl)
+{
+    return takes_prefixes(L, h) ? layout(batch, groups, L, h, dl).total : latent_decode_workspace(batch, L, h, dl);
+}
 
 cudaError_t launch_latent_decode_shared(const LatentDecodeArgs &a, const SharedGroups &g, cudaStream_t st)
 {
-    // Entries of 64 rows and more are bound by the tensor cores in either form: there is nothing to save (4 draft tokens x 128
-    // heads of 18 entries on 9,001 tokens: 221 us, with the prefixes' kernel 309 us).
-    if (static_cast<int64_t>(a.L) * a.h >= N) return launch_latent_decode(a, st);
+    if (!takes_prefixes(a.L, a.h)) return launch_latent_decode(a, st);
     return a.dl == 512 ? launch<512>(a, g, st) : launch<256>(a, g, st);
 }
 
