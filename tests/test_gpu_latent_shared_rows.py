@@ -98,6 +98,20 @@ def test_members_that_save_nothing_do_not_make_a_group_share(others, dl):
     assert_attention(got[0][some], got[1][some], ref, others)
 
 
+@pytest.mark.parametrize("heads,shares", [(1, True), (32, True), (48, True), (64, False), (128, False)])
+def test_which_kernels_take_a_batch_that_sharing_pays_for(heads, shares):
+    """Compared with the plain call on the same batch, whose items are cut alike: bit for bit the same where entries have 64 rows and more, summed
+    in another order where they have fewer."""
+    R, n, page, dl = (600 if heads == 1 else 64), 32768, 64, 512
+    cache, table, _, rows = paged_latents([n], page, dl, seed=41)
+    tables, sl = table.expand(R, -1).contiguous(), torch.full((R,), n, **I32)
+    q = queries(R, 1, heads, dl + 64, seed=41)
+    got = run_shared(q, cache, tables, sl, torch.tensor([0, R], **I32), torch.tensor([n], **I32), dl)
+    assert same_bits(got, run_plain(q, cache, tables, sl, dl)) != shares
+    some = [0, R - 1]
+    assert_attention(got[0][some], got[1][some], decode_reference(q[some], lambda i, m: rows[0][:m], [n, n], SCALE, dl))
+
+
 @pytest.mark.parametrize("dl,heads,R,prefix,shares", [(512, 16, 4, 32768, False), (512, 8, 8, 16384, False), (512, 4, 4, 32768, False), (512, 16, 64, 8192, True),
                                                       (256, 8, 256, 512, True), (256, 32, 256, 1024, True), (256, 16, 4, 4096, False), (256, 4, 64, 4096, True)])
 def test_sharing_follows_what_was_measured(dl, heads, R, prefix, shares):
