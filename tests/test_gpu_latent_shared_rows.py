@@ -142,3 +142,19 @@ def test_values_of_a_long_prefix_that_a_short_member_does_not_see(bad):
     others = [r for r in range(R) if r != 17]
     assert not torch.isfinite(out[others][..., [9, 300]]).any()
     assert_attention(out[[17]], lse[[17]], decode_reference(q[[17]], lambda r, m: rows[0][:m], [40], SCALE, dl))
+
+
+@pytest.mark.parametrize("groups", [[9000], [8000, 1000], [1] * 300 + [8500]])
+def test_batches_of_many_thousand_entries(groups):
+    """More entries than the plan keeps lengths of, of many lengths, in batches that sharing pays for."""
+    page, dl, R = 64, 256, sum(groups)
+    cache, table, _, rows = paged_latents([1000], page, dl, seed=43)
+    tables = table.expand(R, -1).contiguous()
+    lens = [(r * 37) % 1001 if r % 11 else 0 for r in range(R)]
+    cu = torch.tensor([0] + groups, **I32).cumsum(0, dtype=torch.int32)
+    q, sl = queries(R, 1, 1, dl + 64, seed=43), torch.tensor(lens, **I32)
+    got = run_shared(q, cache, tables, sl, cu, torch.full((len(groups),), 700, **I32), dl)
+    assert not same_bits(got, run_plain(q, cache, tables, sl, dl))
+    some = list(range(40)) + list(range(8180, 8204)) + list(range(R - 40, R))
+    assert_attention(got[0][some], got[1][some], decode_reference(q[some], lambda i, m: rows[0][:m], [lens[i] for i in some], SCALE, dl))
+    assert (got[0][sl == 0] == 0).all() and (got[1][sl == 0] == -math.inf).all()
