@@ -79,11 +79,6 @@ struct Maps {
     CUtensorMap q, cache;
 };
 
-__host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn)  // bf16 operands, fp32 accumulator, B K-major
-{
-    return tc::idesc_bf16(M, N, false) | ((a_mn ? 1u : 0u) << 15);
-}
-
 template <class C> struct Bars {
     uint64_t full[C::RING], empty[C::RING], rope_full[C::ROPE], rope_empty[C::ROPE];
     uint64_t q_full, q_free, s[2], s_free[2], p, o, drain[2];
@@ -684,8 +679,7 @@ template <bool Shared> cudaError_t dispatch(Params p, cudaStream_t st)
     p.rows = p.a.L * p.a.h;
     p.scale_log2 = p.a.scale * kLog2e;
     const int n = rows_per_group(p.rows);
-    p.box_rows = T;  // the largest power of two that divides the page, at most a tile
-    while (p.a.page % p.box_rows != 0) p.box_rows >>= 1;
+    p.box_rows = box_rows(p.a.page);
     if (p.a.dl == 512)
         return n == 16 ? launch<512, 16, Shared>(p, st) : n == 32 ? launch<512, 32, Shared>(p, st) : launch<512, 64, Shared>(p, st);
     return n == 16 ? launch<256, 16, Shared>(p, st) : n == 32 ? launch<256, 32, Shared>(p, st) : launch<256, 64, Shared>(p, st);

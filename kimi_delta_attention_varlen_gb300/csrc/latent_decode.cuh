@@ -23,7 +23,7 @@ constexpr int kSoftThreads = 128;
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kStatusExpired = 6;
-constexpr int kJoinCtas = 6;  // a SM: as many as stay resident
+constexpr int kJoinCtas = 6;  // a SM, of which the registers let two or three be resident at once
 
 struct Params {
     LatentDecodeArgs a;
@@ -62,6 +62,11 @@ __device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 
 // What a sum relative to the maximum `from` is worth relative to `to`.
 __device__ __forceinline__ float rebase(float from, float to) { return from == to ? 1.f : ex2_approx(from - to); }
 __device__ __forceinline__ float log_sum(float m, float sum) { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2; }
+
+__host__ __device__ constexpr uint32_t idesc(int M, int n, bool a_mn)  // bf16 operands, fp32 accumulator, B K-major
+{
+    return tc::idesc_bf16(M, n, false) | ((a_mn ? 1u : 0u) << 15);
+}
 
 struct Edge {
     int64_t r, tiles_before;
@@ -119,6 +124,15 @@ __device__ __forceinline__ void ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16])
                    "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
                    "=r"(r[14]), "=r"(r[15])
                  : "r"(taddr));
+}
+
+__device__ __forceinline__ void ld1(uint32_t taddr, uint32_t &r)  // this thread's lane, one column
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n" : "=r"(r) : "r"(taddr));
+}
+__device__ __forceinline__ void st1(uint32_t taddr, uint32_t r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(r) : "memory");
 }
 
 template <int Threads = kSoftThreads>
@@ -407,6 +421,14 @@ inline bool encode(CUtensorMap *m, const void *base, int64_t n0, int64_t n1, int
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, elem,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of a box of a page: the largest power of two that divides it, at most a tile.
+inline int box_rows(int64_t page)
+{
+    int rows = T;
+    while (page % rows != 0) rows >>= 1;
+    return rows;
 }
 
 inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -95,15 +95,6 @@ __device__ __forceinline__ int exponent_for(uint32_t most, int p, uint32_t f)
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 __device__ __forceinline__ uint32_t bf16x2_finite_magnitude(uint32_t u) { return u & 0x7fff7fffu & ~bf16x2_not_finite(u); }
 
-__device__ __forceinline__ void ld1(uint32_t taddr, uint32_t &r)  // this thread's lane, one column
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n" : "=r"(r) : "r"(taddr));
-}
-__device__ __forceinline__ void st1(uint32_t taddr, uint32_t r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(r) : "memory");
-}
-
 template <int DL, int N>
 __global__ void __launch_bounds__(kThreads, 1) latent_decode8_kernel(Params p, const __grid_constant__ Maps maps)
 {
@@ -686,8 +677,7 @@ cudaError_t launch_latent_decode8(const LatentDecodeArgs &a, cudaStream_t st)
     p.a = a;
     p.rows = a.L * a.h;
     p.scale_log2 = a.scale * kLog2e;
-    p.box_rows = T;  // the largest power of two that divides the page, at most a tile
-    while (a.page % p.box_rows != 0) p.box_rows >>= 1;
+    p.box_rows = box_rows(a.page);
     if (rows_per_group(p.rows) == 16) return a.dl == 512 ? launch<512, 16>(p, st) : launch<256, 16>(p, st);
     return a.dl == 512 ? launch<512, 32>(p, st) : launch<256, 32>(p, st);
 }

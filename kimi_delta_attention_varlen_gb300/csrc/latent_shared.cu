@@ -204,20 +204,6 @@ struct PrefixEdge {
     int32_t block, tile;
 };
 
-__host__ __device__ constexpr uint32_t idesc(int M, int n, bool a_mn)  // bf16 operands, fp32 accumulator, B K-major
-{
-    return tc::idesc_bf16(M, n, false) | ((a_mn ? 1u : 0u) << 15);
-}
-
-__device__ __forceinline__ void ld2(uint32_t taddr, uint32_t &r)  // this thread's lane, one column
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n" : "=r"(r) : "r"(taddr));
-}
-__device__ __forceinline__ void st2(uint32_t taddr, uint32_t r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(r) : "memory");
-}
-
 template <int DL>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ SharedParams sp, const __grid_constant__ Maps maps)
 {
@@ -733,11 +719,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                         const int row = 32 * q + __ffs(rows) - 1;
                         uint32_t o[C::PAIRS / 2];
 #pragma unroll
-                        for (int c = 0; c < C::PAIRS / 2; ++c) ld2(tl + (half * (C::PAIRS / 2) + c) * N + row, o[c]);
+                        for (int c = 0; c < C::PAIRS / 2; ++c) ld1(tl + (half * (C::PAIRS / 2) + c) * N + row, o[c]);
                         tc::wait_ld();
 #pragma unroll
                         for (int c = 0; c < C::PAIRS / 2; ++c)
-                            st2(tl + (half * (C::PAIRS / 2) + c) * N + row, __float_as_uint(__uint_as_float(o[c]) * corr[row]));
+                            st1(tl + (half * (C::PAIRS / 2) + c) * N + row, __float_as_uint(__uint_as_float(o[c]) * corr[row]));
                     }
                 tc::wait_st();
             }
@@ -814,8 +800,7 @@ template <int DL> cudaError_t launch(const LatentDecodeArgs &a, const SharedGrou
     p.a = a;
     p.rows = a.L * a.h;
     p.scale_log2 = a.scale * kLog2e;
-    p.box_rows = T;  // the largest power of two that divides the page, at most a tile
-    while (a.page % p.box_rows != 0) p.box_rows >>= 1;
+    p.box_rows = box_rows(a.page);
     p.status = reinterpret_cast<int32_t *>(ws);
     p.item0 = reinterpret_cast<int32_t *>(ws + y.lists);
     p.item1 = p.item0 + grid;
