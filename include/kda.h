@@ -740,8 +740,10 @@ int kda_latent_decode_shared(const void *q, int32_t io_dtype, int64_t batch, int
  *   statistics and sums are fp32; the products are exact in their operands: a
  *   query enters as two e4m3 parts (its bf16 digits; what lies 2^-22 below the
  *   row's largest value is rounded), a weight as three (2^-12 of the weight; the
- *   last part ends 2^-21 below the largest weight of any 16,384 tokens).  Other
- *   arguments, results, non-finite values and errors as for kda_latent_decode.
+ *   last part ends 2^-21 below the largest weight of any 16,384 tokens, so that
+ *   behind one that outweighs all others the sum of those may be off by 2^-8 of
+ *   it, which the log-sum-exp is not).  Other arguments, results, non-finite
+ *   values and errors as for kda_latent_decode.
  * Errors: as for the bf16 calls; KDA_ERR_DTYPE when the cache is not KDA_U8 (for
  * kda_latent_read: KDA_U8 or bf16), KDA_ERR_SHAPE when its k is not that of dl
  * and dr, KDA_ERR_UNSUPPORTED outside dl in {256, 512}, dr == 64, page_size a

@@ -6,7 +6,9 @@
 // and the codes are operands of the tensor cores as they are: nothing is converted on its way from the page.
 //
 // The other operand of an e4m3 product is e4m3 too.  Three binary digits follow the leading one there, so
-//   a query value (bf16: eight digits)  = q1 + q2 / 16                exactly, the parts rows g and g + 8 of one product,
+//   a query value (bf16: eight digits)  = q1 + q2 / 16                the parts rows g and g + 8 of one product (exactly down to
+//                                                                     2^-15 of the row's largest value; below, e4m3's subnormals
+//                                                                     round q2 / 16 to steps of 2^-13, 2^-22 of that value at most),
 //   a weight w (to fp16: eleven digits) = (w1 + w2 / 16 + w3 / 256) / 16, the parts side by side in N,
 // each part the rounding of what the one before left off; the accumulators of the parts are added up in fp32, those of the
 // scores for every tile, those of the outputs once at the end of a segment.
@@ -24,12 +26,13 @@
 //
 // What bounds it: the chain of a tile through the softmax warps (scores, maximum, exponentials, parts, hand-over: about 2,200
 // cycles, where the bytes of a tile, 41 KB, take 1,800) and the end of a segment (6,800 cycles).  512 requests of 512..8,192 tokens,
-// 32 heads: 286..290 us = 4.9 TB/s (bf16 pages: 426 us); two of 131,072: 56 us (66); one of 1,009: 16 us (13).  33 requests x 4 draft
-// tokens x 128 heads: 280 us (bf16 pages: 222 us): 32 rows to a group where that form has 64, so the pages come twice as
+// 32 heads: 290..294 us = 4.9 TB/s (bf16 pages: 425 us); two of 131,072: 57 us (66); one of 1,009: 16 us (13).  33 requests x 4 draft
+// tokens x 128 heads: 281..286 us (bf16 pages: 225 us): 32 rows to a group where that form has 64, so the pages come twice as
 // often, from L2.  Instructions count here as code: the kernel's roles share an instruction cache, and the epilogue in two places
-// cost the 512 requests 23 us, unrolled once more 30 us.  Tried and not kept: four softmax warps (341 us at that time, eight
-// with half of the tokens each 317), two groups of four that take the tiles in turn (399), weights in two places so that the next
-// are written while these are read (316), the rope products of a tile ahead (313), queries read twice instead of held (318).
+// cost the 512 requests 23 us, unrolled once more 30 us.  dl = 512 at 32 rows spills 220 bytes a thread at its 128 registers.  Tried and not
+// kept, when the kernel took 317 us: four softmax warps (341), two groups of four that take the tiles in turn (399); when it took 290:
+// weights in two places so that the next are written while these are read (316), the products of a tile's scores a tile ahead (313),
+// both (332), queries read twice instead of held (318).
 //
 // Every wait is bounded; an expired one sets the workspace's status word (6) and ends the CTA.
 #include <cuda_fp16.h>

@@ -7,7 +7,8 @@
 //
 // What bounds it: bytes (644 + 1,152 a token), and before them the look-ups, five loads that wait for one another (offsets, request,
 // length, page, row).  A CTA's rows are looked up together, a row a lane; reading keeps four rows a warp in flight behind them.
-// 73,364 tokens: written in 29.6 us = 4.5 TB/s, read in 24.3 us = 5.5 TB/s (one look-up a warp: 37.5 and 27.6 us); 24 new tokens 3.1 us.
+// 73,364 tokens: written in 29.9 us = 4.4 TB/s (fp32 rows 36.2 us = 6.0 TB/s), read in 24.1 us = 5.5 TB/s (one
+// look-up a warp: 37.5 and 27.6 us); 24 new tokens 3.0 us.
 // Loads and stores are whole 16- or 8-byte vectors, consecutive across the warp.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

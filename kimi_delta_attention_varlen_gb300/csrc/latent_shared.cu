@@ -3,7 +3,7 @@
 // For a query row, softmax attention over [0, n) is the join of that over [0, b) and over [b, n): with each part's maximum m,
 // sum l of e^(z - m) and sum o of e^(z - m) x, everything is brought to the larger m and added.  b is the end of the group's last
 // whole shared page.  Four steps on the stream:
-//   plan      b of each group, a member that holds the pages (the longest), b of each entry
+//   plan      whether sharing pays; b of each group, a member that holds the pages (the longest), b of each entry
 //   prefixes  the rows of all members of a group together, 64 at a time, against [0, b): an item is (group, block of 64 rows);
 //             o, m, l to the workspace, in fp32, unnormalised
 //   join      of the parts of items that fell into several shares
@@ -18,11 +18,12 @@
 // half of a tile's tokens each, since the ring has room for two tiles and a tile keeps its place until its second product is done.
 //
 // What bounds it: shared memory.  A tile of 64 tokens x 64 rows moves 319 KB through it (operands of S 147, of O^T 98, the copy 74:
-// 2,500 cycles at 128 bytes each), and takes 3,430 cycles: the copies wait for the products' reads, and the ring has room for one
-// tile beside the one that is worked on.  64 requests of 32 heads on 32,768 tokens: 188 us of 229 us (apart: 344 us); 500 requests
-// on seven system prompts of 3,000..6,001 tokens 212 us of 389 us (447 us); the rest's kernel then adds the prefix's sums, 64 KB a
+// 2,500 cycles at 128 bytes each), and takes about 3,300 cycles: the copies wait for the products' reads, and the ring has room for one
+// tile beside the one that is worked on.  64 requests of 32 heads on 32,768 tokens: 181 us of 221..228 us (apart: 344 us); 500 requests
+// on seven system prompts of 3,000..6,001 tokens 204 us of 377..380 us (447 us); the rest's kernel then adds the prefix's sums, 64 KB a
 // request, which it loads a step ahead.  Tried and not kept: panels copied once for two CTAs of a cluster (multicast, an item of
-// 128 rows: 237 and 450 us where it was 233 and 446 then).
+// 128 rows: 237 and 450 us where it was 233 and 446 then).  Where the plan finds nothing to share, it and two kernels that leave at once
+// cost 7..8 us beside kda_latent_decode (8 samples of 4,133 tokens: 28 us and 21 us).
 //
 // Every wait is bounded; an expired one sets the workspace's status word (6) and ends the CTA.
 #include "latent_decode.cuh"
@@ -81,7 +82,7 @@ __device__ __forceinline__ void entries_of(const SharedParams &s, int64_t g, int
     if (*to < *from) *to = *from;
 }
 
-// What a tile of 64 tokens takes a CTA, in cycles: with up to 32 rows of an entry, and with 64 rows (of an entry or of a
+// What a tile of 64 tokens takes a CTA, in cycles (the figures that decide best, below): with up to 32 rows of an entry, and with 64 rows (of an entry or of a
 // prefix); alike for latents of 256 and of 512, whose tiles wait for the same softmax.  What comes with a block of 64 rows of a prefix
 // whatever its length, what joining the prefix's part takes an entry of 32 rows of 512 (in proportion to both), and what launches and
 // joins take the GPU, a CTA.
@@ -95,7 +96,7 @@ constexpr int kLengths = 8192;  // entries whose lengths the plan loads at once;
 
 // By one CTA, a group a warp.  Sharing pays where it saves more tiles' time than the joins and launches take; an entry saves the tiles
 // that it would take apart, so one that is shorter than the prefix saves few and an empty one none.  Where it does not pay,
-// nothing is shared and each entry takes all of its tokens (measured both ways: 64 entries of 32 heads on 32,768 tokens 227 us
+// nothing is shared and each entry takes all of its tokens (measured both ways: 64 entries of 32 heads on 32,768 tokens 221 us
 // against 344 us apart; 8 on 4,133 tokens 43 us against 29 us with nothing shared).  752 batches of 1 to 56 rows an entry, latents of 256
 // and 512, one to seven prefixes of 200 to 39,000 tokens under 2 to 256 entries, each timed both ways: but for five of them the rule
 // takes the faster side or loses less than 5 % (11 % at the most, 0.1 % on average).
